@@ -17,6 +17,11 @@
  * spec_tree_init / spec_tree_expand (/ spec_tree_expand_multi) build the draft tree on
  * the device;
  * spec_accept_noalloc is spec_accept without a workspace argument.
+ * Around them: spec_page_table_resize grows the sequences' page-table rows for a step and
+ * maps its tokens to slots; spec_qk_norm_rope norms and rotates the projected queries and
+ * keys of the tree into the layouts the attention reads; spec_tree_verify_attn_kv8p and
+ * spec_kv_commit_kv8p are the attention and the commit over an FP8 (E4M3) cache with a
+ * scale per (page, KV head).
  *
  * Sources of the operations (page title, then section):
  *   "EAGLE-2 deep dive" (techknowgenie): architecture section (all tree tokens
@@ -110,11 +115,13 @@ typedef enum {
 typedef enum { SPEC_F32 = 0, SPEC_BF16 = 1 } spec_dtype;
 typedef enum { SPEC_GREEDY = 0, SPEC_STOCHASTIC = 1 } spec_mode;
 typedef enum { SPEC_OP_MASK = 0, SPEC_OP_ATTN = 1, SPEC_OP_ACCEPT = 2, SPEC_OP_COMMIT = 3,
-               SPEC_OP_TREE = 4 } spec_op;
+               SPEC_OP_TREE = 4, SPEC_OP_ATTN_KV8P = 5 } spec_op;
 
 /* Bytes of workspace `op` needs for these sizes (0 when it needs none).
  * For SPEC_OP_ATTN the result depends on (batch, max_nodes, hq, hkv, d,
  * max_prefix, total_nodes); for SPEC_OP_ACCEPT on (batch, total_nodes, vocab); for
+ * SPEC_OP_ATTN_KV8P (the attention over a cache with page scales) on what SPEC_OP_ATTN
+ * does, with d = 128; for
  * SPEC_OP_TREE (the draft-tree state of spec_tree_init / spec_tree_expand) on
  * (batch, max_nodes).
  * Unused arguments may be 0. Returns 0 for invalid sizes. */
@@ -523,6 +530,135 @@ int spec_kv_commit_kv8(const void* k_tree, const void* v_tree, const float* kv_s
                        int num_pages, int page_size, const int32_t* prefix_len, int32_t* seq_len_out,
                        uint8_t* k_pool, uint8_t* v_pool, int batch, int total_nodes, int hkv, int d,
                        int32_t* dev_status, void* stream);
+
+/*
+ * spec_tree_verify_attn_kv8p — spec_tree_verify_attn over an E4M3 paged cache whose scales
+ *   belong to pages: one for K and one for V of every (page, KV head).
+ *
+ *   q, k_tree, v_tree, out  bf16, as spec_tree_verify_attn_kv8
+ *   k_pool, v_pool  uint8 [num_pages][hkv][16][128]  OCP E4M3 codes
+ *   kv_scale    float [num_pages][hkv][2]  (K scale, V scale) of a page and head; a code
+ *               stands for value * scale. Any positive scale; each is read as
+ *               min(max(scale, 2^-50), 2^50) (0 and NaN read as 2^-50).
+ *   hq / hkv    any group size up to 128 (it need not divide 128).
+ *   Everything else as spec_tree_verify_attn (d = 128, page_size 16, else
+ *   SPEC_ERR_UNSUPPORTED; kv_scale 8-byte aligned, the other tensors 16, else
+ *   SPEC_ERR_ARG). What a row may not see does not reach it: cache rows past prefix_len,
+ *   tree nodes its mask bits leave out and nodes of other sequences may hold infinities,
+ *   NaN or NaN codes. A row that does see a NaN or an infinity in k or v may be NaN in
+ *   every element. A row that sees no key at all is 0 with lse = -infinity.
+ *   Rows at or past qo_indptr[batch] are left as they were.
+ *   ws          workspace of spec_workspace_size(SPEC_OP_ATTN_KV8P, ...) bytes (256-byte
+ *               aligned; any contents).
+ *   Device errors: SPEC_ERR_PAGE (the page is read as zeros), SPEC_ERR_CAPACITY (a tree
+ *   past max_nodes, a prefix past its row: that sequence's rows are left as they were),
+ *   SPEC_ERR_TIMEOUT.
+ */
+int spec_tree_verify_attn_kv8p(const void* q, const uint8_t* k_pool, const uint8_t* v_pool,
+                               const float* kv_scale, int num_pages, int page_size,
+                               const int32_t* page_table, int max_pages, const int32_t* prefix_len,
+                               int max_prefix, const void* k_tree, const void* v_tree,
+                               const uint64_t* mask, const int32_t* qo_indptr, int batch,
+                               int total_nodes, int max_nodes, int hq, int hkv, int d, float sm_scale,
+                               void* out, float* lse, void* ws, size_t ws_bytes, int32_t* dev_status,
+                               void* stream);
+
+/*
+ * spec_kv_commit_kv8p — spec_kv_commit from bf16 tree rows into a cache with page scales;
+ *   it keeps the scales.
+ *   For every page it writes to, every KV head, K and V apart: let t be the largest finite
+ *   |x| of the rows written to the page and s0 the smallest power of two in [2^-50, 2^50]
+ *   with t <= 448 s0. A page without older rows (slots below prefix_len[b]) gets the scale
+ *   s = s0, whatever it held; a page with older rows s = max(s0, its scale). Written rows
+ *   become the E4M3 codes nearest to x / s (ties to the even code, beyond +-448, and
+ *   infinities, saturated to +-448, NaN kept); where s has grown, the older rows' codes
+ *   become those nearest to value * old scale / s. Rows past the written ones keep their
+ *   codes (they hold nothing). So a scale never shrinks while its page holds a token.
+ *   A page that receives rows must belong to one sequence of the call.
+ *
+ *   kv_scale    float [num_pages][hkv][2] (in/out)
+ *   The other arguments, the checks and the device errors are those of spec_kv_commit with
+ *   dtype = SPEC_BF16. d a multiple of 16 and page_size * d <= 8192, else
+ *   SPEC_ERR_UNSUPPORTED.
+ */
+int spec_kv_commit_kv8p(const void* k_tree, const void* v_tree, const int32_t* path, int path_cap,
+                        const int32_t* accept_len, const int32_t* qo_indptr,
+                        const int32_t* page_table, int max_pages, int num_pages, int page_size,
+                        const int32_t* prefix_len, int32_t* seq_len_out, uint8_t* k_pool,
+                        uint8_t* v_pool, float* kv_scale, int batch, int total_nodes, int hkv, int d,
+                        int32_t* dev_status, void* stream);
+
+/*
+ * spec_qk_norm_rope — queries and keys of the tree's nodes from the projection's output:
+ *   normed per head, rotated to their positions, written in the layouts the attention
+ *   reads (and the values copied into theirs).
+ *   For node t of sequence b the position is prefix_len[b] + depth[t], the place the node
+ *   takes if its path is accepted. Every query and key head x (d elements):
+ *     y = x / sqrt(mean(x^2) + eps) * weight   (weight NULL: y = x), then the rot_dim / 2
+ *     pairs (u, v) of its first rot_dim elements become (u c - v s, v c + u s) with the
+ *     cosine c and sine s of the position's table row; later elements pass through.
+ *   Pair i is (y[i], y[i + rot_dim / 2]), or (y[2i], y[2i + 1]) where interleaved != 0.
+ *   fp32 arithmetic, rounded once.
+ *
+ *   dtype      SPEC_F32 or SPEC_BF16, of every tensor but the table.
+ *   q_in       [total_nodes] rows of hq * d elements, q_stride elements apart (the heads of
+ *              a fused projection can be read in place); k_in, v_in likewise with hkv * d.
+ *              v_in / v_out: both or neither. Strides: multiples of 16 bytes.
+ *   q_weight, k_weight  [d], either NULL.
+ *   cos_sin    float [max_pos][rot_dim]: rot_dim / 2 cosines, then rot_dim / 2 sines of
+ *              each position (NULL where rot_dim = 0).
+ *   depth      int32 [total_nodes] from spec_build_tree_mask; NULL: node i of a sequence
+ *              stands i tokens past its prefix (a chain, a prompt chunk).
+ *   q_out      [total_nodes][hq][d];  k_out, v_out  [total_nodes][hkv][d]. An output may be
+ *              its own input where the strides agree; no other overlap.
+ *   d and rot_dim multiples of 16, d <= 512, rot_dim <= d, at most 4096 heads, else
+ *   SPEC_ERR_UNSUPPORTED; every tensor 16-byte aligned, eps >= 0, else SPEC_ERR_ARG.
+ *   Device errors: SPEC_ERR_INDEX (a negative depth or prefix, a position outside
+ *   [0, max_pos): that node's outputs are left as they were). Rows at or past
+ *   qo_indptr[batch] are left as they were.
+ */
+int spec_qk_norm_rope(int dtype, const void* q_in, long long q_stride, const void* k_in,
+                      long long k_stride, const void* v_in, long long v_stride, const void* q_weight,
+                      const void* k_weight, float eps, const float* cos_sin, int max_pos, int rot_dim,
+                      int interleaved, const int32_t* prefix_len, const int32_t* depth,
+                      const int32_t* qo_indptr, int batch, int total_nodes, int hq, int hkv, int d,
+                      void* q_out, void* k_out, void* v_out, int32_t* dev_status, void* stream);
+
+/*
+ * spec_page_table_resize — the page-table rows a step needs, from the lengths on the
+ *   device, and the slots of its tokens. (The commit leaves seq_len on the device; with
+ *   this call the next step's pages are given out there too, with no host round trip.)
+ *   Sequence b needs ceil((seq_len[b] + n_b) / page_size) pages, n_b = qo_indptr[b+1] -
+ *   qo_indptr[b]. What its row lacks is taken off the stack of free pages; with
+ *   shrink != 0 the row's entries past its need go back onto it (a finished sequence: 0
+ *   tokens). Returned pages are pushed first, by rising sequence and entry; then the
+ *   sequences, in order, each pop their pages while all of a sequence's fit in what is
+ *   left (the first that does not fit, and every later one that asks, get none and keep
+ *   their row: SPEC_ERR_CAPACITY).
+ *
+ *   seq_len    int32 [batch]   tokens in the cache
+ *   qo_indptr  int32 [batch+1] the step's nodes (counts may be 0)
+ *   held, held_out  int32 [batch]  pages of each row before and after; may be one buffer
+ *   page_table int32 [batch][max_pages] (in/out)  entries held .. need-1 of a growing row are
+ *              written, nothing else; entries past held_out[b] mean nothing
+ *   free_pages int32 [num_pages] (in/out)  the stack: places 0 .. n_free-1 hold free pages
+ *   n_free, n_free_out  int32 [1]  its height before and after; may be one buffer
+ *   slot_map   int64 [total_nodes] (out, nullable)  node i of sequence b as the token at
+ *              seq_len[b] + i: page * page_size + row, or -1 where the row does not reach
+ *              (and for every node of a sequence with SPEC_ERR_INDEX).
+ *              Rows at or past qo_indptr[batch] are left as they were.
+ *   batch <= 4096 and batch * max_pages < 2^31, else SPEC_ERR_UNSUPPORTED.
+ *   Device errors: SPEC_ERR_INDEX (a negative length or count, held outside
+ *   [0, max_pages]), SPEC_ERR_CAPACITY (a need past max_pages: in both cases that row
+ *   stays; too few free pages; a stack that would be outside [0, num_pages], then nothing
+ *   moves), SPEC_ERR_PAGE (a page id outside [0, num_pages)). No page may stand twice in
+ *   the rows and the stack.
+ */
+int spec_page_table_resize(const int32_t* seq_len, const int32_t* qo_indptr, const int32_t* held,
+                           int32_t* page_table, int max_pages, int32_t* free_pages, int num_pages,
+                           const int32_t* n_free, int page_size, int shrink, int batch,
+                           int total_nodes, int32_t* held_out, int32_t* n_free_out,
+                           long long* slot_map, int32_t* dev_status, void* stream);
 
 #ifdef __cplusplus
 }

@@ -48,6 +48,7 @@ from .accept import greedy_accept, stochastic_accept, AcceptResult
 from .commit import kv_commit, token_insert
 from .draft_tree import best_first_tree, topk_softmax
 from .fp8 import e4m3_decode, e4m3_encode, kv_quantize, kv_dequantize
+from .serving import kv8p_values, kv8p_commit, qk_norm_rope, page_table_resize
 
 __all__ = [
     "ancestor_mask",
@@ -67,4 +68,8 @@ __all__ = [
     "e4m3_encode",
     "kv_quantize",
     "kv_dequantize",
+    "kv8p_values",
+    "kv8p_commit",
+    "qk_norm_rope",
+    "page_table_resize",
 ]

@@ -19,6 +19,7 @@ SPEC_OK = 0
 SPEC_F32, SPEC_BF16 = 0, 1
 SPEC_GREEDY, SPEC_STOCHASTIC = 0, 1
 SPEC_OP_MASK, SPEC_OP_ATTN, SPEC_OP_ACCEPT, SPEC_OP_COMMIT, SPEC_OP_TREE = 0, 1, 2, 3, 4
+SPEC_OP_ATTN_KV8P = 5
 STATUS = {
     0: "SPEC_OK", -1: "SPEC_ERR_ARG", -2: "SPEC_ERR_PARENT", -3: "SPEC_ERR_PAGE", -4: "SPEC_ERR_CAPACITY",
     -5: "SPEC_ERR_WORKSPACE", -6: "SPEC_ERR_UNSUPPORTED", -7: "SPEC_ERR_CUDA", -8: "SPEC_ERR_TIMEOUT",
@@ -27,9 +28,11 @@ STATUS = {
 EXPORTS = ("spec_version", "spec_status_string", "spec_workspace_size", "spec_attn_plan", "spec_build_tree_mask",
            "spec_tree_verify_attn", "spec_accept", "spec_kv_commit", "spec_accept_commit", "spec_accept_noalloc",
            "spec_tree_init", "spec_tree_expand", "spec_tree_verify_attn_kv8", "spec_kv_commit_kv8",
-           "spec_tree_verify_attn_parents", "spec_tree_expand_multi", "spec_accept_plan", "spec_set_early_reads")
+           "spec_tree_verify_attn_parents", "spec_tree_expand_multi", "spec_accept_plan", "spec_set_early_reads",
+           "spec_tree_verify_attn_kv8p", "spec_kv_commit_kv8p", "spec_qk_norm_rope", "spec_page_table_resize")
 
 _P, _I, _F, _Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+_L = ctypes.c_longlong
 _SIGS = {
     "spec_version": (_I, []),
     "spec_status_string": (ctypes.c_char_p, [_I]),
@@ -55,6 +58,12 @@ _SIGS = {
     "spec_tree_verify_attn_parents": (_I, [_P, _P, _P, _I, _I, _P, _I, _P, _I, _P, _P, _P, _P, _I, _I, _I, _I, _I,
                                            _I, _F, _P, _P, _P, _Z, _P, _P]),
     "spec_kv_commit_kv8": (_I, [_P, _P, _P, _P, _I, _P, _P, _P, _I, _I, _I, _P, _P, _P, _P, _I, _I, _I, _I, _P, _P]),
+    "spec_tree_verify_attn_kv8p": (_I, [_P, _P, _P, _P, _I, _I, _P, _I, _P, _I, _P, _P, _P, _P, _I, _I, _I, _I, _I,
+                                        _I, _F, _P, _P, _P, _Z, _P, _P]),
+    "spec_kv_commit_kv8p": (_I, [_P, _P, _P, _I, _P, _P, _P, _I, _I, _I, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _P]),
+    "spec_qk_norm_rope": (_I, [_I, _P, _L, _P, _L, _P, _L, _P, _P, _F, _P, _I, _I, _I, _P, _P, _P, _I, _I, _I, _I, _I,
+                               _P, _P, _P, _P, _P]),
+    "spec_page_table_resize": (_I, [_P, _P, _P, _P, _I, _P, _I, _P, _I, _I, _I, _I, _P, _P, _P, _P, _P]),
 }
 
 _lib = None
@@ -359,3 +368,100 @@ def spec_tree_verify_attn_parents(q, k_pool, v_pool, page_table, prefix_len, max
         qo_indptr.numel() - 1, T, int(max_nodes), hq, hkv, d, float(sm_scale), _ptr(out), _ptr(lse),
         _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), _ptr(dev_status), _stream(stream))
     return _check(st, "spec_tree_verify_attn_parents")
+
+
+def spec_tree_verify_attn_kv8p(q, k_pool, v_pool, kv_scale, page_table, prefix_len, max_prefix, k_tree, v_tree,
+                               mask, qo_indptr, max_nodes, out, lse=None, ws=None, sm_scale=0.0, dev_status=None,
+                               stream=None):
+    """Tree-verify attention over an FP8 cache with page scales: k_pool/v_pool uint8 E4M3
+    codes [pages,Hkv,16,128], kv_scale float32 [pages,Hkv,2] (K scale, V scale); q, k_tree,
+    v_tree and out bf16. ws: spec_workspace_size(SPEC_OP_ATTN_KV8P, ...) bytes."""
+    for t, what in ((q, "q"), (k_tree, "k_tree"), (v_tree, "v_tree"), (out, "out")):
+        _need(t, torch.bfloat16, what)
+    _need_kv8p(k_pool, v_pool, kv_scale)
+    T, hq, d = q.shape
+    num_pages, hkv, ps, _ = k_pool.shape
+    st = load().spec_tree_verify_attn_kv8p(
+        _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(kv_scale), num_pages, ps, _ptr(page_table), page_table.shape[1],
+        _ptr(prefix_len), int(max_prefix), _ptr(k_tree), _ptr(v_tree), _ptr(mask), _ptr(qo_indptr),
+        qo_indptr.numel() - 1, T, int(max_nodes), hq, hkv, d, float(sm_scale), _ptr(out), _ptr(lse),
+        _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), _ptr(dev_status), _stream(stream))
+    return _check(st, "spec_tree_verify_attn_kv8p")
+
+
+def _need_kv8p(k_pool, v_pool, kv_scale):
+    _need(k_pool, torch.uint8, "k_pool (E4M3 codes)")
+    _need(v_pool, torch.uint8, "v_pool (E4M3 codes)")
+    _need(kv_scale, torch.float32, "kv_scale")
+    if v_pool.shape != k_pool.shape or tuple(kv_scale.shape) != (k_pool.shape[0], k_pool.shape[1], 2):
+        raise ValueError("kv_scale: [num_pages][hkv][2], and pools of one shape, expected")
+
+
+def spec_kv_commit_kv8p(k_tree, v_tree, path, accept_len, qo_indptr, page_table, prefix_len, k_pool, v_pool,
+                        kv_scale, seq_len_out=None, dev_status=None, stream=None):
+    """Commit of bf16 tree K/V rows into an FP8 cache with page scales (codes and scales
+    are updated in place)."""
+    _need(k_tree, torch.bfloat16, "k_tree")
+    _need(v_tree, torch.bfloat16, "v_tree")
+    _need_kv8p(k_pool, v_pool, kv_scale)
+    T, hkv, d = k_tree.shape
+    num_pages, _, ps, _ = k_pool.shape
+    st = load().spec_kv_commit_kv8p(
+        _ptr(k_tree), _ptr(v_tree), _ptr(path), path.shape[1], _ptr(accept_len), _ptr(qo_indptr), _ptr(page_table),
+        page_table.shape[1], num_pages, ps, _ptr(prefix_len), _ptr(seq_len_out), _ptr(k_pool), _ptr(v_pool),
+        _ptr(kv_scale), qo_indptr.numel() - 1, T, hkv, d, _ptr(dev_status), _stream(stream))
+    return _check(st, "spec_kv_commit_kv8p")
+
+
+def _rows(t, what):
+    """(pointer, elements between rows) of [T][heads][d] rows whose heads are contiguous."""
+    if not t.is_cuda:
+        raise ValueError("device tensor expected")
+    T, h, d = t.shape
+    if (d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d):
+        raise ValueError(f"{what}: contiguous heads expected")
+    return t.data_ptr(), t.stride(0) if T > 1 else h * d
+
+
+def spec_qk_norm_rope(q, k, v, cos_sin, prefix_len, qo_indptr, q_out, k_out, v_out, depth=None, q_weight=None,
+                      k_weight=None, eps=1e-6, interleaved=False, dev_status=None, stream=None):
+    """Norm per head and rotation of projected rows: q [T,Hq,D], k and v [T,Hkv,D] (views of
+    a fused projection: any row stride), cos_sin float32 [max_pos, rot_dim] or None (no
+    rotation); q_out, k_out, v_out contiguous. v and v_out may both be None."""
+    dt = _dtype(q)
+    for t, what in ((k, "k"), (q_out, "q_out"), (k_out, "k_out"), (v, "v"), (v_out, "v_out"),
+                    (q_weight, "q_weight"), (k_weight, "k_weight")):
+        if t is not None:
+            _need(t, q.dtype, what)
+    T, hq, d = q.shape
+    hkv = k.shape[1]
+    if cos_sin is not None:
+        _need(cos_sin, torch.float32, "cos_sin")
+    qp, qs = _rows(q, "q")
+    kp, ks = _rows(k, "k")
+    vp, vs = (None, 0) if v is None else _rows(v, "v")
+    max_pos, rot = (0, 0) if cos_sin is None else cos_sin.shape
+    st = load().spec_qk_norm_rope(
+        dt, qp, qs, kp, ks, vp, vs, _ptr(q_weight), _ptr(k_weight), float(eps), _ptr(cos_sin), max_pos, rot,
+        1 if interleaved else 0, _ptr(prefix_len), _ptr(depth), _ptr(qo_indptr), qo_indptr.numel() - 1, T, hq, hkv, d,
+        _ptr(q_out), _ptr(k_out), _ptr(v_out), _ptr(dev_status), _stream(stream))
+    return _check(st, "spec_qk_norm_rope")
+
+
+def spec_page_table_resize(seq_len, qo_indptr, held, page_table, free_pages, n_free, held_out, n_free_out,
+                           slot_map=None, page_size=16, shrink=False, dev_status=None, stream=None):
+    """Grow (with shrink also cut) the page-table rows to the lengths of a step, from a
+    stack of free pages; slot_map int64 [total_nodes]. held_out / n_free_out may be held /
+    n_free themselves."""
+    for t, what in ((seq_len, "seq_len"), (held, "held"), (page_table, "page_table"), (free_pages, "free_pages"),
+                    (n_free, "n_free"), (held_out, "held_out"), (n_free_out, "n_free_out"),
+                    (qo_indptr, "qo_indptr")):
+        _need(t, torch.int32, what)
+    if slot_map is not None:
+        _need(slot_map, torch.int64, "slot_map")
+    st = load().spec_page_table_resize(
+        _ptr(seq_len), _ptr(qo_indptr), _ptr(held), _ptr(page_table), page_table.shape[1], _ptr(free_pages),
+        free_pages.numel(), _ptr(n_free), int(page_size), 1 if shrink else 0, qo_indptr.numel() - 1,
+        0 if slot_map is None else slot_map.numel(), _ptr(held_out), _ptr(n_free_out), _ptr(slot_map),
+        _ptr(dev_status), _stream(stream))
+    return _check(st, "spec_page_table_resize")

@@ -35,6 +35,29 @@ int launch_attn_tc(const void* q, const void* k_pool, const void* v_pool, int nu
                    int total_nodes, int max_nodes, int hq, int hkv, int d, float sm_scale, void* out, float* lse,
                    void* ws, int32_t* status, cudaStream_t stream, const float* kv_scale, const int32_t* parent);
 
+size_t attn_kv8p_ws_bytes(int batch, int max_nodes, int hq, int hkv, int max_prefix);
+int launch_attn_kv8p(const void* q, const uint8_t* k_pool, const uint8_t* v_pool, const float* kv_scale, int num_pages,
+                     const int32_t* page_table, int max_pages, const int32_t* prefix_len, int max_prefix,
+                     const void* k_tree, const void* v_tree, const uint64_t* mask, const int32_t* qo, int batch,
+                     int total_nodes, int max_nodes, int hq, int hkv, float sm_scale, void* out, float* lse, void* ws,
+                     int32_t* status, cudaStream_t stream);
+bool commit_kv8p_shape(int page_size, int d);
+int launch_kv_commit_kv8p(const void* k_tree, const void* v_tree, const int32_t* path, int path_cap,
+                          const int32_t* accept_len, const int32_t* qo, const int32_t* page_table, int max_pages,
+                          int num_pages, int page_size, const int32_t* prefix_len, int32_t* seq_len_out,
+                          uint8_t* k_pool, uint8_t* v_pool, float* kv_scale, int batch, int hkv, int d,
+                          int32_t* status, cudaStream_t stream);
+int launch_qk_norm_rope(int dtype, const void* q_in, long q_stride, const void* k_in, long k_stride, const void* v_in,
+                        long v_stride, const void* q_weight, const void* k_weight, float eps, const float* cos_sin,
+                        int max_pos, int rot, bool interleaved, const int32_t* prefix_len, const int32_t* depth,
+                        const int32_t* qo, int batch, int total_nodes, int hq, int hkv, int d, void* q_out,
+                        void* k_out, void* v_out, int32_t* status, cudaStream_t stream);
+int page_table_max_batch();
+int launch_page_table(const int32_t* seq_len, const int32_t* qo, const int32_t* held, int32_t* page_table,
+                      int max_pages, int32_t* free_pages, int num_pages, const int32_t* n_free, int page_size,
+                      int shrink, int batch, int total_nodes, int32_t* held_out, int32_t* n_free_out,
+                      long long* slot_map, int32_t* status, cudaStream_t stream);
+
 constexpr int kMaxNodes = kMaxTreeNodes;
 
 static size_t attn_ws_bytes(int batch, int total_nodes, int max_nodes, int hq, int hkv, int d, int max_prefix) {
@@ -62,7 +85,7 @@ using namespace specv;
 
 extern "C" {
 
-int spec_version(void) { return 112; }
+int spec_version(void) { return 113; }
 
 int spec_set_early_reads(int enable) { return g_early_reads.exchange(enable ? 1 : 0); }
 
@@ -89,6 +112,10 @@ size_t spec_workspace_size(int op, int batch, int total_nodes, int max_nodes, in
     case SPEC_OP_ATTN:
       if (hq <= 0 || hkv <= 0 || hq % hkv || d <= 0 || max_nodes <= 0 || max_prefix < 0) return 0;
       return attn_ws_bytes(batch, total_nodes, max_nodes, hq, hkv, d, max_prefix);
+    case SPEC_OP_ATTN_KV8P:
+      if (hq <= 0 || hkv <= 0 || hq % hkv || d != 128 || max_nodes <= 0 || max_nodes > kMaxNodes || max_prefix < 0)
+        return 0;
+      return attn_kv8p_ws_bytes(batch, max_nodes, hq, hkv, max_prefix);
     case SPEC_OP_ACCEPT:
       if (vocab <= 0) return 0;
       return accept_ws_bytes(batch, total_nodes, vocab);
@@ -429,6 +456,91 @@ int spec_kv_commit_kv8(const void* k_tree, const void* v_tree, const float* kv_s
                           static_cast<cudaStream_t>(stream), TokenInsert{nullptr, nullptr, 0}, kv_scale);
 }
 
+
+int spec_tree_verify_attn_kv8p(const void* q, const uint8_t* k_pool, const uint8_t* v_pool, const float* kv_scale,
+                               int num_pages, int page_size, const int32_t* page_table, int max_pages,
+                               const int32_t* prefix_len, int max_prefix, const void* k_tree, const void* v_tree,
+                               const uint64_t* mask, const int32_t* qo_indptr, int batch, int total_nodes,
+                               int max_nodes, int hq, int hkv, int d, float sm_scale, void* out, float* lse, void* ws,
+                               size_t ws_bytes, int32_t* dev_status, void* stream) {
+  if (batch < 0 || total_nodes < 0 || max_nodes < 1 || max_nodes > kMaxNodes || max_prefix < 0 ||
+      num_pages < 0 || max_pages < 0)
+    return SPEC_ERR_ARG;
+  if (hq <= 0 || hkv <= 0 || hq % hkv != 0) return SPEC_ERR_ARG;
+  if (d != 128 || page_size != 16 || hq / hkv > 128) return SPEC_ERR_UNSUPPORTED;
+  if (!grid_fits((long)batch * hkv)) return SPEC_ERR_UNSUPPORTED;
+  if (batch == 0 || total_nodes == 0) return SPEC_OK;
+  if (!q || !k_tree || !v_tree || !mask || !qo_indptr || !prefix_len || !out) return SPEC_ERR_ARG;
+  if (max_prefix > 0 && (!k_pool || !v_pool || !kv_scale || !page_table || max_pages <= 0 || num_pages <= 0))
+    return SPEC_ERR_ARG;
+  if ((long)max_pages * page_size < max_prefix) return SPEC_ERR_ARG;
+  if (!aligned16(q) || !aligned16(k_tree) || !aligned16(v_tree) || !aligned16(out) ||
+      (max_prefix > 0 && (!aligned16(k_pool) || !aligned16(v_pool) || (reinterpret_cast<uintptr_t>(kv_scale) & 7))))
+    return SPEC_ERR_ARG;
+  const size_t need =
+      spec_workspace_size(SPEC_OP_ATTN_KV8P, batch, total_nodes, max_nodes, hq, hkv, d, max_prefix, 0);
+  if (need > 0 && (ws == nullptr || ws_bytes < need || (reinterpret_cast<uintptr_t>(ws) & 255)))
+    return SPEC_ERR_WORKSPACE;
+  if (!(sm_scale > 0.f)) sm_scale = 1.0f / sqrtf((float)d);
+  return launch_attn_kv8p(q, k_pool, v_pool, kv_scale, num_pages, page_table, max_pages, prefix_len, max_prefix,
+                          k_tree, v_tree, mask, qo_indptr, batch, total_nodes, max_nodes, hq, hkv, sm_scale, out, lse,
+                          ws, dev_status, static_cast<cudaStream_t>(stream));
+}
+
+int spec_kv_commit_kv8p(const void* k_tree, const void* v_tree, const int32_t* path, int path_cap,
+                        const int32_t* accept_len, const int32_t* qo_indptr, const int32_t* page_table, int max_pages,
+                        int num_pages, int page_size, const int32_t* prefix_len, int32_t* seq_len_out, uint8_t* k_pool,
+                        uint8_t* v_pool, float* kv_scale, int batch, int total_nodes, int hkv, int d,
+                        int32_t* dev_status, void* stream) {
+  const int rc = check_commit(SPEC_BF16, k_tree, v_tree, path, path_cap, accept_len, qo_indptr, page_table,
+                              max_pages, num_pages, page_size, prefix_len, k_pool, v_pool, batch, total_nodes, hkv, d);
+  if (rc != SPEC_OK || batch == 0) return rc;
+  if (!commit_kv8p_shape(page_size, d) || !grid_fits(hkv)) return SPEC_ERR_UNSUPPORTED;
+  if (!kv_scale) return SPEC_ERR_ARG;
+  return launch_kv_commit_kv8p(k_tree, v_tree, path, path_cap, accept_len, qo_indptr, page_table, max_pages,
+                               num_pages, page_size, prefix_len, seq_len_out, k_pool, v_pool, kv_scale, batch, hkv, d,
+                               dev_status, static_cast<cudaStream_t>(stream));
+}
+
+int spec_qk_norm_rope(int dtype, const void* q_in, long long q_stride, const void* k_in, long long k_stride,
+                      const void* v_in, long long v_stride, const void* q_weight, const void* k_weight, float eps,
+                      const float* cos_sin, int max_pos, int rot_dim, int interleaved, const int32_t* prefix_len,
+                      const int32_t* depth, const int32_t* qo_indptr, int batch, int total_nodes, int hq, int hkv,
+                      int d, void* q_out, void* k_out, void* v_out, int32_t* dev_status, void* stream) {
+  if (dtype != SPEC_F32 && dtype != SPEC_BF16) return SPEC_ERR_UNSUPPORTED;
+  if (batch < 0 || total_nodes < 0 || hq <= 0 || hkv <= 0 || d <= 0 || rot_dim < 0 || max_pos < 0) return SPEC_ERR_ARG;
+  if (d % 16 != 0 || d > 512 || rot_dim % 16 != 0 || rot_dim > d || hq > 4096 || hkv > 4096)
+    return SPEC_ERR_UNSUPPORTED;
+  if (!(eps >= 0.f) || (v_in == nullptr) != (v_out == nullptr)) return SPEC_ERR_ARG;
+  const long long vec = dtype == SPEC_F32 ? 4 : 8;  // elements of a 16-byte access
+  if (q_stride < (long long)hq * d || k_stride < (long long)hkv * d || q_stride % vec || k_stride % vec ||
+      (v_in && (v_stride < (long long)hkv * d || v_stride % vec)))
+    return SPEC_ERR_ARG;
+  if (batch == 0 || total_nodes == 0) return SPEC_OK;
+  if (!q_in || !k_in || !q_out || !k_out || !prefix_len || !qo_indptr) return SPEC_ERR_ARG;
+  if (rot_dim > 0 && (!cos_sin || max_pos == 0)) return SPEC_ERR_ARG;
+  if (!aligned16(q_in) || !aligned16(k_in) || !aligned16(v_in) || !aligned16(q_out) || !aligned16(k_out) ||
+      !aligned16(v_out) || !aligned16(q_weight) || !aligned16(k_weight) || !aligned16(cos_sin))
+    return SPEC_ERR_ARG;
+  return launch_qk_norm_rope(dtype, q_in, (long)q_stride, k_in, (long)k_stride, v_in, (long)v_stride, q_weight,
+                             k_weight, eps, cos_sin, max_pos, rot_dim, interleaved != 0, prefix_len, depth, qo_indptr,
+                             batch, total_nodes, hq, hkv, d, q_out, k_out, v_out, dev_status,
+                             static_cast<cudaStream_t>(stream));
+}
+
+int spec_page_table_resize(const int32_t* seq_len, const int32_t* qo_indptr, const int32_t* held, int32_t* page_table,
+                           int max_pages, int32_t* free_pages, int num_pages, const int32_t* n_free, int page_size,
+                           int shrink, int batch, int total_nodes, int32_t* held_out, int32_t* n_free_out,
+                           long long* slot_map, int32_t* dev_status, void* stream) {
+  if (batch < 0 || total_nodes < 0 || max_pages <= 0 || num_pages <= 0 || page_size <= 0) return SPEC_ERR_ARG;
+  if (batch > page_table_max_batch() || (long)batch * max_pages > 0x7FFFFFFFL) return SPEC_ERR_UNSUPPORTED;
+  if (batch == 0) return SPEC_OK;
+  if (!seq_len || !qo_indptr || !held || !page_table || !free_pages || !n_free || !held_out || !n_free_out)
+    return SPEC_ERR_ARG;
+  return launch_page_table(seq_len, qo_indptr, held, page_table, max_pages, free_pages, num_pages, n_free, page_size,
+                           shrink != 0, batch, total_nodes, held_out, n_free_out, slot_map, dev_status,
+                           static_cast<cudaStream_t>(stream));
+}
 
 int spec_tree_init(const int32_t* root_tokens, int batch, int max_nodes, void* state, size_t state_bytes,
                    int32_t* parent_out, int32_t* tokens_out, int32_t* n_nodes_out, int32_t* next_node,

@@ -3,6 +3,7 @@
 
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <stdint.h>
 
 #include <mutex>
@@ -37,6 +38,25 @@ template <typename T> __device__ __forceinline__ T from_f32(float x);
 template <> __device__ __forceinline__ float from_f32<float>(float x) { return x; }
 template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) {
   return __float2bfloat16_rn(x);
+}
+
+// The scale of one page of an 8-bit cache, as every call reads it: within [2^-50, 2^50]. (The
+// attention weighs a key by p * v_scale and divides its row sum by v_scale again; with scales
+// this near to each other neither can leave fp32's range. A scale of 0 or NaN, which a cache
+// does not hold, reads as 2^-50.)
+constexpr float kPageScaleMin = 8.8817841970012523e-16f, kPageScaleMax = 1125899906842624.0f;
+constexpr int kPageScaleExp = 50;
+__device__ __forceinline__ float page_scale(float s) { return fminf(fmaxf(s, kPageScaleMin), kPageScaleMax); }
+
+// Four E4M3 codes (byte i = element i) -> fp32, exactly (a NaN code gives NaN).
+__device__ __forceinline__ float4 e4m3x4_to_f32(uint32_t w) {
+  uint32_t lo, hi;
+  asm("{ .reg .b16 a, b; mov.b32 {a, b}, %2; cvt.rn.f16x2.e4m3x2 %0, a; cvt.rn.f16x2.e4m3x2 %1, b; }"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+  const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+  const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+  return make_float4(x.x, x.y, y.x, y.y);
 }
 
 // Programmatic dependent launch: a kernel launched with programmatic stream

@@ -1,0 +1,231 @@
+// Page-table rows grown (or shrunk) to the sequences' lengths, and the step's slot map.
+//
+// The lengths of a speculative step stay on the device (the commit writes seq_len there), so
+// the pages of the next step have to be given out there too. Sequence b needs
+//   need = ceil((seq_len[b] + n_b) / page_size) pages   (n_b = its nodes of this step)
+// and holds held[b]; what it lacks comes off a stack of free pages, what it no longer needs
+// (only where asked) goes back onto it. The result is a function of the inputs alone: with
+// exclusive sums over the sequences, G_b of the pages asked for and R_b of those returned,
+// and n1 = n_free + sum of the returned,
+//   returned page k of b      -> place n_free + R_b + k of the stack,
+//   page j granted to b       <- place n1 - 1 - (G_b + j),   granted while G_b + grow_b <= n1.
+//
+// Every CTA makes both sums itself (a few loads and one scan), so no CTA waits for another:
+// nothing one CTA writes is read by another. Grants read places below n_free, or returned
+// pages straight from the rows that give them up (the ends of shrinking rows, which nobody
+// writes); returned pages are written to places from n_free on; grants go to the entries past
+// a growing row's end. Only the two counters could be overwritten too early where they are
+// updated in place, so a second kernel, which starts after the first has ended, writes them.
+// Bound: latency for a step; the 8-byte slots' stores for a batch of prompts.
+#include "common.cuh"
+
+namespace specv {
+
+constexpr int kPageThreads = 512;
+constexpr int kPageMaxBatch = 4096;
+constexpr int kPagePer = kPageMaxBatch / kPageThreads;
+
+struct PageArgs {
+  const int32_t* seq_len;
+  const int32_t* qo;
+  const int32_t* held;
+  int32_t* page_table;
+  int32_t* free_pages;
+  const int32_t* n_free;
+  int32_t* held_out;
+  int32_t* n_free_out;
+  long long* slot_map;
+  int batch, total_nodes, max_pages, num_pages, page_size, shrink;
+  int32_t* status;
+};
+
+// What sequence b asks for (grow) and gives back (back); a sequence with bad or too long
+// sizes does neither (*code says which).
+struct PageWant {
+  int grow, back;
+};
+__device__ __forceinline__ PageWant page_want(const PageArgs& p, int b, int* code) {
+  const int len = __ldg(p.seq_len + b), n = __ldg(p.qo + b + 1) - __ldg(p.qo + b), held = __ldg(p.held + b);
+  *code = 0;
+  if (len < 0 || n < 0 || held < 0 || held > p.max_pages) {
+    *code = SPEC_ERR_INDEX;
+    return PageWant{0, 0};
+  }
+  const long long need = ((long long)len + n + p.page_size - 1) / p.page_size;
+  if (need > p.max_pages) {
+    *code = SPEC_ERR_CAPACITY;
+    return PageWant{0, 0};
+  }
+  return PageWant{need > held ? (int)need - held : 0, p.shrink && need < held ? held - (int)need : 0};
+}
+
+struct PagePlan {
+  int grow[kPageMaxBatch], back[kPageMaxBatch];  // inclusive sums over the sequences
+  int wg[kPageThreads / 32], wb[kPageThreads / 32];
+};
+
+// Inclusive sums of grow and back over the batch (the whole CTA); the totals fit 32 bits
+// (at most batch * max_pages entries of one table, checked on the host).
+__device__ __forceinline__ void page_plan(const PageArgs& p, PagePlan& s, bool tell) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = ceil_div(p.batch, kPageThreads);
+  int g[kPagePer], r[kPagePer], sg = 0, sr = 0;
+#pragma unroll
+  for (int i = 0; i < kPagePer; ++i) {
+    g[i] = r[i] = 0;
+    const int b = tid * per + i;
+    if (i < per && b < p.batch) {
+      int code;
+      const PageWant w = page_want(p, b, &code);
+      if (code != 0 && tell) report(p.status, code);
+      g[i] = w.grow;
+      r[i] = w.back;
+    }
+    sg += g[i];
+    sr += r[i];
+    g[i] = sg;
+    r[i] = sr;
+  }
+  int xg = sg, xr = sr;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int a = __shfl_up_sync(0xffffffffu, xg, o), c = __shfl_up_sync(0xffffffffu, xr, o);
+    if (lane >= o) {
+      xg += a;
+      xr += c;
+    }
+  }
+  if (lane == 31) {
+    s.wg[warp] = xg;
+    s.wb[warp] = xr;
+  }
+  __syncthreads();
+  int bg = xg - sg, br = xr - sr;
+  for (int w = 0; w < warp; ++w) {
+    bg += s.wg[w];
+    br += s.wb[w];
+  }
+#pragma unroll
+  for (int i = 0; i < kPagePer; ++i) {
+    const int b = tid * per + i;
+    if (i < per && b < p.batch) {
+      s.grow[b] = bg + g[i];
+      s.back[b] = br + r[i];
+    }
+  }
+  __syncthreads();
+}
+
+// First b with sums[b] > x (sums rise; x < sums[batch - 1]).
+__device__ __forceinline__ int page_owner(const int* sums, int batch, int x) {
+  int lo = 0, hi = batch - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (sums[mid] > x) hi = mid;
+    else lo = mid + 1;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ int page_returned(const PageArgs& p, const PagePlan& s, int r) {
+  const int b = page_owner(s.back, p.batch, r);
+  // row b gives up its last back_b entries, in order
+  return __ldcg(p.page_table + (size_t)b * p.max_pages + __ldg(p.held + b) - (s.back[b] - r));
+}
+
+__device__ __forceinline__ int page_granted(const PageArgs& p, const PagePlan& s, int n0, int n1, int x) {
+  const int at = n1 - 1 - x;
+  return at < n0 ? __ldcg(p.free_pages + at) : page_returned(p, s, at - n0);
+}
+
+__global__ void __launch_bounds__(kPageThreads) page_table_kernel(const PageArgs p) {
+  __shared__ PagePlan s;
+  pdl_trigger();
+  pdl_wait();
+  const int n0 = __ldg(p.n_free);
+  page_plan(p, s, blockIdx.x == 0);
+  const int asked = s.grow[p.batch - 1], back = s.back[p.batch - 1];
+  const int n1 = n0 + back;
+  const bool sane = n0 >= 0 && n1 <= p.num_pages;  // else the stack is not what it should be: nothing moves
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    if (!sane) report(p.status, SPEC_ERR_CAPACITY);
+    else if (asked > n1) report(p.status, SPEC_ERR_CAPACITY);
+  }
+  const int step = gridDim.x * kPageThreads, first = blockIdx.x * kPageThreads + threadIdx.x;
+  int granted = 0;
+  if (sane) {
+    granted = asked;
+    if (asked > n1) {  // in order, while they last
+      const int b = page_owner(s.grow, p.batch, n1);
+      granted = b > 0 ? s.grow[b - 1] : 0;
+    }
+    for (int x = first; x < granted; x += step) {
+      const int b = page_owner(s.grow, p.batch, x);
+      const int j = x - (b > 0 ? s.grow[b - 1] : 0);
+      const int page = page_granted(p, s, n0, n1, x);
+      if (page < 0 || page >= p.num_pages) report(p.status, SPEC_ERR_PAGE);
+      p.page_table[(size_t)b * p.max_pages + __ldg(p.held + b) + j] = page;
+    }
+    for (int r = first; r < back - granted; r += step) p.free_pages[n0 + r] = page_returned(p, s, r);
+  }
+  if (p.slot_map == nullptr) return;
+  const int last = min(p.total_nodes, __ldg(p.qo + p.batch));  // rows behind the last sequence stay as they are
+  for (int t = first; t < last; t += step) {
+    const int b = seq_of_row(p.qo, p.batch, t);
+    const int lo = __ldg(p.qo + b), len = __ldg(p.seq_len + b), held = __ldg(p.held + b);
+    long long slot = -1;
+    int page = -1;
+    if (len >= 0 && t >= lo && held >= 0 && held <= p.max_pages) {
+      const long long at = (long long)len + (t - lo);
+      const long long lp = at / p.page_size;
+      const int g0 = b > 0 ? s.grow[b - 1] : 0, r0 = b > 0 ? s.back[b - 1] : 0;
+      const int keeps = sane ? held - (s.back[b] - r0) : held;
+      if (lp < keeps) page = __ldcg(p.page_table + (size_t)b * p.max_pages + lp);
+      else if (s.grow[b] <= granted && lp < (long long)held + s.grow[b] - g0)
+        page = page_granted(p, s, n0, n1, g0 + (int)(lp - held));
+      if (page >= 0 && page < p.num_pages) slot = (long long)page * p.page_size + at % p.page_size;
+      else if (lp < keeps) report(p.status, SPEC_ERR_PAGE);
+    }
+    p.slot_map[t] = slot;
+  }
+}
+
+__global__ void __launch_bounds__(kPageThreads) page_count_kernel(const PageArgs p) {
+  __shared__ PagePlan s;
+  pdl_wait();  // the kernel before has read the counters that this one may overwrite
+  const int n0 = __ldg(p.n_free);
+  page_plan(p, s, false);
+  const int asked = s.grow[p.batch - 1], back = s.back[p.batch - 1];
+  const int n1 = n0 + back;
+  const bool sane = n0 >= 0 && n1 <= p.num_pages;
+  int granted = sane ? asked : 0;
+  if (sane && asked > n1) {
+    const int b = page_owner(s.grow, p.batch, n1);
+    granted = b > 0 ? s.grow[b - 1] : 0;
+  }
+  for (int b = threadIdx.x; b < p.batch; b += kPageThreads) {
+    const int g0 = b > 0 ? s.grow[b - 1] : 0, r0 = b > 0 ? s.back[b - 1] : 0;
+    int now = p.held[b];
+    if (sane) now += (s.grow[b] <= granted ? s.grow[b] - g0 : 0) - (s.back[b] - r0);
+    p.held_out[b] = now;
+  }
+  if (threadIdx.x == 0) *p.n_free_out = sane ? n1 - granted : n0;
+}
+
+int launch_page_table(const int32_t* seq_len, const int32_t* qo, const int32_t* held, int32_t* page_table,
+                      int max_pages, int32_t* free_pages, int num_pages, const int32_t* n_free, int page_size,
+                      int shrink, int batch, int total_nodes, int32_t* held_out, int32_t* n_free_out,
+                      long long* slot_map, int32_t* status, cudaStream_t stream) {
+  const PageArgs p{seq_len,  qo,    held,        page_table, free_pages, n_free,    held_out, n_free_out,
+                   slot_map, batch, total_nodes, max_pages,  num_pages,  page_size, shrink,   status};
+  const int work = slot_map != nullptr && total_nodes > batch ? total_nodes : batch;
+  const int ctas = ceil_div(work, kPageThreads);
+  if (launch_pdl(page_table_kernel, dim3(ctas < 304 ? ctas : 304), dim3(kPageThreads), 0, stream, p) != cudaSuccess)
+    return SPEC_ERR_CUDA;
+  if (launch_pdl(page_count_kernel, dim3(1), dim3(kPageThreads), 0, stream, p) != cudaSuccess) return SPEC_ERR_CUDA;
+  return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+}
+
+int page_table_max_batch() { return kPageMaxBatch; }
+
+}  // namespace specv
