@@ -69,7 +69,7 @@
  *     only after that wait, whether or not it signals early). A caller whose
  *     preceding kernel writes none of the inputs listed below can let two
  *     kernels read them before the wait with spec_set_early_reads(1):
- *     spec_tree_verify_attn (and its _kv8 and _parents forms) then reads q,
+ *     spec_tree_verify_attn (and its _kv8, _kv8p and _parents forms) then reads q,
  *     k_pool, v_pool, k_tree, v_tree, page_table, prefix_len, qo_indptr and
  *     kv_scale (everything but the mask or parent array) before it waits, and
  *     greedy spec_accept (and spec_accept_commit), when it walks from the root
@@ -551,7 +551,7 @@ int spec_kv_commit_kv8(const void* k_tree, const void* v_tree, const float* kv_s
  *   ws          workspace of spec_workspace_size(SPEC_OP_ATTN_KV8P, ...) bytes (256-byte
  *               aligned; any contents).
  *   Device errors: SPEC_ERR_PAGE (the page is read as zeros), SPEC_ERR_CAPACITY (a tree
- *   past max_nodes, a prefix past its row: that sequence's rows are left as they were),
+ *   past max_nodes, a prefix past max_prefix: that sequence's rows are left as they were),
  *   SPEC_ERR_TIMEOUT.
  */
 int spec_tree_verify_attn_kv8p(const void* q, const uint8_t* k_pool, const uint8_t* v_pool,

@@ -1,110 +1,919 @@
-// Tree-verify attention over an 8-bit paged cache with a scale per (page, KV head).
+// Tree-verify attention over an 8-bit paged cache with a scale per (page, KV head), on the
+// 5th-generation tensor cores.
 //
-// Row (node i of sequence b, query head h, g = h / (hq / hkv)), over the prefix keys j (page
-// and row of slot j) and the tree nodes that row's mask bits name:
-//   s_j = sm_scale * q . (k_code_j * ks[page_j][g]),   tree: q . k_j
-//   out = sum_j 2^((s_j - m) log2 e) v_j / sum_j 2^((s_j - m) log2 e),  v_j = v_code_j * vs
-// One warp per row, one pass over the keys with the running maximum and sum.
+// Row (node i of sequence b, query head h, g = h / G, G = hq / hkv), over the prefix keys j
+// (slot j's page and row) and the tree nodes its mask bits name:
+//   x_j = sm_scale * q . k_j,   out = sum_j e^(x_j) v_j / sum_j e^(x_j),
+//   prefix: k_j = k_code_j * ks[page_j][g], v_j = v_code_j * vs[page_j][g];  tree: bf16 rows.
+//
+// K's codes go to the tensor cores as they are (kind::f8f6f4), so QK needs no widened copy of
+// K. Its other operand has to be E4M3 too: a row of q, scaled by a power of two to a largest
+// element in [2^7, 2^8), is the sum of two E4M3 values, hi = e4m3(q) and lo = e4m3(q - hi): a
+// bf16 has 8 significant bits, an E4M3 4, so the sum is exact for elements within 2^10 of the
+// row's largest (and off by at most 2^-18 of it below). Two products of twice bf16's rate cost
+// what one bf16 product does.
+// P V runs in fp16: E4M3 is a subset of fp16, and P needs the range (a key that takes nearly
+// all of a row's weight leaves the others' weights 2^20 and more below it, where two E4M3
+// terms have run out of exponents). Four warps widen V's codes, one conversion for two.
+// The page's scales stay outside the products: ks multiplies the score's fp32 factor, and vs
+// enters the exponent, P_j = 2^(x_j log2 e + log2 vs_j - M + 11), where M follows the largest
+// x log2 e + log2 vs (P stays below 2^15, and full precision reaches 2^25 below the largest);
+// the row sum adds P_j / vs_j per page.
+//
+// A CTA = (key split, pair of row tiles, sequence x KV head). A row tile is 128 rows: 128 / G
+// nodes (rounded down) of G heads each. K/V come in blocks: first the split's tree blocks (64
+// nodes, bf16), then its prefix blocks (128 keys, 8 pages, TMA page by page). Two slots work
+// side by side, each with its S (128 columns) and O (128) in TMEM, its MMA-issuing warp and
+// four softmax warps, one row per thread:
+//   - two row tiles: each slot has a tile, both take every block;
+//   - one (few nodes, or a single token): both slots hold its rows and take the blocks in
+//     turn; their sums are joined in shared memory at the end.
+// Within a slot S, softmax and PV of a block follow each other (P overwrites S); the other
+// slot's products fill the tensor cores meanwhile.
+// Warps (512 threads): 0 TMA producer, 1 and 2 MMA issuers (1 also allocates TMEM), 4-7 and
+// 8-11 softmax of slots 0 and 1, 12-15 V's converters. Every wait is bounded.
+// Splits write O / l in fp32 and the log2-sum-exp, joined by a second kernel.
 #include "attn_common.cuh"
+#include "tc_host.cuh"
+#include "tc_math.cuh"
 
 namespace specv {
+namespace kv8p {
 
-struct Kv8pArgs {
+constexpr int kRows = 128;      // rows of a tile
+constexpr int kKeys = 128;      // keys of a prefix block
+constexpr int kPages = kKeys / 16;
+constexpr int kTreeKeys = 64;   // nodes of a tree block
+constexpr int kD = 128;
+constexpr int kThreads = 512;
+constexpr int kSoft0 = 4, kCvt = 12;         // first softmax warp, first converter warp
+constexpr int kStK = 3, kStC = 3, kStV = 2;  // stages: K, V codes, V in 16 bits
+constexpr uint32_t kSlab = 128 * 128;        // 128 rows of 128 bytes
+constexpr uint32_t kTreeSlab = kTreeKeys * 128;
+constexpr uint32_t kQTile = 2 * kSlab;       // bf16 halves, later the hi and lo codes
+constexpr uint32_t kOffQ = 0;
+constexpr uint32_t kOffK = kOffQ + 2 * kQTile;
+constexpr uint32_t kOffC = kOffK + kStK * kSlab;
+constexpr uint32_t kOffV = kOffC + kStC * kSlab;
+constexpr uint32_t kOffBar = kOffV + kStV * 2 * kSlab;
+constexpr int kScales = 8;                   // blocks whose page scales are kept
+constexpr uint32_t kOffScale = kOffBar + 512;
+constexpr uint32_t kSmem = kOffScale + kScales * kPages * 16 + 1024;  // + alignment slack
+static_assert(kSmem <= 232448, "shared memory over the per-CTA limit");
+constexpr uint32_t kTmemCols = 512;          // slot t: S at 256 t, O at 256 t + 128
+constexpr float kShift = 11.f;               // log2 of the largest P when M is set
+constexpr float kGrow = 4.f;                 // growth of the largest score that M may lag behind
+constexpr uint32_t kIdQK = tc::idesc_e4m3(kRows, kKeys);
+constexpr uint32_t kIdPV = tc::idesc_f16(kRows, kD, 1);
+constexpr uint32_t kIdTreeQK = tc::idesc_bf16(kRows, kTreeKeys, 0);
+constexpr uint32_t kIdTreePV = tc::idesc_bf16(kRows, kD, 1);
+constexpr int kMaxSplits = 32;
+constexpr int kMaxTreeBlocks = kMaxTreeNodes / kTreeKeys;
+
+struct Params {
   const __nv_bfloat16* q;
-  const uint8_t* k_pool;
-  const uint8_t* v_pool;
   const float2* kv_scale;
   const int32_t* page_table;
   int max_pages, num_pages;
+  int max_len;  // longest prefix that the row of pages and the caller's bound allow
   const int32_t* prefix_len;
-  const __nv_bfloat16* k_tree;
-  const __nv_bfloat16* v_tree;
   const uint64_t* mask;
   int mask_words;
   const int32_t* qo;
-  int batch, total_nodes, hq, hkv;
+  int hq, hkv, G, npt;  // npt: nodes of a row tile
+  int splits, mtiles;
   float scale_log2;
   __nv_bfloat16* out;
   float* lse;
+  float4* part_o;   // [tile][split][32 chunks of 4 columns][128 rows], O / l
+  float* part_lse;  // [tile][split][128 rows] log2-sum-exp (-inf: no keys)
   int32_t* status;
+  int early;
 };
 
-__device__ __forceinline__ float4 bf16x4(const __nv_bfloat16* p) {
-  const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
-  return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u), __uint_as_float(u.y << 16),
-                     __uint_as_float(u.y & 0xFFFF0000u));
+struct Bars {
+  uint64_t q16[2], q8[2];                     // a slot's q in bf16 / as two E4M3 terms
+  uint64_t k_full[kStK], k_empty[kStK], c_full[kStC], c_empty[kStC], v_full[kStV], v_empty[kStV];
+  uint64_t s_full[2], p_full[2], o_full[2];
+  uint64_t sc_full[kScales];
+  uint64_t bad[kMaxTreeBlocks];  // tree nodes whose V row holds an infinity or NaN
+  uint32_t tmem;
+  int abort;
+};
+static_assert(sizeof(Bars) <= 512, "barrier block over its reserved bytes");
+
+// The blocks of one key split: units are the tree blocks (4 each), then the prefix pages; a
+// split takes a contiguous run of units, a tree block goes to the split of its first unit.
+struct Split {
+  int tb_lo, nt;      // tree blocks
+  int pg_lo, pg_hi;   // prefix pages
+  int nb;             // blocks in all
+};
+__device__ __forceinline__ Split split_of(int P, int N, int splits, int s) {
+  const int np = (P + 15) >> 4, nt = (N + kTreeKeys - 1) / kTreeKeys;
+  const long units = 4L * nt + np;
+  const int lo = (int)(s * units / splits), hi = (int)((s + 1) * units / splits);
+  Split r;
+  r.tb_lo = min(nt, (lo + 3) >> 2);
+  r.nt = min(nt, (hi + 3) >> 2) - r.tb_lo;
+  r.pg_lo = max(lo - 4 * nt, 0);
+  r.pg_hi = max(hi - 4 * nt, 0);
+  r.nb = r.nt + (r.pg_hi - r.pg_lo + kPages - 1) / kPages;
+  return r;
 }
 
-__global__ void __launch_bounds__(256) attn_kv8p_kernel(const Kv8pArgs p) {
-  pdl_wait();
-  const int lane = threadIdx.x & 31;
-  const long row = (long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int t = (int)(row / p.hq), h = (int)(row - (long)t * p.hq);
-  if (t >= p.total_nodes || t >= __ldg(p.qo + p.batch)) return;
-  const int b = seq_of_row(p.qo, p.batch, t);
+__device__ __forceinline__ uint16_t e4m3x2(float x0, float x1) {
+  uint16_t c;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(x1), "f"(x0));
+  return c;
+}
+__device__ __forceinline__ uint32_t half2_of(uint16_t codes) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(codes));
+  return h;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+
+// 16-byte chunk c of row r of a 128-byte-row slab, in the 128-byte swizzle
+__device__ __forceinline__ uint32_t swz(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
+
+// A row of q as hi and lo E4M3 codes, in place of its bf16 halves; returns the factor that the
+// codes have to be multiplied by. (A row with an infinity or NaN gets a NaN code.)
+__device__ __forceinline__ float split_row(uint8_t* q, int r, const uint4* w) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) top = max(top, max(u[k] & 0x7FFFu, (u[k] >> 16) & 0x7FFFu));
+  }
+  const int e = max((int)(top >> 7), 1);       // exponent field of the largest element
+  // up * 2^(e - 134) = 1: q * up has its largest element in [2^7, 2^8). Both factors are made
+  // of two powers of two, as one may leave fp32's range.
+  const int sh = 134 - e;                      // in [-120, 133]
+  const float up0 = __uint_as_float((uint32_t)(127 + sh / 2) << 23);
+  const float up1 = __uint_as_float((uint32_t)(127 + sh - sh / 2) << 23);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {  // 16 elements, one 16-byte chunk of codes
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint4 v = w[2 * i + (k >> 1)];
+      const uint32_t a = (k & 1) ? v.z : v.x, b = (k & 1) ? v.w : v.y;
+      const float x0 = __uint_as_float(a << 16) * up0 * up1, x1 = __uint_as_float(a & 0xFFFF0000u) * up0 * up1;
+      const float x2 = __uint_as_float(b << 16) * up0 * up1, x3 = __uint_as_float(b & 0xFFFF0000u) * up0 * up1;
+      const uint16_t h01 = e4m3x2(x0, x1), h23 = e4m3x2(x2, x3);
+      const uint32_t f01 = half2_of(h01), f23 = half2_of(h23);
+      const float2 g01 = __half22float2(*reinterpret_cast<const __half2*>(&f01));
+      const float2 g23 = __half22float2(*reinterpret_cast<const __half2*>(&f23));
+      hi[k] = h01 | ((uint32_t)h23 << 16);
+      lo[k] = e4m3x2(x0 - g01.x, x1 - g01.y) | ((uint32_t)e4m3x2(x2 - g23.x, x3 - g23.y) << 16);
+    }
+    *reinterpret_cast<uint4*>(q + swz(r, i)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    *reinterpret_cast<uint4*>(q + kSlab + swz(r, i)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+  }
+  if (top >= 0x7F80u) q[swz(r, 0)] = 0x7F;
+  return __uint_as_float((uint32_t)(127 - sh / 2) << 23) * __uint_as_float((uint32_t)(127 - (sh - sh / 2)) << 23);
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_kv8p_kernel(const __grid_constant__ CUtensorMap tm_kp, const __grid_constant__ CUtensorMap tm_vp,
+                     const __grid_constant__ CUtensorMap tm_kt, const __grid_constant__ CUtensorMap tm_vt,
+                     const Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  Bars& bars = *reinterpret_cast<Bars*>(smem + kOffBar);
+  const uint32_t sb = tc::smem_u32(smem);
+  const int split = blockIdx.x, pair = blockIdx.y, bg = blockIdx.z;
+  pdl_trigger();  // the split merge waits for this grid to end
+  if (threadIdx.x == 0) {
+    tc::prefetch_tmap(&tm_kp);
+    tc::prefetch_tmap(&tm_vp);
+    tc::prefetch_tmap(&tm_kt);
+    tc::prefetch_tmap(&tm_vt);
+  }
+  if (!p.early) pdl_wait();
+  const int b = bg / p.hkv, g = bg - b * p.hkv;
   const int base = __ldg(p.qo + b), N = __ldg(p.qo + b + 1) - base, P = __ldg(p.prefix_len + b);
-  if (N > p.mask_words * 64 || P < 0 || P > p.max_pages * 16) {
-    if (lane == 0) report(p.status, SPEC_ERR_CAPACITY);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int node0 = 2 * pair * p.npt;
+  if (node0 >= N) return;
+  if (N > p.mask_words * 64 || P < 0 || P > p.max_len) {
+    if (threadIdx.x == 0 && split == 0) {
+      pdl_wait();
+      report(p.status, SPEC_ERR_CAPACITY);
+    }
     return;
   }
-  const int g = h / (p.hq / p.hkv);
-  const float4 q = bf16x4(p.q + row * 128 + 4 * lane);
-  float m = -INFINITY, l = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  auto key = [&](float4 k, float4 v, float ks, float vs) {
-    float s = q.x * k.x + q.y * k.y + q.z * k.z + q.w * k.w;
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-    s *= p.scale_log2 * ks;
-    const float mx = fmaxf(m, s);
-    const float a = mx == -INFINITY ? 1.f : exp2f(m - mx), w = mx == -INFINITY ? 0.f : exp2f(s - mx);
-    l = l * a + w;
-    const float wv = w * vs;
-    o = make_float4(o.x * a + wv * v.x, o.y * a + wv * v.y, o.z * a + wv * v.z, o.w * a + wv * v.w);
-    m = mx;
-  };
-  for (int j = 0; j < P; ++j) {
-    const int page = __ldg(p.page_table + (size_t)b * p.max_pages + (j >> 4));
-    if (page < 0 || page >= p.num_pages) {
-      report(p.status, SPEC_ERR_PAGE);
-      key(make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f), 1.f, 1.f);
-      continue;
+  const bool two = node0 + p.npt < N;  // two row tiles; else both slots hold the same rows
+  const Split sp = split_of(P, N, p.splits, split);
+  const int nb = sp.nb, nt = sp.nt;
+  // slot t's blocks are i0(t), i0 + step, ... below nb
+  const int step = two ? 1 : 2;
+
+  // softmax threads: slot, row, and what the row stands for
+  const int slot = warp >= 8 ? 1 : 0;
+  const int row = threadIdx.x & 127;
+  const int node = node0 + (two ? slot * p.npt : 0) + row / p.G;
+  const int head = g * p.G + row % p.G;
+  const bool valid = row < p.npt * p.G && node < N;
+  const size_t orow = (size_t)(base + node) * p.hq + head;
+  const int tile = 2 * pair + (two ? slot : 0) + p.mtiles * bg;
+
+  if (nb == 0) {  // an empty key split: nothing for the merge
+    if (warp >= kSoft0 && warp < kCvt) {
+      pdl_wait();
+      if (valid) p.part_lse[((size_t)tile * p.splits + split) * kRows + row] = -INFINITY;
     }
-    const size_t unit = (size_t)page * p.hkv + g;
-    const float2 sc = __ldg(p.kv_scale + unit);
-    const size_t at = (unit * 16 + (j & 15)) * 128 + 4 * lane;
-    key(e4m3x4_to_f32(__ldg(reinterpret_cast<const uint32_t*>(p.k_pool + at))),
-        e4m3x4_to_f32(__ldg(reinterpret_cast<const uint32_t*>(p.v_pool + at))), page_scale(sc.x), page_scale(sc.y));
+    return;
   }
-  const uint64_t* mrow = p.mask + (size_t)t * p.mask_words;
-  for (int j = 0; j < N; ++j) {
-    if (!((__ldg(mrow + (j >> 6)) >> (j & 63)) & 1)) continue;
-    const size_t at = ((size_t)(base + j) * p.hkv + g) * 128 + 4 * lane;
-    key(bf16x4(p.k_tree + at), bf16x4(p.v_tree + at), 1.f, 1.f);
+
+  auto bar = [&](uint64_t* x) { return tc::smem_u32(x); };
+  volatile int* abort = &bars.abort;
+  if (warp == 0) {
+    if (lane == 0) {
+      for (int t = 0; t < 2; ++t) {
+        tc::mbar_init(bar(&bars.q16[t]), 128);
+        tc::mbar_init(bar(&bars.q8[t]), 128);
+        tc::mbar_init(bar(&bars.s_full[t]), 1);
+        tc::mbar_init(bar(&bars.p_full[t]), 128);
+        tc::mbar_init(bar(&bars.o_full[t]), 1);
+      }
+      const int users = two ? 2 : 1;
+      for (int s = 0; s < kStK; ++s) {
+        tc::mbar_init(bar(&bars.k_full[s]), 1);
+        tc::mbar_init(bar(&bars.k_empty[s]), users);
+      }
+      for (int s = 0; s < kStC; ++s) {
+        tc::mbar_init(bar(&bars.c_full[s]), 1);
+        tc::mbar_init(bar(&bars.c_empty[s]), 4);
+      }
+      for (int s = 0; s < kStV; ++s) {
+        tc::mbar_init(bar(&bars.v_full[s]), 4);
+        tc::mbar_init(bar(&bars.v_empty[s]), users);
+      }
+      for (int s = 0; s < kScales; ++s) tc::mbar_init(bar(&bars.sc_full[s]), 1);
+      for (int s = 0; s < kMaxTreeBlocks; ++s) bars.bad[s] = 0;
+      bars.abort = 0;
+      tc::mbar_fence_init();
+    }
+  } else if (warp == 1) {
+    tc::tmem_alloc(bar(reinterpret_cast<uint64_t*>(&bars.tmem)), kTmemCols);
+    tc::tmem_relinquish();
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  const __nv_bfloat162 a = __floats2bfloat162_rn(o.x * inv, o.y * inv), c = __floats2bfloat162_rn(o.z * inv, o.w * inv);
-  *reinterpret_cast<uint2*>(p.out + row * 128 + 4 * lane) =
-      make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&c));
-  if (lane == 0 && p.lse != nullptr) p.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = bars.tmem;
+
+  float m = -INFINITY, l = 0.f;  // softmax threads: running maximum and sum
+  bool ok = true;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------------ TMA producer
+    // Page ids of four blocks at a time, one per lane, a batch ahead; then their scales.
+    auto ids_of = [&](int k) -> int {
+      const int lp = sp.pg_lo + 32 * k + lane;
+      int page = p.num_pages;  // out of range: TMA reads zeros
+      if (lp < sp.pg_hi) {
+        const int x = __ldg(p.page_table + (size_t)b * p.max_pages + lp);
+        if (x >= 0 && x < p.num_pages) page = x;
+        else report(p.status, SPEC_ERR_PAGE);
+      }
+      return page;
+    };
+    auto scale_of = [&](int page) {
+      return page < p.num_pages ? __ldg(p.kv_scale + (size_t)page * p.hkv + g) : make_float2(1.f, 1.f);
+    };
+    int ids = ids_of(0), ids_next = ids_of(1);
+    float2 sc = scale_of(ids), sc_next = make_float2(1.f, 1.f);
+    int done = 0;  // blocks whose copies were issued
+    for (int i = 0; i < nb; ++i) {
+      const int sk = i % kStK, sc_ = i % kStC;
+      if (i >= kStK && !warp_wait(bar(&bars.k_empty[sk]), ((i / kStK) & 1) ^ 1, abort)) break;
+      if (i >= kStC && !warp_wait(bar(&bars.c_empty[sc_]), ((i / kStC) & 1) ^ 1, abort)) break;
+      const uint32_t kdst = sb + kOffK + sk * kSlab, cdst = sb + kOffC + sc_ * kSlab;
+      if (lane == 0) {
+        tc::mbar_arrive_expect_tx(bar(&bars.k_full[sk]), kSlab);
+        tc::mbar_arrive_expect_tx(bar(&bars.c_full[sc_]), kSlab);
+      }
+      __syncwarp();
+      if (i < nt) {
+        if (lane < 4) {  // K and V, two 64-column halves each
+          const int half = lane & 1, row0 = base + (sp.tb_lo + i) * kTreeKeys;
+          if (lane < 2) tc::tma_load_3d(kdst + half * kTreeSlab, &tm_kt, bar(&bars.k_full[sk]), half * 64, g, row0);
+          else tc::tma_load_3d(cdst + half * kTreeSlab, &tm_vt, bar(&bars.c_full[sc_]), half * 64, g, row0);
+        }
+      } else {
+        const int j = i - nt;
+        if (j > 0 && (j & 3) == 0) {
+          ids = ids_next;
+          sc = sc_next;
+          ids_next = ids_of((j >> 2) + 1);
+        }
+        const int from = (j & 3) * kPages + (lane & 7);
+        const int page = __shfl_sync(0xffffffffu, ids, from);
+        if (lane < kPages) tc::tma_load_4d(kdst + lane * 2048, &tm_kp, bar(&bars.k_full[sk]), 0, 0, g, page);
+        else if (lane < 2 * kPages)
+          tc::tma_load_4d(cdst + (lane - kPages) * 2048, &tm_vp, bar(&bars.c_full[sc_]), 0, 0, g, page);
+        if ((j & 3) == 1) sc_next = scale_of(ids_next);
+        const float ks = page_scale(__shfl_sync(0xffffffffu, sc.x, from));
+        const float vs = page_scale(__shfl_sync(0xffffffffu, sc.y, from));
+        if (lane < kPages)
+          *reinterpret_cast<float4*>(smem + kOffScale + ((j % kScales) * kPages + lane) * 16) =
+              make_float4(ks, log2f(vs), 1.f / vs, 0.f);
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(bar(&bars.sc_full[j % kScales]));
+      }
+      done = i + 1;
+    }
+    if (done < nb && lane == 0) {  // given up: leave no copy in flight
+      report(p.status, SPEC_ERR_TIMEOUT);
+      int zero = 0;
+      for (int i = max(0, done - kStK); i < done; ++i)
+        tc::mbar_wait(bar(&bars.k_full[i % kStK]), (i / kStK) & 1, &zero, kWaitLimit);
+      zero = 0;
+      for (int i = max(0, done - kStC); i < done; ++i)
+        tc::mbar_wait(bar(&bars.c_full[i % kStC]), (i / kStC) & 1, &zero, kWaitLimit);
+    }
+    __syncwarp();
+  } else if (warp == 1 || warp == 2) {
+    // ------------------------------------------------------------------ MMA issuers
+    const int t = warp - 1;
+    if (lane == 0) {
+      const uint32_t qb = sb + kOffQ + t * kQTile, ts = tmem + t * 256, to = ts + 128;
+      bool issued = false, any = false, q8 = false, q16 = false;
+      for (int i = two ? 0 : t; ok && i < nb; i += step) {
+        const int sk = i % kStK, sv = i % kStV;
+        const uint32_t kb = sb + kOffK + sk * kSlab, vb = sb + kOffV + sv * 2 * kSlab;
+        const bool tree = i < nt;
+        if (tree && !q16) ok = tc::mbar_wait(bar(&bars.q16[t]), 0, abort, kWaitLimit), q16 = true;
+        if (!tree && !q8) ok = tc::mbar_wait(bar(&bars.q8[t]), 0, abort, kWaitLimit), q8 = true;
+        ok = ok && tc::mbar_wait(bar(&bars.k_full[sk]), (i / kStK) & 1, abort, kWaitLimit);
+        if (!ok) break;
+        tc::fence_after_sync();
+        if (tree) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            tc::mma_bf16(ts, tc::sdesc_sw128(qb + (k >> 2) * kSlab + (k & 3) * 32, 16, 1024),
+                         tc::sdesc_sw128(kb + (k >> 2) * kTreeSlab + (k & 3) * 32, 16, 1024), kIdTreeQK, k > 0);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)  // hi, then lo
+            tc::mma_f8(ts, tc::sdesc_sw128(qb + (k >> 2) * kSlab + (k & 3) * 32, 16, 1024),
+                       tc::sdesc_sw128(kb + (k & 3) * 32, 16, 1024), kIdQK, k > 0);
+        }
+        issued = true;
+        tc::mma_commit(bar(&bars.s_full[t]));
+        tc::mma_commit(bar(&bars.k_empty[sk]));
+        const int n = two ? i : i >> 1;  // this slot's blocks so far
+        ok = tc::mbar_wait(bar(&bars.v_full[sv]), (i / kStV) & 1, abort, kWaitLimit) &&
+             tc::mbar_wait(bar(&bars.p_full[t]), n & 1, abort, kWaitLimit);
+        if (!ok) break;
+        tc::fence_after_sync();
+        if (tree) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)  // P's two bf16 terms, four steps of 16 nodes each
+            tc::mma_bf16_ts(to, ts + 8 * k, tc::sdesc_sw128(vb + (k & 3) * 2048, kSlab, 1024), kIdTreePV,
+                            any || k > 0);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            tc::mma_bf16_ts(to, ts + 8 * k, tc::sdesc_sw128(vb + k * 2048, kSlab, 1024), kIdPV, any || k > 0);
+        }
+        any = true;
+        tc::mma_commit(bar(&bars.v_empty[sv]));
+      }
+      if (!ok) report(p.status, SPEC_ERR_TIMEOUT);
+      // every product issued has completed before O is read and TMEM released
+      if (issued) {
+        tc::mma_commit(bar(&bars.o_full[t]));
+        int zero = 0;
+        tc::mbar_wait(bar(&bars.o_full[t]), 0, &zero, kWaitLimit);
+      }
+    }
+    __syncwarp();
+  } else if (warp >= kCvt) {
+    // ------------------------------------------------------------------ V converters
+    const int ct = threadIdx.x - kCvt * 32;
+    for (int i = 0; i < nb; ++i) {
+      const int sc_ = i % kStC, sv = i % kStV;
+      if (!warp_wait(bar(&bars.c_full[sc_]), (i / kStC) & 1, abort) ||
+          (i >= kStV && !warp_wait(bar(&bars.v_empty[sv]), ((i / kStV) & 1) ^ 1, abort))) {
+        if (lane == 0) report(p.status, SPEC_ERR_TIMEOUT);
+        break;
+      }
+      const uint8_t* src = smem + kOffC + sc_ * kSlab;
+      uint8_t* dst = smem + kOffV + sv * 2 * kSlab;
+      if (i < nt) {
+        // bf16 rows as they are, but for rows past the tree and elements that are not finite
+        // (a weight of 0 times either would reach rows whose mask leaves the node out)
+        const int tb = sp.tb_lo + i, nvalid = N - tb * kTreeKeys;
+#pragma unroll
+        for (int it = 0; it < 8; ++it) {
+          const int id = it * 128 + ct, half = id >> 9, off = id & 511, r = off >> 3;
+          uint4 w = *reinterpret_cast<const uint4*>(src + half * kTreeSlab + off * 16);
+          uint32_t u[4] = {w.x, w.y, w.z, w.w};
+          bool bad = false;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if (r >= nvalid) u[k] = 0;
+            if ((u[k] & 0x7F80u) == 0x7F80u) {
+              u[k] &= 0xFFFF0000u;
+              bad = true;
+            }
+            if ((u[k] & 0x7F800000u) == 0x7F800000u) {
+              u[k] &= 0xFFFFu;
+              bad = true;
+            }
+          }
+          if (bad) atomicOr(reinterpret_cast<unsigned long long*>(&bars.bad[tb]), 1ull << r);
+          *reinterpret_cast<uint4*>(dst + half * kSlab + off * 16) = make_uint4(u[0], u[1], u[2], u[3]);
+        }
+      } else {
+        const int pg = sp.pg_lo + (i - nt) * kPages;
+        const int nvalid = min(P, sp.pg_hi * 16) - pg * 16;  // rows past it may hold anything
+#pragma unroll
+        for (int it = 0; it < 8; ++it) {
+          const int id = it * 128 + ct;
+          const int r = (id & 7) | ((id >> 6) << 3), cc = (id >> 3) & 7;
+          uint4 w = *reinterpret_cast<const uint4*>(src + swz(r, cc));
+          if (r >= nvalid) w = make_uint4(0, 0, 0, 0);
+          const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+          uint32_t h[8];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            h[2 * k] = half2_of((uint16_t)(u[k] & 0xFFFFu));
+            h[2 * k + 1] = half2_of((uint16_t)(u[k] >> 16));
+          }
+          uint8_t* to = dst + (cc >> 2) * kSlab;
+          *reinterpret_cast<uint4*>(to + swz(r, (cc & 3) * 2)) = make_uint4(h[0], h[1], h[2], h[3]);
+          *reinterpret_cast<uint4*>(to + swz(r, (cc & 3) * 2 + 1)) = make_uint4(h[4], h[5], h[6], h[7]);
+        }
+      }
+      tc::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        tc::mbar_arrive(bar(&bars.v_full[sv]));
+        tc::mbar_arrive(bar(&bars.c_empty[sc_]));
+      }
+    }
+  } else if (warp >= kSoft0) {
+    // ------------------------------------------------------------------ softmax
+    const int i0 = two ? 0 : slot;
+    const uint32_t ts = tmem + slot * 256 + ((uint32_t)((warp & 3) * 32) << 16), to = ts + 128;
+    uint8_t* q = smem + kOffQ + slot * kQTile;
+    const bool live = __any_sync(0xffffffffu, valid);  // a warp without rows only keeps step
+    const int last_tree = i0 < nt ? i0 + (nt - 1 - i0) / step * step : -1;
+    float qf = 0.f;  // the factor of the row's codes
+    uint64_t bits = 0ull;
+    const uint64_t* mrow = p.mask + (size_t)(base + node) * p.mask_words;
+    if (i0 < nb) {
+      uint4 w[16];
+      const uint4* src = reinterpret_cast<const uint4*>(p.q + orow * kD);
+#pragma unroll
+      for (int k = 0; k < 16; ++k) w[k] = valid ? __ldg(src + k) : make_uint4(0, 0, 0, 0);
+      if (last_tree >= 0) {
+#pragma unroll
+        for (int k = 0; k < 16; ++k) *reinterpret_cast<uint4*>(q + (k >> 3) * kSlab + swz(row, k & 7)) = w[k];
+        tc::fence_proxy_async_smem();
+        tc::mbar_arrive(bar(&bars.q16[slot]));
+        pdl_wait();  // the mask may come from the kernel before
+        if (valid) bits = __ldcg(mrow + sp.tb_lo + i0);
+      } else {
+        qf = split_row(q, row, w);
+        tc::fence_proxy_async_smem();
+        tc::mbar_arrive(bar(&bars.q8[slot]));
+      }
+    }
+    for (int i = i0, n = 0; i < nb; i += step, ++n) {
+      if (!warp_wait(bar(&bars.s_full[slot]), n & 1, abort)) {
+        ok = false;
+        break;
+      }
+      tc::fence_after_sync();  // S of this block; O of all before
+      float alpha = 1.f;
+      bool rescale = false;
+      auto raise = [&](float mx) {
+        if (mx > -INFINITY && (m == -INFINITY || mx > m + kGrow)) {
+          alpha = m == -INFINITY ? 0.f : ex2_approx(m - mx);
+          m = mx;
+          l *= alpha;
+          rescale = n > 0;
+        }
+        if (__any_sync(0xffffffffu, rescale)) {
+#pragma unroll 1
+          for (int ch = 0; ch < kD / 32; ++ch) {
+            float o[32];
+            tc::tmem_ld32(to + ch * 32, o);
+            tc::tmem_wait_ld();
+            const float f = rescale ? alpha : 1.f;
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] *= f;
+            tc::tmem_st32(to + ch * 32, o);
+          }
+        }
+      };
+      if (i < nt) {
+        if (live) {
+          float s[kTreeKeys];
+          tc::tmem_ld32(ts, s);
+          tc::tmem_ld32(ts + 32, s + 32);
+          tc::tmem_wait_ld();
+          const uint64_t see = bits;
+          if (valid && i + step < nt) bits = __ldcg(mrow + sp.tb_lo + i + step);
+          float mx = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < kTreeKeys; ++c) {
+            s[c] = ((see >> c) & 1ull) ? s[c] * p.scale_log2 : -INFINITY;
+            mx = fmaxf(mx, s[c]);
+          }
+          raise(mx);
+          const float off = m == -INFINITY ? 0.f : kShift - m;
+          uint32_t hi[kTreeKeys / 2], lo[kTreeKeys / 2];
+          float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll
+          for (int c = 0; c < kTreeKeys; c += 2) {
+            const float a = ex2_approx(s[c] + off), d = ex2_approx(s[c + 1] + off);
+            sum0 += a;
+            sum1 += d;
+            const uint32_t h = pack_bf16x2(a, d);
+            hi[c >> 1] = h;
+            lo[c >> 1] = pack_bf16x2(a - __uint_as_float(h << 16), d - __uint_as_float(h & 0xFFFF0000u));
+          }
+          l += sum0 + sum1;
+          tc::tmem_st32_u(ts, hi);
+          tc::tmem_st32_u(ts + 32, lo);
+          tc::tmem_wait_st();
+        }
+        tc::fence_before_sync();
+        tc::mbar_arrive(bar(&bars.p_full[slot]));
+        if (i == last_tree && i + step < nb) {
+          // the tree's last S is complete, so q's bf16 rows have been read: codes in their place
+          uint4 w[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) w[k] = *reinterpret_cast<const uint4*>(q + (k >> 3) * kSlab + swz(row, k & 7));
+          qf = split_row(q, row, w);
+          tc::fence_proxy_async_smem();
+          tc::mbar_arrive(bar(&bars.q8[slot]));
+        }
+        continue;
+      }
+      const int j = i - nt;
+      if (!warp_wait(bar(&bars.sc_full[j % kScales]), (j / kScales) & 1, abort)) {
+        ok = false;
+        break;
+      }
+      if (live) {
+        const float4* scale = reinterpret_cast<const float4*>(smem + kOffScale) + (j % kScales) * kPages;
+        const int nvalid = min(P, sp.pg_hi * 16) - (sp.pg_lo + j * kPages) * 16;
+        const float sc = p.scale_log2 * qf;
+        // (kept above 0, so that a key past the prefix stays at -inf; a score is 0 there all the same)
+        auto factor = [&](float ks) { return fmaxf(sc * ks, 1e-37f); };
+        float s[64];
+        // the largest x log2 e + log2 vs: columns 64-127, then 0-63 (which stay in registers)
+        float mx = -INFINITY;
+#pragma unroll
+        for (int h = 1; h >= 0; --h) {
+          tc::tmem_ld32(ts + 64 * h, s);
+          tc::tmem_ld32(ts + 64 * h + 32, s + 32);
+          tc::tmem_wait_ld();
+          if (nvalid < kKeys) {
+#pragma unroll
+            for (int c = 0; c < 64; ++c) s[c] = 64 * h + c < nvalid ? s[c] : -INFINITY;
+          }
+#pragma unroll
+          for (int g4 = 0; g4 < 4; ++g4) {
+            const float* v = s + 16 * g4;
+            float x = fmax3(v[0], v[1], v[2]);
+#pragma unroll
+            for (int c = 3; c < 15; c += 2) x = fmax3(x, v[c], v[c + 1]);
+            const float4 f = scale[4 * h + g4];
+            mx = fmaxf(mx, fmaf(fmaxf(x, v[15]), factor(f.x), f.y));
+          }
+        }
+        raise(mx);
+        const float off = m == -INFINITY ? 0.f : kShift - m;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (h == 1) {
+            tc::tmem_ld32(ts + 64, s);
+            tc::tmem_ld32(ts + 96, s + 32);
+            tc::tmem_wait_ld();
+            if (nvalid < kKeys) {
+#pragma unroll
+              for (int c = 0; c < 64; ++c) s[c] = 64 + c < nvalid ? s[c] : -INFINITY;
+            }
+          }
+          uint32_t pk[32];
+#pragma unroll
+          for (int g4 = 0; g4 < 4; ++g4) {
+            const float4 f = scale[4 * h + g4];
+            const float2 f2 = make_float2(factor(f.x), factor(f.x)), o2 = make_float2(off + f.y, off + f.y);
+            float2 r0 = make_float2(0.f, 0.f), r1 = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int c = 16 * g4; c < 16 * g4 + 16; c += 4) {
+              const float2 a = ffma2(make_float2(s[c], s[c + 1]), f2, o2);
+              const float2 d = ffma2(make_float2(s[c + 2], s[c + 3]), f2, o2);
+              const float2 ea = make_float2(ex2_approx(a.x), ex2_approx(a.y));
+              const float2 ed = make_float2(ex2_approx(d.x), ex2_approx(d.y));
+              r0 = fadd2(r0, ea);
+              r1 = fadd2(r1, ed);
+              pk[c >> 1] = pack_f16x2(ea.x, ea.y);
+              pk[(c >> 1) + 1] = pack_f16x2(ed.x, ed.y);
+            }
+            l = fmaf((r0.x + r0.y) + (r1.x + r1.y), f.z, l);
+          }
+          tc::tmem_st32_u(ts + 32 * h, pk);
+        }
+        tc::tmem_wait_st();
+      }
+      tc::fence_before_sync();
+      tc::mbar_arrive(bar(&bars.p_full[slot]));
+    }
+    if (!ok && lane == 0) report(p.status, SPEC_ERR_TIMEOUT);
+  }
+
+  // ---------------------------------------------------------------------- epilogue
+  tc::fence_before_sync();
+  __syncthreads();  // every product is complete, every copy has landed
+  tc::fence_after_sync();
+  if (warp >= kSoft0 && warp < kCvt) {
+    const uint32_t to = tmem + slot * 256 + 128 + ((uint32_t)((warp & 3) * 32) << 16);
+    // one tile: slot 1 hands its sums to slot 0 through shared memory (chunk of 4 columns,
+    // then row: consecutive lanes, consecutive 16 bytes)
+    float4* join = reinterpret_cast<float4*>(smem + kOffQ);
+    float2* join_ml = reinterpret_cast<float2*>(smem + kOffK);
+    const bool live = __any_sync(0xffffffffu, valid);
+    if (!two) {
+      if (slot == 1 && live) {
+        if (valid) join_ml[row] = make_float2(m, l);
+        if (nb > 1) {
+#pragma unroll 1
+          for (int ch = 0; ch < kD / 32; ++ch) {
+            float o[32];
+            __syncwarp();
+            tc::tmem_ld32(to + ch * 32, o);
+            tc::tmem_wait_ld();
+            if (valid) {
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                join[(ch * 8 + k) * kRows + row] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+            }
+          }
+        }
+      }
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+    }
+    if (live && (two || slot == 0)) {
+      float w0 = 1.f, w1 = 0.f;
+      const bool joined = !two && nb > 1;
+      if (joined && valid) {
+        const float2 x = join_ml[row];
+        const float top = fmaxf(m, x.x);
+        w0 = m == -INFINITY ? 0.f : ex2_approx(m - top);
+        w1 = x.x == -INFINITY ? 0.f : ex2_approx(x.x - top);
+        l = l * w0 + x.y * w1;
+        m = top;
+      }
+      float inv = l == 0.f ? 0.f : 1.f / l;
+      // a tree node that this row sees holds an infinity or NaN in V
+      for (int i = 0; i < nt; ++i) {
+        const uint64_t bad = bars.bad[sp.tb_lo + i];
+        if (bad != 0 && valid && (__ldcg(p.mask + (size_t)(base + node) * p.mask_words + sp.tb_lo + i) & bad) != 0)
+          inv = __int_as_float(0x7FC00000);
+      }
+      if (!ok || *abort) inv = 0.f;
+      pdl_wait();  // nothing is written before the kernel before has finished
+      const float lse2 = l == 0.f ? -INFINITY : m + log2f(l) - kShift;
+#pragma unroll 1
+      for (int ch = 0; ch < kD / 32; ++ch) {
+        float o[32];
+        __syncwarp();
+        tc::tmem_ld32(to + ch * 32, o);
+        tc::tmem_wait_ld();
+        if (!valid) continue;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          float4 x = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+          if (joined) {
+            const float4 y = join[(ch * 8 + k) * kRows + row];
+            x = make_float4(x.x * w0 + y.x * w1, x.y * w0 + y.y * w1, x.z * w0 + y.z * w1, x.w * w0 + y.w * w1);
+          }
+          o[4 * k] = x.x * inv;
+          o[4 * k + 1] = x.y * inv;
+          o[4 * k + 2] = x.z * inv;
+          o[4 * k + 3] = x.w * inv;
+        }
+        if (p.splits == 1) {
+          uint4* dst = reinterpret_cast<uint4*>(p.out + orow * kD + ch * 32);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            dst[k] = make_uint4(pack_bf16x2(o[8 * k], o[8 * k + 1]), pack_bf16x2(o[8 * k + 2], o[8 * k + 3]),
+                                pack_bf16x2(o[8 * k + 4], o[8 * k + 5]), pack_bf16x2(o[8 * k + 6], o[8 * k + 7]));
+        } else {
+          float4* po = p.part_o + ((size_t)tile * p.splits + split) * (kRows * kD / 4);
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            po[(ch * 8 + k) * kRows + row] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+        }
+      }
+      if (valid) {
+        if (p.splits > 1) p.part_lse[((size_t)tile * p.splits + split) * kRows + row] = lse2;
+        else if (p.lse != nullptr) p.lse[orow] = lse2 * kLn2;
+      }
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == 1) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, kTmemCols);
+  }
 }
 
-size_t attn_kv8p_ws_bytes(int, int, int, int, int) { return 0; }
+// Merge of the key splits: out = sum_s 2^(lse_s - M) O_s / sum_s 2^(lse_s - M). One thread per
+// (tile, 4 columns, row), every load issued before any is used.
+struct MergeParams {
+  const float4* part_o;
+  const float* part_lse;
+  const int32_t* qo;
+  const int32_t* prefix_len;
+  int max_len, mask_words;
+  int splits, mtiles, hkv, hq, G, npt;
+  long tiles;
+  __nv_bfloat16* out;
+  float* lse;
+};
+constexpr int kMergeThreads = 64;
+
+template <int MAXS>
+__global__ void __launch_bounds__(kMergeThreads) attn_kv8p_merge_kernel(const MergeParams p) {
+  pdl_trigger();
+  const long idx = (long)blockIdx.x * kMergeThreads + threadIdx.x;
+  if (idx >= p.tiles * 32 * kRows) return;
+  const int tile = (int)(idx / (32 * kRows)), rem = (int)(idx - (long)tile * 32 * kRows);
+  const int c = rem / kRows, r = rem % kRows;
+  const int tt = tile % p.mtiles, bg = tile / p.mtiles, b = bg / p.hkv, g = bg - b * p.hkv;
+  const int node = tt * p.npt + r / p.G;
+  if (r >= p.npt * p.G) return;
+  pdl_wait();  // the attention grid has finished: its partials are visible
+  const int base = __ldg(p.qo + b), N = __ldg(p.qo + b + 1) - base, P = __ldg(p.prefix_len + b);
+  if (node >= N || N > p.mask_words * 64 || P < 0 || P > p.max_len) return;  // as the attention
+  const float* ls = p.part_lse + (size_t)tile * p.splits * kRows + r;
+  const float4* po = p.part_o + (size_t)tile * p.splits * (kRows * kD / 4) + c * kRows + r;
+  float lv[MAXS];
+  float4 o[MAXS];
+#pragma unroll
+  for (int s = 0; s < MAXS; ++s) {
+    lv[s] = s < p.splits ? __ldcg(ls + s * kRows) : -INFINITY;
+    o[s] = s < p.splits ? __ldcg(po + (size_t)s * (kRows * kD / 4)) : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  float M = -INFINITY, L = 0.f;
+#pragma unroll
+  for (int s = 0; s < MAXS; ++s) M = fmaxf(M, lv[s]);
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int s = 0; s < MAXS; ++s) {
+    if (lv[s] == -INFINITY) continue;  // nothing in it: its row was not written
+    const float w = ex2_approx(lv[s] - M);
+    L += w;
+    acc = make_float4(fmaf(o[s].x, w, acc.x), fmaf(o[s].y, w, acc.y), fmaf(o[s].z, w, acc.z), fmaf(o[s].w, w, acc.w));
+  }
+  const float inv = L == 0.f ? 0.f : 1.f / L;
+  const size_t orow = (size_t)(base + node) * p.hq + g * p.G + r % p.G;
+  *reinterpret_cast<uint2*>(p.out + orow * kD + c * 4) =
+      make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+  if (c == 0 && p.lse != nullptr) p.lse[orow] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+}
+
+// ------------------------------------------------------------------------------------ host
+
+static int tiles_of(int max_nodes, int npt) { return ceil_div(max_nodes, npt); }
+
+// Key splits per work item (sequence, KV head, pair of row tiles), from the sizes alone; one
+// CTA fits on an SM. Fewer items than SMs: the splits that cover the SMs. Otherwise the count
+// in 1..8 whose waves cost least (a CTA's fixed cost counted as two blocks), if that is at
+// least 8% below the unsplit cost (the merge kernel is not in the model).
+static int splits_of(int batch, int max_nodes, int hq, int hkv, int max_prefix) {
+  const int npt = kRows / (hq / hkv);
+  const long items = (long)batch * hkv * ceil_div(tiles_of(max_nodes, npt), 2), sms = sm_count();
+  const int blocks = ceil_div(max_prefix, kKeys) + ceil_div(max_nodes, kTreeKeys);
+  long s = 1;
+  if (items > 0 && items < sms) {
+    s = sms / items;
+  } else if (items > 0) {
+    long best = -1;
+    for (long c = 1; c <= 8; ++c) {
+      const long cost = ((items * c + sms - 1) / sms) * ((blocks + c - 1) / c + 2);
+      if (best < 0 || cost < best) {
+        best = cost;
+        s = c;
+      }
+    }
+    if (s > 1 && best * 100 > ((items + sms - 1) / sms) * (blocks + 2) * 92) s = 1;
+  }
+  if (s > blocks) s = blocks;
+  if (s > kMaxSplits) s = kMaxSplits;
+  return s < 1 ? 1 : (int)s;
+}
+
+struct Ws {
+  size_t o, total;
+};
+static Ws ws_of(long tiles, int splits) {
+  Ws w;
+  w.o = align_up(sizeof(float) * tiles * splits * kRows, 256);
+  w.total = w.o + sizeof(float) * tiles * splits * kRows * kD;
+  return w;
+}
+
+}  // namespace kv8p
+
+size_t attn_kv8p_ws_bytes(int batch, int max_nodes, int hq, int hkv, int max_prefix) {
+  const int s = kv8p::splits_of(batch, max_nodes, hq, hkv, max_prefix);
+  if (s <= 1) return 0;
+  return kv8p::ws_of((long)batch * hkv * kv8p::tiles_of(max_nodes, kv8p::kRows / (hq / hkv)), s).total;
+}
 
 int launch_attn_kv8p(const void* q, const uint8_t* k_pool, const uint8_t* v_pool, const float* kv_scale, int num_pages,
                      const int32_t* page_table, int max_pages, const int32_t* prefix_len, int max_prefix,
                      const void* k_tree, const void* v_tree, const uint64_t* mask, const int32_t* qo, int batch,
                      int total_nodes, int max_nodes, int hq, int hkv, float sm_scale, void* out, float* lse, void* ws,
                      int32_t* status, cudaStream_t stream) {
-  (void)max_prefix;
-  (void)ws;
-  const Kv8pArgs p{static_cast<const __nv_bfloat16*>(q), k_pool, v_pool, reinterpret_cast<const float2*>(kv_scale),
-                   page_table, max_pages, num_pages, prefix_len, static_cast<const __nv_bfloat16*>(k_tree),
-                   static_cast<const __nv_bfloat16*>(v_tree), mask, (max_nodes + 63) >> 6, qo, batch, total_nodes, hq,
-                   hkv, sm_scale * kLog2e, static_cast<__nv_bfloat16*>(out), lse, status};
-  const long rows = (long)total_nodes * hq;
-  if (launch_pdl(attn_kv8p_kernel, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, stream, p) != cudaSuccess)
+  using namespace kv8p;
+  const int G = hq / hkv;
+  CUtensorMap tm_kp, tm_vp, tm_kt, tm_vt;
+  {
+    const cuuint64_t dims[3] = {(cuuint64_t)kD, (cuuint64_t)hkv, (cuuint64_t)total_nodes};
+    const cuuint64_t str[2] = {(cuuint64_t)kD * 2, (cuuint64_t)hkv * kD * 2};
+    const cuuint32_t box[3] = {64, 1, (cuuint32_t)kTreeKeys};
+    if (!encode_bf16(&tm_kt, k_tree, 3, dims, str, box)) return SPEC_ERR_CUDA;
+    if (!encode_bf16(&tm_vt, v_tree, 3, dims, str, box)) return SPEC_ERR_CUDA;
+  }
+  if (max_prefix > 0) {  // one 16-token x 128-code tile (2 KB) per (page, head), 128-byte rows
+    const cuuint64_t dims[4] = {(cuuint64_t)kD, 16, (cuuint64_t)hkv, (cuuint64_t)num_pages};
+    const cuuint64_t str[3] = {(cuuint64_t)kD, (cuuint64_t)16 * kD, (cuuint64_t)hkv * 16 * kD};
+    const cuuint32_t box[4] = {(cuuint32_t)kD, 16, 1, 1};
+    if (!encode_tiled(&tm_kp, CU_TENSOR_MAP_DATA_TYPE_UINT8, k_pool, 4, dims, str, box)) return SPEC_ERR_CUDA;
+    if (!encode_tiled(&tm_vp, CU_TENSOR_MAP_DATA_TYPE_UINT8, v_pool, 4, dims, str, box)) return SPEC_ERR_CUDA;
+  } else {  // no prefix anywhere: the pool's maps are not used
+    tm_kp = tm_kt;
+    tm_vp = tm_vt;
+  }
+  static PerDevice smem_set;
+  if (per_device(smem_set, [](int) {
+        return cudaFuncSetAttribute(attn_kv8p_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) ==
+                       cudaSuccess
+                   ? 1
+                   : 0;
+      }) == 0)
     return SPEC_ERR_CUDA;
+  Params prm;
+  prm.q = static_cast<const __nv_bfloat16*>(q);
+  prm.kv_scale = reinterpret_cast<const float2*>(kv_scale);
+  prm.page_table = page_table;
+  prm.max_pages = max_pages;
+  prm.num_pages = num_pages;
+  prm.max_len = max_prefix;  // (the caller's rows hold it: checked on the host)
+  prm.prefix_len = prefix_len;
+  prm.mask = mask;
+  prm.mask_words = (max_nodes + 63) >> 6;
+  prm.qo = qo;
+  prm.hq = hq;
+  prm.hkv = hkv;
+  prm.G = G;
+  prm.npt = kRows / G;
+  prm.splits = splits_of(batch, max_nodes, hq, hkv, max_prefix);
+  prm.mtiles = tiles_of(max_nodes, prm.npt);
+  prm.scale_log2 = sm_scale * kLog2e;
+  prm.out = static_cast<__nv_bfloat16*>(out);
+  prm.lse = lse;
+  const long tiles = (long)batch * hkv * prm.mtiles;
+  const Ws w = ws_of(tiles, prm.splits);
+  uint8_t* wb = static_cast<uint8_t*>(ws);
+  prm.part_lse = prm.splits > 1 ? reinterpret_cast<float*>(wb) : nullptr;
+  prm.part_o = prm.splits > 1 ? reinterpret_cast<float4*>(wb + w.o) : nullptr;
+  prm.status = status;
+  prm.early = early_reads() ? 1 : 0;
+  const dim3 grid(prm.splits, ceil_div(prm.mtiles, 2), batch * hkv);
+  if (launch_pdl(attn_kv8p_kernel, grid, dim3(kThreads), kSmem, stream, tm_kp, tm_vp, tm_kt, tm_vt, prm) != cudaSuccess)
+    return SPEC_ERR_CUDA;
+  if (prm.splits > 1) {
+    MergeParams mp{prm.part_o, prm.part_lse, qo, prefix_len, prm.max_len, prm.mask_words, prm.splits, prm.mtiles, hkv,
+                   hq, G, prm.npt, tiles, prm.out, lse};
+    const long threads = tiles * 32 * kRows;
+    const dim3 mg((unsigned)((threads + kMergeThreads - 1) / kMergeThreads)), mb(kMergeThreads);
+    const cudaError_t e = prm.splits <= 4    ? launch_pdl(attn_kv8p_merge_kernel<4>, mg, mb, 0, stream, mp)
+                          : prm.splits <= 8  ? launch_pdl(attn_kv8p_merge_kernel<8>, mg, mb, 0, stream, mp)
+                          : prm.splits <= 20 ? launch_pdl(attn_kv8p_merge_kernel<20>, mg, mb, 0, stream, mp)
+                                             : launch_pdl(attn_kv8p_merge_kernel<kMaxSplits>, mg, mb, 0, stream, mp);
+    if (e != cudaSuccess) return SPEC_ERR_CUDA;
+  }
   return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
 

@@ -53,10 +53,9 @@
 // serialization so it is resident before this grid ends, combines them by log-sum-exp.
 // Rounding the normalised partials to bf16 adds at most 2^-9 max|v| to the output error
 // (the merge is a convex combination of them).
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
 #include "attn_common.cuh"
+#include "tc_host.cuh"
+#include "tc_math.cuh"
 #include "tc_ptx.cuh"
 
 namespace specv {
@@ -72,7 +71,6 @@ constexpr int kCvtWarps = 4;                       // FP8 cache: code -> bf16 co
 constexpr int kF8Stages = 3;
 constexpr int kParMax = kMaxTreeNodes;             // nodes per tree (parent array staged in smem)
 constexpr float kRescaleThr = 8.0f;            // log2 units: P entries stay <= 2^8
-constexpr long long kWaitLimit = 4000000000LL;  // cycles (about 2 s) before a wait gives up
 
 constexpr uint32_t kQSlab = kTcRows * 128;                  // 16 KB: 128 rows x 64 bf16
 constexpr uint32_t kQTile = 2 * kQSlab;
@@ -134,23 +132,10 @@ struct TcBars {
 };
 static_assert(sizeof(TcBars) <= 256, "barrier block over its reserved bytes");
 
-// One lane waits, the whole warp gets the answer: keeps warp-collective tcgen05.ld/st
-// and __syncwarp on a converged warp even when a wait gives up.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
-  int ok = 0;
-  if ((threadIdx.x & 31) == 0) ok = tc::mbar_wait(bar, parity, abort, kWaitLimit) ? 1 : 0;
-  return __shfl_sync(0xffffffffu, ok, 0) != 0;
-}
-
 // the 128 softmax threads of one tile (barrier 1 + tile; 0 is __syncthreads)
 __device__ __forceinline__ void tile_bar_sync(int tile) {
   if (tile == 0) asm volatile("bar.sync 1, 128;" ::: "memory");
   else asm volatile("bar.sync 2, 128;" ::: "memory");
-}
-
-__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
 }
 
 // Four E4M3 codes (byte i = element i) -> four bf16 (lo: elements 0, 1; hi: 2, 3), exactly.
@@ -173,36 +158,6 @@ __device__ __forceinline__ void e4m3x4_to_bf16x4(uint32_t w, uint32_t& lo, uint3
   asm("prmt.b32 %0, %1, 0, 0xB3A2;" : "=r"(b) : "r"(w));  // [sgn b3, b3, sgn b2, b2]
   lo = e4m3x2_lanes_to_bf16x2(a);
   hi = e4m3x2_lanes_to_bf16x2(b);
-}
-
-// Two fp32 lanes per instruction (packed f32x2 on this architecture); each lane is the
-// scalar operation, rounded to nearest.
-__device__ __forceinline__ float2 ffma2(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("{ .reg .b64 ra, rb, rc, rd; mov.b64 ra, {%2, %3}; mov.b64 rb, {%4, %5}; mov.b64 rc, {%6, %7};"
-      " fma.rn.f32x2 rd, ra, rb, rc; mov.b64 {%0, %1}, rd; }"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-  return d;
-}
-__device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
-  float2 d;
-  asm("{ .reg .b64 ra, rb, rd; mov.b64 ra, {%2, %3}; mov.b64 rb, {%4, %5}; add.rn.f32x2 rd, ra, rb;"
-      " mov.b64 {%0, %1}, rd; }"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
-}
-__device__ __forceinline__ float fmax3(float a, float b, float c) {
-  float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
-
-__device__ __forceinline__ float ex2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
 }
 
 // Key split of a sequence, balanced to the 16-token page: the work units are the prefix
@@ -870,37 +825,6 @@ __global__ void __launch_bounds__(kMergeThreads) attn_tc_merge_kernel(const TcMe
 
 // ------------------------------------------------------------------------------ host
 
-// The driver's tensor-map encoder, looked up once per process (a thread-safe static; the
-// entry point is the same for every device). nullptr when there is no driver.
-static PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-  static const PFN_cuTensorMapEncodeTiled_v12000 fn = []() -> PFN_cuTensorMapEncodeTiled_v12000 {
-    void* ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-    return nullptr;
-  }();
-  return fn;
-}
-
-// Tensor map with 128-byte swizzle and zero fill out of bounds; dims/box innermost first.
-static bool encode_tiled(CUtensorMap* m, CUtensorMapDataType type, const void* ptr, int rank,
-                         const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box) {
-  auto enc = tensor_map_encoder();
-  if (enc == nullptr) return false;
-  cuuint32_t es[5] = {1, 1, 1, 1, 1};
-  return enc(m, type, rank, const_cast<void*>(ptr), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-static bool encode_bf16(CUtensorMap* m, const void* ptr, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
-                        const cuuint32_t* box) {
-  return encode_tiled(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, ptr, rank, dims, strides, box);
-}
-
 // The shapes the tensor-core kernel serves (every bf16 call with d = 128 must be one of
 // them: such a call never runs on the CUDA-core kernel instead).
 bool attn_tc_shape(int dtype, int hq, int hkv, int d, int page_size, int max_nodes) {
@@ -912,15 +836,6 @@ bool attn_tc_shape(int dtype, int hq, int hkv, int d, int page_size, int max_nod
 // The driver entry point that encodes tensor maps was found (false on a host without a
 // CUDA driver): a tensor-core call without it fails with SPEC_ERR_CUDA.
 bool attn_tc_ready() { return tensor_map_encoder() != nullptr; }
-
-static int sm_count() {
-  static PerDevice cache;
-  const int n = per_device(cache, [](int dev) {
-    int v = 0;
-    return cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess && v > 0 ? v : 0;
-  });
-  return n > 0 ? n : 152;  // no device visible (sizing on a build machine): the GB300 count
-}
 
 static int tc_mtiles(int max_nodes, int G) { return ceil_div(max_nodes * G, kTcRows); }
 
