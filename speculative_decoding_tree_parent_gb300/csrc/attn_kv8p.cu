@@ -23,15 +23,15 @@
 // A CTA = (key split, pair of row tiles, sequence x KV head). A row tile is 128 rows: 128 / G
 // nodes (rounded down) of G heads each. K/V come in blocks: first the split's tree blocks (64
 // nodes, bf16), then its prefix blocks (128 keys, 8 pages, TMA page by page). Two slots work
-// side by side, each with its S (128 columns) and O (128) in TMEM, its MMA-issuing warp and
-// four softmax warps, one row per thread:
+// side by side, each with its S (128 columns) and O (128) in TMEM and four softmax warps, one
+// row per thread:
 //   - two row tiles: each slot has a tile, both take every block;
 //   - one (few nodes, or a single token): both slots hold its rows and take the blocks in
 //     turn; their sums are joined in shared memory at the end.
 // Within a slot S, softmax and PV of a block follow each other (P overwrites S); the other
 // slot's products fill the tensor cores meanwhile.
-// Warps (512 threads): 0 TMA producer, 1 and 2 MMA issuers (1 also allocates TMEM), 4-7 and
-// 8-11 softmax of slots 0 and 1, 12-15 V's converters. Every wait is bounded.
+// Warps (512 threads): 0 and 3 TMA producers, 1 and 2 MMA issuers (1 also allocates TMEM), 4-7
+// and 8-11 softmax of slots 0 and 1, 12-15 V's converters. Every wait is bounded.
 // Splits write O / l in fp32 and the log2-sum-exp, joined by a second kernel.
 #include "attn_common.cuh"
 #include "tc_host.cuh"
@@ -94,8 +94,9 @@ struct Params {
 struct Bars {
   uint64_t q16[2], q8[2];                     // a slot's q in bf16 / as two E4M3 terms
   uint64_t k_full[kStK], k_empty[kStK], c_full[kStC], c_empty[kStC], v_full[kStV], v_empty[kStV];
-  uint64_t s_full[2], p_full[2], o_full[2];
+  uint64_t s_full[2], p_full[2][2], o_full[2];  // p_full: P's first and second half
   uint64_t sc_full[kScales];
+  uint64_t go;                                // slot 0 has its first P
   uint64_t bad[kMaxTreeBlocks];  // tree nodes whose V row holds an infinity or NaN
   uint32_t tmem;
   int abort;
@@ -138,12 +139,42 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return d;
 }
 
+// The whole warp waits together. (One lane waiting for the others, with its answer shuffled to
+// them, cost about 1000 cycles a wait to bring the warp back together.)
+__device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, volatile int* abort) {
+  return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, abort, kWaitLimit));
+}
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(e));
+  return e != 0;
+}
+
+// One arrival for a warp whose lanes have all done their part.
+__device__ __forceinline__ void warp_arrive(uint32_t bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) tc::mbar_arrive(bar);
+}
+
+// Registers: 512 threads start with 128 each. The softmax warps (two warpgroups) take 192 to
+// hold a row's 128 scores at once; the other two warpgroups keep 64: 256 * (192 + 64) = 512 * 128.
+__device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 192;"); }
+__device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 64;"); }
+
+// All threads, from their own roles' code.
+__device__ __forceinline__ void cta_sync() { asm volatile("bar.sync 2, 512;" ::: "memory"); }
+
 // 16-byte chunk c of row r of a 128-byte-row slab, in the 128-byte swizzle
 __device__ __forceinline__ uint32_t swz(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
 
 // A row of q as hi and lo E4M3 codes, in place of its bf16 halves; returns the factor that the
 // codes have to be multiplied by. (A row with an infinity or NaN gets a NaN code.)
-__device__ __forceinline__ float split_row(uint8_t* q, int r, const uint4* w) {
+__device__ __forceinline__ float split_row(uint8_t* q, int r) {
+  uint4 w[16];
+#pragma unroll
+  for (int k = 0; k < 16; ++k) w[k] = *reinterpret_cast<const uint4*>(q + (k >> 3) * kSlab + swz(r, k & 7));
   uint32_t top = 0;
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
@@ -199,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (!p.early) pdl_wait();
   const int b = bg / p.hkv, g = bg - b * p.hkv;
   const int base = __ldg(p.qo + b), N = __ldg(p.qo + b + 1) - base, P = __ldg(p.prefix_len + b);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // (warp: uniform)
   const int node0 = 2 * pair * p.npt;
   if (node0 >= N) return;
   if (N > p.mask_words * 64 || P < 0 || P > p.max_len) {
@@ -237,12 +268,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) {
     if (lane == 0) {
       for (int t = 0; t < 2; ++t) {
-        tc::mbar_init(bar(&bars.q16[t]), 128);
-        tc::mbar_init(bar(&bars.q8[t]), 128);
+        tc::mbar_init(bar(&bars.q16[t]), 4);
+        tc::mbar_init(bar(&bars.q8[t]), 4);
         tc::mbar_init(bar(&bars.s_full[t]), 1);
-        tc::mbar_init(bar(&bars.p_full[t]), 128);
+        tc::mbar_init(bar(&bars.p_full[t][0]), 4);  // one arrival per softmax warp
+        tc::mbar_init(bar(&bars.p_full[t][1]), 4);
         tc::mbar_init(bar(&bars.o_full[t]), 1);
       }
+      tc::mbar_init(bar(&bars.go), 4);
       const int users = two ? 2 : 1;
       for (int s = 0; s < kStK; ++s) {
         tc::mbar_init(bar(&bars.k_full[s]), 1);
@@ -273,41 +306,45 @@ __global__ void __launch_bounds__(kThreads, 1)
   float m = -INFINITY, l = 0.f;  // softmax threads: running maximum and sum
   bool ok = true;
 
-  if (warp == 0) {
-    // ------------------------------------------------------------------ TMA producer
-    // Page ids of four blocks at a time, one per lane, a batch ahead; then their scales.
+  if (warp < kSoft0) regs_down();  // (by the whole warpgroup at once)
+  if (warp == 0 || warp == 3) {
+    // ------------------------------------------------------------------ TMA producers
+    // Warp 0 loads K and the pages' scales, warp 3 V's codes (one warp issuing all 16 copies of
+    // a block was the slowest of its parts). Page ids of four blocks at a time, one per lane,
+    // a batch ahead of their use; an id is checked when its batch comes up.
+    const bool isv = warp == 3;
+    constexpr int kSt = kStK;
+    static_assert(kStK == kStC, "one ring length for both producers");
+    uint64_t* full = isv ? bars.c_full : bars.k_full;
+    uint64_t* empty = isv ? bars.c_empty : bars.k_empty;
+    const uint32_t ring = sb + (isv ? kOffC : kOffK);
+    const CUtensorMap* tm_tree = isv ? &tm_vt : &tm_kt;
+    const CUtensorMap* tm_pool = isv ? &tm_vp : &tm_kp;
     auto ids_of = [&](int k) -> int {
       const int lp = sp.pg_lo + 32 * k + lane;
-      int page = p.num_pages;  // out of range: TMA reads zeros
-      if (lp < sp.pg_hi) {
-        const int x = __ldg(p.page_table + (size_t)b * p.max_pages + lp);
-        if (x >= 0 && x < p.num_pages) page = x;
-        else report(p.status, SPEC_ERR_PAGE);
-      }
-      return page;
+      return lp < sp.pg_hi ? __ldg(p.page_table + (size_t)b * p.max_pages + lp) : p.num_pages;
+    };
+    auto checked = [&](int page, int k) -> int {
+      if (page >= 0 && page < p.num_pages) return page;
+      if (!isv && sp.pg_lo + 32 * k + lane < sp.pg_hi) report(p.status, SPEC_ERR_PAGE);
+      return p.num_pages;  // out of range: TMA reads zeros
     };
     auto scale_of = [&](int page) {
-      return page < p.num_pages ? __ldg(p.kv_scale + (size_t)page * p.hkv + g) : make_float2(1.f, 1.f);
+      return !isv && page < p.num_pages ? __ldg(p.kv_scale + (size_t)page * p.hkv + g) : make_float2(1.f, 1.f);
     };
-    int ids = ids_of(0), ids_next = ids_of(1);
+    int ids = checked(ids_of(0), 0), ids_next = ids_of(1);
     float2 sc = scale_of(ids), sc_next = make_float2(1.f, 1.f);
     int done = 0;  // blocks whose copies were issued
     for (int i = 0; i < nb; ++i) {
-      const int sk = i % kStK, sc_ = i % kStC;
-      if (i >= kStK && !warp_wait(bar(&bars.k_empty[sk]), ((i / kStK) & 1) ^ 1, abort)) break;
-      if (i >= kStC && !warp_wait(bar(&bars.c_empty[sc_]), ((i / kStC) & 1) ^ 1, abort)) break;
-      const uint32_t kdst = sb + kOffK + sk * kSlab, cdst = sb + kOffC + sc_ * kSlab;
-      if (lane == 0) {
-        tc::mbar_arrive_expect_tx(bar(&bars.k_full[sk]), kSlab);
-        tc::mbar_arrive_expect_tx(bar(&bars.c_full[sc_]), kSlab);
-      }
+      const int st = i % kSt;
+      if (i >= kSt && !wait_all(bar(&empty[st]), ((i / kSt) & 1) ^ 1, abort)) break;
+      const uint32_t dst = ring + st * kSlab;
+      if (lane == 0) tc::mbar_arrive_expect_tx(bar(&full[st]), kSlab);
       __syncwarp();
       if (i < nt) {
-        if (lane < 4) {  // K and V, two 64-column halves each
-          const int half = lane & 1, row0 = base + (sp.tb_lo + i) * kTreeKeys;
-          if (lane < 2) tc::tma_load_3d(kdst + half * kTreeSlab, &tm_kt, bar(&bars.k_full[sk]), half * 64, g, row0);
-          else tc::tma_load_3d(cdst + half * kTreeSlab, &tm_vt, bar(&bars.c_full[sc_]), half * 64, g, row0);
-        }
+        if (lane < 2)  // two 64-column halves
+          tc::tma_load_3d(dst + lane * kTreeSlab, tm_tree, bar(&full[st]), lane * 64, g,
+                          base + (sp.tb_lo + i) * kTreeKeys);
       } else {
         const int j = i - nt;
         if (j > 0 && (j & 3) == 0) {
@@ -317,93 +354,123 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const int from = (j & 3) * kPages + (lane & 7);
         const int page = __shfl_sync(0xffffffffu, ids, from);
-        if (lane < kPages) tc::tma_load_4d(kdst + lane * 2048, &tm_kp, bar(&bars.k_full[sk]), 0, 0, g, page);
-        else if (lane < 2 * kPages)
-          tc::tma_load_4d(cdst + (lane - kPages) * 2048, &tm_vp, bar(&bars.c_full[sc_]), 0, 0, g, page);
-        if ((j & 3) == 1) sc_next = scale_of(ids_next);
-        const float ks = page_scale(__shfl_sync(0xffffffffu, sc.x, from));
-        const float vs = page_scale(__shfl_sync(0xffffffffu, sc.y, from));
-        if (lane < kPages)
-          *reinterpret_cast<float4*>(smem + kOffScale + ((j % kScales) * kPages + lane) * 16) =
-              make_float4(ks, log2f(vs), 1.f / vs, 0.f);
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(bar(&bars.sc_full[j % kScales]));
+        if (lane < kPages) tc::tma_load_4d(dst + lane * 2048, tm_pool, bar(&full[st]), 0, 0, g, page);
+        if ((j & 3) == 2) {
+          ids_next = checked(ids_next, (j >> 2) + 1);
+          sc_next = scale_of(ids_next);
+        }
+        if (!isv) {
+          const float ks = page_scale(__shfl_sync(0xffffffffu, sc.x, from));
+          const float vs = page_scale(__shfl_sync(0xffffffffu, sc.y, from));
+          if (lane < kPages)
+            *reinterpret_cast<float4*>(smem + kOffScale + ((j % kScales) * kPages + lane) * 16) =
+                make_float4(ks, log2f(vs), 1.f / vs, 0.f);
+          warp_arrive(bar(&bars.sc_full[j % kScales]));
+        }
       }
       done = i + 1;
     }
     if (done < nb && lane == 0) {  // given up: leave no copy in flight
       report(p.status, SPEC_ERR_TIMEOUT);
       int zero = 0;
-      for (int i = max(0, done - kStK); i < done; ++i)
-        tc::mbar_wait(bar(&bars.k_full[i % kStK]), (i / kStK) & 1, &zero, kWaitLimit);
-      zero = 0;
-      for (int i = max(0, done - kStC); i < done; ++i)
-        tc::mbar_wait(bar(&bars.c_full[i % kStC]), (i / kStC) & 1, &zero, kWaitLimit);
+      for (int i = max(0, done - kSt); i < done; ++i)
+        tc::mbar_wait(bar(&full[i % kSt]), (i / kSt) & 1, &zero, kWaitLimit);
     }
     __syncwarp();
   } else if (warp == 1 || warp == 2) {
     // ------------------------------------------------------------------ MMA issuers
+    // One warp per slot. Slot 1 starts when slot 0 has its first P, so that the slots run about
+    // half a period apart, one's softmax under the other's products.
     const int t = warp - 1;
-    if (lane == 0) {
-      const uint32_t qb = sb + kOffQ + t * kQTile, ts = tmem + t * 256, to = ts + 128;
-      bool issued = false, any = false, q8 = false, q16 = false;
-      for (int i = two ? 0 : t; ok && i < nb; i += step) {
-        const int sk = i % kStK, sv = i % kStV;
-        const uint32_t kb = sb + kOffK + sk * kSlab, vb = sb + kOffV + sv * 2 * kSlab;
-        const bool tree = i < nt;
-        if (tree && !q16) ok = tc::mbar_wait(bar(&bars.q16[t]), 0, abort, kWaitLimit), q16 = true;
-        if (!tree && !q8) ok = tc::mbar_wait(bar(&bars.q8[t]), 0, abort, kWaitLimit), q8 = true;
-        ok = ok && tc::mbar_wait(bar(&bars.k_full[sk]), (i / kStK) & 1, abort, kWaitLimit);
-        if (!ok) break;
-        tc::fence_after_sync();
-        if (tree) {
-#pragma unroll
+    const bool leader = elect_one();
+    const int cnt = two ? nb : (nb + 1 - t) / 2;
+    bool q8 = false, q16 = false;
+    // the slot's n-th block
+    auto block = [&](int n) { return two ? n : 2 * n + t; };
+    // what QK of the n-th block needs
+    auto wait_qk = [&](int n) {
+      const int i = block(n), sk = i % kStK;
+      if (i < nt && !q16) ok = ok && wait_all(bar(&bars.q16[t]), 0, abort), q16 = true;
+      if (i >= nt && !q8) ok = ok && wait_all(bar(&bars.q8[t]), 0, abort), q8 = true;
+      ok = ok && wait_all(bar(&bars.k_full[sk]), (i / kStK) & 1, abort);
+    };
+    auto qk = [&](int n) {
+      const int i = block(n), sk = i % kStK;
+      const uint32_t ts = tmem + t * 256;
+      const uint64_t qd = tc::sdesc_sw128(sb + kOffQ + t * kQTile, 16, 1024);
+      const uint64_t kd = tc::sdesc_sw128(sb + kOffK + sk * kSlab, 16, 1024);
+      if (leader) {
+        if (i < nt) {
+#pragma unroll 1
           for (int k = 0; k < 8; ++k)
-            tc::mma_bf16(ts, tc::sdesc_sw128(qb + (k >> 2) * kSlab + (k & 3) * 32, 16, 1024),
-                         tc::sdesc_sw128(kb + (k >> 2) * kTreeSlab + (k & 3) * 32, 16, 1024), kIdTreeQK, k > 0);
+            tc::mma_bf16(ts, qd + (((k >> 2) * kSlab + (k & 3) * 32) >> 4),
+                         kd + (((k >> 2) * kTreeSlab + (k & 3) * 32) >> 4), kIdTreeQK, k > 0);
         } else {
 #pragma unroll
           for (int k = 0; k < 8; ++k)  // hi, then lo
-            tc::mma_f8(ts, tc::sdesc_sw128(qb + (k >> 2) * kSlab + (k & 3) * 32, 16, 1024),
-                       tc::sdesc_sw128(kb + (k & 3) * 32, 16, 1024), kIdQK, k > 0);
+            tc::mma_f8(ts, qd + (((k >> 2) * kSlab + (k & 3) * 32) >> 4), kd + (((k & 3) * 32) >> 4), kIdQK, k > 0);
         }
-        issued = true;
         tc::mma_commit(bar(&bars.s_full[t]));
         tc::mma_commit(bar(&bars.k_empty[sk]));
-        const int n = two ? i : i >> 1;  // this slot's blocks so far
-        ok = tc::mbar_wait(bar(&bars.v_full[sv]), (i / kStV) & 1, abort, kWaitLimit) &&
-             tc::mbar_wait(bar(&bars.p_full[t]), n & 1, abort, kWaitLimit);
-        if (!ok) break;
-        tc::fence_after_sync();
-        if (tree) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k)  // P's two bf16 terms, four steps of 16 nodes each
-            tc::mma_bf16_ts(to, ts + 8 * k, tc::sdesc_sw128(vb + (k & 3) * 2048, kSlab, 1024), kIdTreePV,
-                            any || k > 0);
+      }
+      __syncwarp();
+    };
+    // half h of PV: P's first or second 64 keys; of a tree block, P's first or second bf16 term
+    auto pv = [&](int n, int h) {
+      const int i = block(n), sv = i % kStV;
+      const uint32_t pa = tmem + t * 256 + 32 * h, to = tmem + t * 256 + 128;
+      const uint64_t vd = tc::sdesc_sw128(sb + kOffV + sv * 2 * kSlab, kSlab, 1024);
+      if (leader) {
+        if (i < nt) {
+#pragma unroll 1
+          for (int k = 0; k < 4; ++k)
+            tc::mma_bf16_ts(to, pa + 8 * k, vd + ((k * 2048) >> 4), kIdTreePV, n > 0 || h > 0 || k > 0);
         } else {
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            tc::mma_bf16_ts(to, ts + 8 * k, tc::sdesc_sw128(vb + k * 2048, kSlab, 1024), kIdPV, any || k > 0);
+          for (int k = 0; k < 4; ++k)
+            tc::mma_bf16_ts(to, pa + 8 * k, vd + (((4 * h + k) * 2048) >> 4), kIdPV, n > 0 || h > 0 || k > 0);
         }
-        any = true;
-        tc::mma_commit(bar(&bars.v_empty[sv]));
+        if (h == 1) tc::mma_commit(bar(&bars.v_empty[sv]));
       }
-      if (!ok) report(p.status, SPEC_ERR_TIMEOUT);
-      // every product issued has completed before O is read and TMEM released
-      if (issued) {
-        tc::mma_commit(bar(&bars.o_full[t]));
-        int zero = 0;
-        tc::mbar_wait(bar(&bars.o_full[t]), 0, &zero, kWaitLimit);
-      }
+      __syncwarp();
+    };
+    if (t == 1 && cnt > 2) ok = wait_all(bar(&bars.go), 0, abort);
+    if (cnt > 0) wait_qk(0);
+    if (cnt > 0 && ok) {
+      tc::fence_after_sync();
+      qk(0);
     }
+    for (int n = 0; ok && n < cnt; ++n) {
+      // PV as the halves of P arrive, then QK of the next block, whose operands have been
+      // waited for by then
+      const int i = block(n), sv = i % kStV;
+      const bool more = n + 1 < cnt;
+      ok = wait_all(bar(&bars.v_full[sv]), (i / kStV) & 1, abort) &&
+           wait_all(bar(&bars.p_full[t][0]), n & 1, abort);
+      if (!ok) break;
+      tc::fence_after_sync();
+      pv(n, 0);
+      if (more) wait_qk(n + 1);
+      ok = ok && wait_all(bar(&bars.p_full[t][1]), n & 1, abort);
+      if (!ok) break;
+      tc::fence_after_sync();
+      pv(n, 1);
+      if (more) qk(n + 1);
+    }
+    if (!ok && leader) report(p.status, SPEC_ERR_TIMEOUT);
+    // every product issued has completed before O is read and TMEM released
+    if (leader) tc::mma_commit(bar(&bars.o_full[t]));
+    int zero = 0;
+    tc::mbar_wait(bar(&bars.o_full[t]), 0, &zero, kWaitLimit);
     __syncwarp();
   } else if (warp >= kCvt) {
+    regs_down();
     // ------------------------------------------------------------------ V converters
     const int ct = threadIdx.x - kCvt * 32;
     for (int i = 0; i < nb; ++i) {
       const int sc_ = i % kStC, sv = i % kStV;
-      if (!warp_wait(bar(&bars.c_full[sc_]), (i / kStC) & 1, abort) ||
-          (i >= kStV && !warp_wait(bar(&bars.v_empty[sv]), ((i / kStV) & 1) ^ 1, abort))) {
+      if (!wait_all(bar(&bars.c_full[sc_]), (i / kStC) & 1, abort) ||
+          (i >= kStV && !wait_all(bar(&bars.v_empty[sv]), ((i / kStV) & 1) ^ 1, abort))) {
         if (lane == 0) report(p.status, SPEC_ERR_TIMEOUT);
         break;
       }
@@ -413,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // bf16 rows as they are, but for rows past the tree and elements that are not finite
         // (a weight of 0 times either would reach rows whose mask leaves the node out)
         const int tb = sp.tb_lo + i, nvalid = N - tb * kTreeKeys;
-#pragma unroll
+#pragma unroll 1
         for (int it = 0; it < 8; ++it) {
           const int id = it * 128 + ct, half = id >> 9, off = id & 511, r = off >> 3;
           uint4 w = *reinterpret_cast<const uint4*>(src + half * kTreeSlab + off * 16);
@@ -463,6 +530,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp >= kSoft0) {
+    regs_up();
     // ------------------------------------------------------------------ softmax
     const int i0 = two ? 0 : slot;
     const uint32_t ts = tmem + slot * 256 + ((uint32_t)((warp & 3) * 32) << 16), to = ts + 128;
@@ -472,26 +540,52 @@ __global__ void __launch_bounds__(kThreads, 1)
     float qf = 0.f;  // the factor of the row's codes
     uint64_t bits = 0ull;
     const uint64_t* mrow = p.mask + (size_t)(base + node) * p.mask_words;
+    const float scale_log2 = p.scale_log2;
+    bool coded = false;  // q's row stands as codes
     if (i0 < nb) {
-      uint4 w[16];
       const uint4* src = reinterpret_cast<const uint4*>(p.q + orow * kD);
+      uint4 w[16];
 #pragma unroll
       for (int k = 0; k < 16; ++k) w[k] = valid ? __ldg(src + k) : make_uint4(0, 0, 0, 0);
-      if (last_tree >= 0) {
 #pragma unroll
-        for (int k = 0; k < 16; ++k) *reinterpret_cast<uint4*>(q + (k >> 3) * kSlab + swz(row, k & 7)) = w[k];
+      for (int k = 0; k < 16; ++k) *reinterpret_cast<uint4*>(q + (k >> 3) * kSlab + swz(row, k & 7)) = w[k];
+      if (last_tree >= 0) {
         tc::fence_proxy_async_smem();
-        tc::mbar_arrive(bar(&bars.q16[slot]));
+        warp_arrive(bar(&bars.q16[slot]));
         pdl_wait();  // the mask may come from the kernel before
         if (valid) bits = __ldcg(mrow + sp.tb_lo + i0);
-      } else {
-        qf = split_row(q, row, w);
-        tc::fence_proxy_async_smem();
-        tc::mbar_arrive(bar(&bars.q8[slot]));
       }
     }
     for (int i = i0, n = 0; i < nb; i += step, ++n) {
-      if (!warp_wait(bar(&bars.s_full[slot]), n & 1, abort)) {
+      if (i >= nt && !coded) {
+        // (the slot's last tree block, if any, has its S: q's bf16 rows have been read)
+        qf = split_row(q, row);
+        coded = true;
+        tc::fence_proxy_async_smem();
+        warp_arrive(bar(&bars.q8[slot]));
+      }
+      // the block's page scales, as factors, exponents and weights of the row sum (they are
+      // there before S is)
+      float pf[kPages], pe[kPages], pw[kPages];
+      int nvalid = kKeys;
+      if (i >= nt) {
+        const int j = i - nt;
+        if (!wait_all(bar(&bars.sc_full[j % kScales]), (j / kScales) & 1, abort)) {
+          ok = false;
+          break;
+        }
+        const float4* scale = reinterpret_cast<const float4*>(smem + kOffScale) + (j % kScales) * kPages;
+#pragma unroll
+        for (int pp = 0; pp < kPages; ++pp) {
+          const float4 f = scale[pp];
+          // (kept above 0, so that a key past the prefix stays at -inf; a score is 0 there all the same)
+          pf[pp] = fmaxf(scale_log2 * qf * f.x, 1e-37f);
+          pe[pp] = f.y;
+          pw[pp] = f.z;
+        }
+        nvalid = min(P, sp.pg_hi * 16) - (sp.pg_lo + j * kPages) * 16;
+      }
+      if (!wait_all(bar(&bars.s_full[slot]), n & 1, abort)) {
         ok = false;
         break;
       }
@@ -529,7 +623,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           float mx = -INFINITY;
 #pragma unroll
           for (int c = 0; c < kTreeKeys; ++c) {
-            s[c] = ((see >> c) & 1ull) ? s[c] * p.scale_log2 : -INFINITY;
+            s[c] = ((see >> c) & 1ull) ? s[c] * scale_log2 : -INFINITY;
             mx = fmaxf(mx, s[c]);
           }
           raise(mx);
@@ -551,104 +645,78 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc::tmem_wait_st();
         }
         tc::fence_before_sync();
-        tc::mbar_arrive(bar(&bars.p_full[slot]));
-        if (i == last_tree && i + step < nb) {
-          // the tree's last S is complete, so q's bf16 rows have been read: codes in their place
-          uint4 w[16];
-#pragma unroll
-          for (int k = 0; k < 16; ++k) w[k] = *reinterpret_cast<const uint4*>(q + (k >> 3) * kSlab + swz(row, k & 7));
-          qf = split_row(q, row, w);
-          tc::fence_proxy_async_smem();
-          tc::mbar_arrive(bar(&bars.q8[slot]));
-        }
+        warp_arrive(bar(&bars.p_full[slot][0]));
+        warp_arrive(bar(&bars.p_full[slot][1]));
+        if (slot == 0 && n == 0) warp_arrive(bar(&bars.go));
         continue;
       }
-      const int j = i - nt;
-      if (!warp_wait(bar(&bars.sc_full[j % kScales]), (j / kScales) & 1, abort)) {
-        ok = false;
-        break;
-      }
       if (live) {
-        const float4* scale = reinterpret_cast<const float4*>(smem + kOffScale) + (j % kScales) * kPages;
-        const int nvalid = min(P, sp.pg_hi * 16) - (sp.pg_lo + j * kPages) * 16;
-        const float sc = p.scale_log2 * qf;
-        // (kept above 0, so that a key past the prefix stays at -inf; a score is 0 there all the same)
-        auto factor = [&](float ks) { return fmaxf(sc * ks, 1e-37f); };
-        float s[64];
-        // the largest x log2 e + log2 vs: columns 64-127, then 0-63 (which stay in registers)
-        float mx = -INFINITY;
+        float s[kKeys];
 #pragma unroll
-        for (int h = 1; h >= 0; --h) {
-          tc::tmem_ld32(ts + 64 * h, s);
-          tc::tmem_ld32(ts + 64 * h + 32, s + 32);
-          tc::tmem_wait_ld();
-          if (nvalid < kKeys) {
+        for (int h = 0; h < 4; ++h) tc::tmem_ld32(ts + 32 * h, s + 32 * h);
+        tc::tmem_wait_ld();
+        if (nvalid < kKeys) {
 #pragma unroll
-            for (int c = 0; c < 64; ++c) s[c] = 64 * h + c < nvalid ? s[c] : -INFINITY;
-          }
+          for (int c = 0; c < kKeys; ++c) s[c] = c < nvalid ? s[c] : -INFINITY;
+        }
+        float mx = -INFINITY;  // the largest x log2 e + log2 vs
 #pragma unroll
-          for (int g4 = 0; g4 < 4; ++g4) {
-            const float* v = s + 16 * g4;
-            float x = fmax3(v[0], v[1], v[2]);
+        for (int pp = 0; pp < kPages; ++pp) {
+          const float* v = s + 16 * pp;
+          float x = fmax3(v[0], v[1], v[2]);
 #pragma unroll
-            for (int c = 3; c < 15; c += 2) x = fmax3(x, v[c], v[c + 1]);
-            const float4 f = scale[4 * h + g4];
-            mx = fmaxf(mx, fmaf(fmaxf(x, v[15]), factor(f.x), f.y));
-          }
+          for (int c = 3; c < 15; c += 2) x = fmax3(x, v[c], v[c + 1]);
+          mx = fmaxf(mx, fmaf(fmaxf(x, v[15]), pf[pp], pe[pp]));
         }
         raise(mx);
         const float off = m == -INFINITY ? 0.f : kShift - m;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (h == 1) {
-            tc::tmem_ld32(ts + 64, s);
-            tc::tmem_ld32(ts + 96, s + 32);
-            tc::tmem_wait_ld();
-            if (nvalid < kKeys) {
+        for (int h = 0; h < 4; ++h) {
+          uint32_t pk[16];
 #pragma unroll
-              for (int c = 0; c < 64; ++c) s[c] = 64 + c < nvalid ? s[c] : -INFINITY;
-            }
-          }
-          uint32_t pk[32];
-#pragma unroll
-          for (int g4 = 0; g4 < 4; ++g4) {
-            const float4 f = scale[4 * h + g4];
-            const float2 f2 = make_float2(factor(f.x), factor(f.x)), o2 = make_float2(off + f.y, off + f.y);
+          for (int pp = 0; pp < 2; ++pp) {
+            const float ff = pf[2 * h + pp], oo = off + pe[2 * h + pp];
+            const float2 f2 = make_float2(ff, ff), o2 = make_float2(oo, oo);
             float2 r0 = make_float2(0.f, 0.f), r1 = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int c = 16 * g4; c < 16 * g4 + 16; c += 4) {
-              const float2 a = ffma2(make_float2(s[c], s[c + 1]), f2, o2);
-              const float2 d = ffma2(make_float2(s[c + 2], s[c + 3]), f2, o2);
+            for (int k = 0; k < 16; k += 4) {
+              const float* v = s + 32 * h + 16 * pp + k;
+              const float2 a = ffma2(make_float2(v[0], v[1]), f2, o2);
+              const float2 d = ffma2(make_float2(v[2], v[3]), f2, o2);
               const float2 ea = make_float2(ex2_approx(a.x), ex2_approx(a.y));
               const float2 ed = make_float2(ex2_approx(d.x), ex2_approx(d.y));
               r0 = fadd2(r0, ea);
               r1 = fadd2(r1, ed);
-              pk[c >> 1] = pack_f16x2(ea.x, ea.y);
-              pk[(c >> 1) + 1] = pack_f16x2(ed.x, ed.y);
+              pk[8 * pp + (k >> 1)] = pack_f16x2(ea.x, ea.y);
+              pk[8 * pp + (k >> 1) + 1] = pack_f16x2(ed.x, ed.y);
             }
-            l = fmaf((r0.x + r0.y) + (r1.x + r1.y), f.z, l);
+            l = fmaf((r0.x + r0.y) + (r1.x + r1.y), pw[2 * h + pp], l);
           }
-          tc::tmem_st32_u(ts + 32 * h, pk);
+          tc::tmem_st16_u(ts + 16 * h, pk);
+          if (h == 1) {  // PV of the first 64 keys may start
+            tc::tmem_wait_st();
+            tc::fence_before_sync();
+            warp_arrive(bar(&bars.p_full[slot][0]));
+          }
         }
         tc::tmem_wait_st();
+      } else {
+        warp_arrive(bar(&bars.p_full[slot][0]));
       }
       tc::fence_before_sync();
-      tc::mbar_arrive(bar(&bars.p_full[slot]));
+      warp_arrive(bar(&bars.p_full[slot][1]));
+      if (slot == 0 && n == 0) warp_arrive(bar(&bars.go));
     }
     if (!ok && lane == 0) report(p.status, SPEC_ERR_TIMEOUT);
-  }
 
-  // ---------------------------------------------------------------------- epilogue
-  tc::fence_before_sync();
-  __syncthreads();  // every product is complete, every copy has landed
-  tc::fence_after_sync();
-  if (warp >= kSoft0 && warp < kCvt) {
-    const uint32_t to = tmem + slot * 256 + 128 + ((uint32_t)((warp & 3) * 32) << 16);
+    // -------------------------------------------------------------------- epilogue
+    tc::fence_before_sync();
+    cta_sync();  // every product is complete, every copy has landed
+    tc::fence_after_sync();
     // one tile: slot 1 hands its sums to slot 0 through shared memory (chunk of 4 columns,
     // then row: consecutive lanes, consecutive 16 bytes)
     float4* join = reinterpret_cast<float4*>(smem + kOffQ);
     float2* join_ml = reinterpret_cast<float2*>(smem + kOffK);
-    const bool live = __any_sync(0xffffffffu, valid);
     if (!two) {
       if (slot == 1 && live) {
         if (valid) join_ml[row] = make_float2(m, l);
@@ -727,6 +795,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         else if (p.lse != nullptr) p.lse[orow] = lse2 * kLn2;
       }
     }
+  }
+  if (warp < kSoft0 || warp >= kCvt) {
+    tc::fence_before_sync();
+    cta_sync();
   }
   tc::fence_before_sync();
   __syncthreads();
