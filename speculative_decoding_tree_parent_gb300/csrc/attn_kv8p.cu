@@ -20,18 +20,19 @@
 // x log2 e + log2 vs (P stays below 2^15, and full precision reaches 2^25 below the largest);
 // the row sum adds P_j / vs_j per page.
 //
-// A CTA = (key split, pair of row tiles, sequence x KV head). A row tile is 128 rows: 128 / G
-// nodes (rounded down) of G heads each. K/V come in blocks: first the split's tree blocks (64
-// nodes, bf16), then its prefix blocks (128 keys, 8 pages, TMA page by page). Two slots work
-// side by side, each with its S (128 columns) and O (128) in TMEM and four softmax warps, one
-// row per thread:
-//   - two row tiles: each slot has a tile, both take every block;
-//   - one (few nodes, or a single token): both slots hold its rows and take the blocks in
-//     turn; their sums are joined in shared memory at the end.
-// Within a slot S, softmax and PV of a block follow each other (P overwrites S); the other
-// slot's products fill the tensor cores meanwhile.
-// Warps (512 threads): 0 and 3 TMA producers, 1 and 2 MMA issuers (1 also allocates TMEM), 4-7
-// and 8-11 softmax of slots 0 and 1, 12-15 V's converters. Every wait is bounded.
+// A CTA = (key split, row tile, sequence x KV head). A row tile is 128 rows: 128 / G nodes
+// (rounded down) of G heads each. K/V come in blocks: first the split's tree blocks (64 nodes,
+// bf16), then its prefix blocks (128 keys, 8 pages, TMA page by page). Two slots work side by
+// side on the same rows, each with its own S (64 keys), P and O in TMEM, its MMA-issuing warp
+// and four softmax warps (one row per thread): slot 0 takes the tree and the first 64 keys of
+// every prefix block, slot 1 the other 64; their sums are joined at the end.
+//   - q stands in TMEM too (bf16 rows for the tree, codes for the prefix: 64 columns either
+//     way), the A operand of QK: read from shared memory for every product it took as much of
+//     that memory's bandwidth as K, and shared memory is what the other warps wait for.
+//   - S and P lie apart, so QK of a slot's next step runs as soon as the softmax has its scores
+//     in registers, under the exponentials; PV follows when P is there.
+// Warps (512 threads): 0 and 3 TMA producers (K, V), 1 and 2 MMA issuers (1 also allocates
+// TMEM), 4-7 and 8-11 softmax of slots 0 and 1, 12-15 V's converters. Every wait is bounded.
 // Splits write O / l in fp32 and the log2-sum-exp, joined by a second kernel.
 #include "attn_common.cuh"
 #include "tc_host.cuh"
@@ -47,23 +48,25 @@ constexpr int kTreeKeys = 64;   // nodes of a tree block
 constexpr int kD = 128;
 constexpr int kThreads = 512;
 constexpr int kSoft0 = 4, kCvt = 12;         // first softmax warp, first converter warp
-constexpr int kStK = 3, kStC = 3, kStV = 2;  // stages: K, V codes, V in 16 bits
+constexpr int kStep = 64;                    // keys of a slot's step: half a prefix block, or a tree block
+constexpr int kStK = 4, kStC = 3, kStV = 3;  // stages: K, V codes, V in 16 bits
 constexpr uint32_t kSlab = 128 * 128;        // 128 rows of 128 bytes
 constexpr uint32_t kTreeSlab = kTreeKeys * 128;
-constexpr uint32_t kQTile = 2 * kSlab;       // bf16 halves, later the hi and lo codes
-constexpr uint32_t kOffQ = 0;
-constexpr uint32_t kOffK = kOffQ + 2 * kQTile;
+constexpr uint32_t kOffK = 0;
 constexpr uint32_t kOffC = kOffK + kStK * kSlab;
 constexpr uint32_t kOffV = kOffC + kStC * kSlab;
 constexpr uint32_t kOffBar = kOffV + kStV * 2 * kSlab;
 constexpr int kScales = 8;                   // blocks whose page scales are kept
 constexpr uint32_t kOffScale = kOffBar + 512;
-constexpr uint32_t kSmem = kOffScale + kScales * kPages * 16 + 1024;  // + alignment slack
+constexpr uint32_t kOffJoin = kOffScale + kScales * kPages * 16;      // float2 [slot][row]: maximum, sum
+constexpr uint32_t kSmem = kOffJoin + 2 * kRows * 8 + 1024;           // + alignment slack
 static_assert(kSmem <= 232448, "shared memory over the per-CTA limit");
-constexpr uint32_t kTmemCols = 512;          // slot t: S at 256 t, O at 256 t + 128
+// TMEM columns: O of slot t at 128 t, q, then S and P of slot t
+constexpr uint32_t kTmemCols = 512, kColQ = 256, kColS = 320, kSlotCols = 96;  // P: 64 columns after S
+constexpr int kLptMax = 1024;                // sequences that are ranked by length
 constexpr float kShift = 11.f;               // log2 of the largest P when M is set
 constexpr float kGrow = 4.f;                 // growth of the largest score that M may lag behind
-constexpr uint32_t kIdQK = tc::idesc_e4m3(kRows, kKeys);
+constexpr uint32_t kIdQK = tc::idesc_e4m3(kRows, kStep);
 constexpr uint32_t kIdPV = tc::idesc_f16(kRows, kD, 1);
 constexpr uint32_t kIdTreeQK = tc::idesc_bf16(kRows, kTreeKeys, 0);
 constexpr uint32_t kIdTreePV = tc::idesc_bf16(kRows, kD, 1);
@@ -81,7 +84,7 @@ struct Params {
   int mask_words;
   const int32_t* qo;
   int hq, hkv, G, npt;  // npt: nodes of a row tile
-  int splits, mtiles;
+  int splits, mtiles, batch, lpt;
   float scale_log2;
   __nv_bfloat16* out;
   float* lse;
@@ -92,11 +95,10 @@ struct Params {
 };
 
 struct Bars {
-  uint64_t q16[2], q8[2];                     // a slot's q in bf16 / as two E4M3 terms
+  uint64_t q16, q8;                           // q in bf16 / as two E4M3 terms
   uint64_t k_full[kStK], k_empty[kStK], c_full[kStC], c_empty[kStC], v_full[kStV], v_empty[kStV];
-  uint64_t s_full[2], p_full[2][2], o_full[2];  // p_full: P's first and second half
+  uint64_t s_full[2], s_free[2], p_full[2], pv_done[2], o_full[2];  // [slot], one phase a step
   uint64_t sc_full[kScales];
-  uint64_t go;                                // slot 0 has its first P
   uint64_t bad[kMaxTreeBlocks];  // tree nodes whose V row holds an infinity or NaN
   uint32_t tmem;
   int abort;
@@ -158,57 +160,77 @@ __device__ __forceinline__ void warp_arrive(uint32_t bar) {
   if ((threadIdx.x & 31) == 0) tc::mbar_arrive(bar);
 }
 
-// Registers: 512 threads start with 128 each. The softmax warps (two warpgroups) take 192 to
-// hold a row's 128 scores at once; the other two warpgroups keep 64: 256 * (192 + 64) = 512 * 128.
-__device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 192;"); }
-__device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 64;"); }
+// Registers: 512 threads start with 128 each. The softmax warps (two warpgroups) take 168, the
+// other two warpgroups keep 88: 256 * (168 + 88) = 512 * 128.
+constexpr int kLaunchRegs = 128;
+__device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 168;"); }
+__device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 88;"); }
 
 // All threads, from their own roles' code.
-__device__ __forceinline__ void cta_sync() { asm volatile("bar.sync 2, 512;" ::: "memory"); }
+__device__ __forceinline__ void cta_sync() { asm volatile("bar.sync 0;" ::: "memory"); }
+
+// The softmax warps of both slots.
+__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
 // 16-byte chunk c of row r of a 128-byte-row slab, in the 128-byte swizzle
 __device__ __forceinline__ uint32_t swz(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
 
-// A row of q as hi and lo E4M3 codes, in place of its bf16 halves; returns the factor that the
-// codes have to be multiplied by. (A row with an infinity or NaN gets a NaN code.)
-__device__ __forceinline__ float split_row(uint8_t* q, int r) {
-  uint4 w[16];
-#pragma unroll
-  for (int k = 0; k < 16; ++k) w[k] = *reinterpret_cast<const uint4*>(q + (k >> 3) * kSlab + swz(r, k & 7));
+// A row of q (64 words of two bf16) to TMEM as hi and lo E4M3 codes (32 columns of four each);
+// returns the factor that the codes have to be multiplied by. (A row with an infinity or NaN gets
+// a NaN code.)
+__device__ __forceinline__ float split_row(const uint32_t* w, uint32_t tq) {
   uint32_t top = 0;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) top = max(top, max(u[k] & 0x7FFFu, (u[k] >> 16) & 0x7FFFu));
-  }
+  for (int i = 0; i < 64; ++i) top = max(top, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
   const int e = max((int)(top >> 7), 1);       // exponent field of the largest element
   // up * 2^(e - 134) = 1: q * up has its largest element in [2^7, 2^8). Both factors are made
   // of two powers of two, as one may leave fp32's range.
-  const int sh = 134 - e;                      // in [-120, 133]
+  const int sh = 134 - e;                      // in [-121, 133]
   const float up0 = __uint_as_float((uint32_t)(127 + sh / 2) << 23);
   const float up1 = __uint_as_float((uint32_t)(127 + sh - sh / 2) << 23);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {  // 16 elements, one 16-byte chunk of codes
-    uint32_t hi[4], lo[4];
+  for (int h = 0; h < 2; ++h) {
+    uint32_t hi[16], lo[16];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const uint4 v = w[2 * i + (k >> 1)];
-      const uint32_t a = (k & 1) ? v.z : v.x, b = (k & 1) ? v.w : v.y;
+    for (int i = 0; i < 16; ++i) {
+      const uint32_t a = w[32 * h + 2 * i], b = w[32 * h + 2 * i + 1];
       const float x0 = __uint_as_float(a << 16) * up0 * up1, x1 = __uint_as_float(a & 0xFFFF0000u) * up0 * up1;
       const float x2 = __uint_as_float(b << 16) * up0 * up1, x3 = __uint_as_float(b & 0xFFFF0000u) * up0 * up1;
       const uint16_t h01 = e4m3x2(x0, x1), h23 = e4m3x2(x2, x3);
       const uint32_t f01 = half2_of(h01), f23 = half2_of(h23);
       const float2 g01 = __half22float2(*reinterpret_cast<const __half2*>(&f01));
       const float2 g23 = __half22float2(*reinterpret_cast<const __half2*>(&f23));
-      hi[k] = h01 | ((uint32_t)h23 << 16);
-      lo[k] = e4m3x2(x0 - g01.x, x1 - g01.y) | ((uint32_t)e4m3x2(x2 - g23.x, x3 - g23.y) << 16);
+      hi[i] = h01 | ((uint32_t)h23 << 16);
+      lo[i] = e4m3x2(x0 - g01.x, x1 - g01.y) | ((uint32_t)e4m3x2(x2 - g23.x, x3 - g23.y) << 16);
     }
-    *reinterpret_cast<uint4*>(q + swz(r, i)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-    *reinterpret_cast<uint4*>(q + kSlab + swz(r, i)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    if (h == 0 && top >= 0x7F80u) hi[0] |= 0x7Fu;
+    tc::tmem_st16_u(tq + 16 * h, hi);
+    tc::tmem_st16_u(tq + 32 + 16 * h, lo);
   }
-  if (top >= 0x7F80u) q[swz(r, 0)] = 0x7F;
   return __uint_as_float((uint32_t)(127 - sh / 2) << 23) * __uint_as_float((uint32_t)(127 - (sh - sh / 2)) << 23);
+}
+
+// The factor from a raw score to log2 units, for a row's and a page's scale; kept above 0 so
+// that a key past the prefix stays at -inf (a score is 0 there all the same).
+__device__ __forceinline__ float factor(float row, float ks) { return fmaxf(row * ks, 1e-37f); }
+
+// The sequence with the n-th most keys (ties: the lower first), from the lengths: CTAs start in
+// the order of their index, so the longest are begun first and the last wave holds the shortest.
+__device__ __forceinline__ int nth_longest(const Params& p, int n, int* keys) {
+  for (int t = threadIdx.x; t < p.batch; t += kThreads)
+    keys[t] = __ldg(p.prefix_len + t) + (__ldg(p.qo + t + 1) - __ldg(p.qo + t));
+  int* found = keys + kLptMax;
+  __syncthreads();
+  for (int t = threadIdx.x; t < p.batch; t += kThreads) {
+    const int k = keys[t];
+    int r = 0;
+    for (int u = 0; u < p.batch; ++u) r += keys[u] > k || (keys[u] == k && u < t) ? 1 : 0;
+    if (r == n) *found = t;  // ranks are distinct: exactly one thread writes
+  }
+  __syncthreads();
+  const int b = *found;
+  __syncthreads();  // (the scratch becomes the K ring)
+  return b;
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -219,7 +241,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Bars& bars = *reinterpret_cast<Bars*>(smem + kOffBar);
   const uint32_t sb = tc::smem_u32(smem);
-  const int split = blockIdx.x, pair = blockIdx.y, bg = blockIdx.z;
+  const int split = blockIdx.x, bg = blockIdx.z;
   pdl_trigger();  // the split merge waits for this grid to end
   if (threadIdx.x == 0) {
     tc::prefetch_tmap(&tm_kp);
@@ -228,10 +250,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::prefetch_tmap(&tm_vt);
   }
   if (!p.early) pdl_wait();
-  const int b = bg / p.hkv, g = bg - b * p.hkv;
+  int b = bg / p.hkv;
+  const int g = bg - b * p.hkv;
+  if (p.lpt) b = nth_longest(p, b, reinterpret_cast<int*>(smem));
   const int base = __ldg(p.qo + b), N = __ldg(p.qo + b + 1) - base, P = __ldg(p.prefix_len + b);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // (warp: uniform)
-  const int node0 = 2 * pair * p.npt;
+  const int node0 = blockIdx.y * p.npt;
   if (node0 >= N) return;
   if (N > p.mask_words * 64 || P < 0 || P > p.max_len) {
     if (threadIdx.x == 0 && split == 0) {
@@ -240,23 +264,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     return;
   }
-  const bool two = node0 + p.npt < N;  // two row tiles; else both slots hold the same rows
   const Split sp = split_of(P, N, p.splits, split);
   const int nb = sp.nb, nt = sp.nt;
-  // slot t's blocks are i0(t), i0 + step, ... below nb
-  const int step = two ? 1 : 2;
+  // slot 0 takes every block (its first 64 keys), slot 1 the prefix blocks with more than 64
+  auto second = [&](int i) { return i >= nt && sp.pg_lo + (i - nt) * kPages + kPages / 2 < sp.pg_hi; };
+  const bool both = nb > nt && second(nt);  // slot 1 has work
 
   // softmax threads: slot, row, and what the row stands for
   const int slot = warp >= 8 ? 1 : 0;
   const int row = threadIdx.x & 127;
-  const int node = node0 + (two ? slot * p.npt : 0) + row / p.G;
+  const int node = node0 + row / p.G;
   const int head = g * p.G + row % p.G;
   const bool valid = row < p.npt * p.G && node < N;
   const size_t orow = (size_t)(base + node) * p.hq + head;
-  const int tile = 2 * pair + (two ? slot : 0) + p.mtiles * bg;
+  const int tile = blockIdx.y + p.mtiles * (b * p.hkv + g);
 
   if (nb == 0) {  // an empty key split: nothing for the merge
-    if (warp >= kSoft0 && warp < kCvt) {
+    if (warp >= kSoft0 && warp < 8) {
       pdl_wait();
       if (valid) p.part_lse[((size_t)tile * p.splits + split) * kRows + row] = -INFINITY;
     }
@@ -267,19 +291,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort = &bars.abort;
   if (warp == 0) {
     if (lane == 0) {
+      tc::mbar_init(bar(&bars.q16), 4);
+      tc::mbar_init(bar(&bars.q8), 4);
       for (int t = 0; t < 2; ++t) {
-        tc::mbar_init(bar(&bars.q16[t]), 4);
-        tc::mbar_init(bar(&bars.q8[t]), 4);
         tc::mbar_init(bar(&bars.s_full[t]), 1);
-        tc::mbar_init(bar(&bars.p_full[t][0]), 4);  // one arrival per softmax warp
-        tc::mbar_init(bar(&bars.p_full[t][1]), 4);
+        tc::mbar_init(bar(&bars.s_free[t]), 4);  // one arrival per softmax warp
+        tc::mbar_init(bar(&bars.p_full[t]), 4);
+        tc::mbar_init(bar(&bars.pv_done[t]), 1);
         tc::mbar_init(bar(&bars.o_full[t]), 1);
       }
-      tc::mbar_init(bar(&bars.go), 4);
-      const int users = two ? 2 : 1;
       for (int s = 0; s < kStK; ++s) {
         tc::mbar_init(bar(&bars.k_full[s]), 1);
-        tc::mbar_init(bar(&bars.k_empty[s]), users);
+        tc::mbar_init(bar(&bars.k_empty[s]), 2);  // both issuers
       }
       for (int s = 0; s < kStC; ++s) {
         tc::mbar_init(bar(&bars.c_full[s]), 1);
@@ -287,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       for (int s = 0; s < kStV; ++s) {
         tc::mbar_init(bar(&bars.v_full[s]), 4);
-        tc::mbar_init(bar(&bars.v_empty[s]), users);
+        tc::mbar_init(bar(&bars.v_empty[s]), 2);
       }
       for (int s = 0; s < kScales; ++s) tc::mbar_init(bar(&bars.sc_full[s]), 1);
       for (int s = 0; s < kMaxTreeBlocks; ++s) bars.bad[s] = 0;
@@ -313,8 +336,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // a block was the slowest of its parts). Page ids of four blocks at a time, one per lane,
     // a batch ahead of their use; an id is checked when its batch comes up.
     const bool isv = warp == 3;
-    constexpr int kSt = kStK;
-    static_assert(kStK == kStC, "one ring length for both producers");
+    const int kSt = isv ? kStC : kStK;
     uint64_t* full = isv ? bars.c_full : bars.k_full;
     uint64_t* empty = isv ? bars.c_empty : bars.k_empty;
     const uint32_t ring = sb + (isv ? kOffC : kOffK);
@@ -335,9 +357,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     int ids = checked(ids_of(0), 0), ids_next = ids_of(1);
     float2 sc = scale_of(ids), sc_next = make_float2(1.f, 1.f);
     int done = 0;  // blocks whose copies were issued
-    for (int i = 0; i < nb; ++i) {
-      const int st = i % kSt;
-      if (i >= kSt && !wait_all(bar(&empty[st]), ((i / kSt) & 1) ^ 1, abort)) break;
+    for (int i = 0, st = 0, turn = 0; i < nb; ++i, ++st) {
+      if (st == kSt) st = 0, ++turn;
+      if (turn > 0 && !wait_all(bar(&empty[st]), (turn & 1) ^ 1, abort)) break;
       const uint32_t dst = ring + st * kSlab;
       if (lane == 0) tc::mbar_arrive_expect_tx(bar(&full[st]), kSlab);
       __syncwarp();
@@ -379,84 +401,98 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp == 1 || warp == 2) {
     // ------------------------------------------------------------------ MMA issuers
-    // One warp per slot. Slot 1 starts when slot 0 has its first P, so that the slots run about
-    // half a period apart, one's softmax under the other's products.
+    // One warp per slot and one step a block: QK of the next block once the softmax holds this
+    // one's scores, then PV as P arrives. A block the slot has no step in it only passes on.
     const int t = warp - 1;
     const bool leader = elect_one();
-    const int cnt = two ? nb : (nb + 1 - t) / 2;
-    bool q8 = false, q16 = false;
-    // the slot's n-th block
-    auto block = [&](int n) { return two ? n : 2 * n + t; };
-    // what QK of the n-th block needs
-    auto wait_qk = [&](int n) {
-      const int i = block(n), sk = i % kStK;
-      if (i < nt && !q16) ok = ok && wait_all(bar(&bars.q16[t]), 0, abort), q16 = true;
-      if (i >= nt && !q8) ok = ok && wait_all(bar(&bars.q8[t]), 0, abort), q8 = true;
+    const uint32_t to = tmem + 128 * t, ts = tmem + kColS + kSlotCols * t, tp = ts + kStep;
+    int n = 0;  // the slot's steps so far
+    // QK of a prefix block into S
+    auto qk = [&](int i) {
+      const int sk = i % kStK;
       ok = ok && wait_all(bar(&bars.k_full[sk]), (i / kStK) & 1, abort);
-    };
-    auto qk = [&](int n) {
-      const int i = block(n), sk = i % kStK;
-      const uint32_t ts = tmem + t * 256;
-      const uint64_t qd = tc::sdesc_sw128(sb + kOffQ + t * kQTile, 16, 1024);
-      const uint64_t kd = tc::sdesc_sw128(sb + kOffK + sk * kSlab, 16, 1024);
+      if (!ok) return;
+      tc::fence_after_sync();
+      const uint64_t kd = tc::sdesc_sw128(sb + kOffK + sk * kSlab + t * (kStep * 128), 16, 1024);
       if (leader) {
-        if (i < nt) {
-#pragma unroll 1
-          for (int k = 0; k < 8; ++k)
-            tc::mma_bf16(ts, qd + (((k >> 2) * kSlab + (k & 3) * 32) >> 4),
-                         kd + (((k >> 2) * kTreeSlab + (k & 3) * 32) >> 4), kIdTreeQK, k > 0);
-        } else {
 #pragma unroll
-          for (int k = 0; k < 8; ++k)  // hi, then lo
-            tc::mma_f8(ts, qd + (((k >> 2) * kSlab + (k & 3) * 32) >> 4), kd + (((k & 3) * 32) >> 4), kIdQK, k > 0);
-        }
+        for (int k = 0; k < 8; ++k)  // hi, then lo
+          tc::mma_f8_ts(ts, tmem + kColQ + 8 * k, kd + (((k & 3) * 32) >> 4), kIdQK, k > 0);
         tc::mma_commit(bar(&bars.s_full[t]));
         tc::mma_commit(bar(&bars.k_empty[sk]));
       }
       __syncwarp();
     };
-    // half h of PV: P's first or second 64 keys; of a tree block, P's first or second bf16 term
-    auto pv = [&](int n, int h) {
-      const int i = block(n), sv = i % kStV;
-      const uint32_t pa = tmem + t * 256 + 32 * h, to = tmem + t * 256 + 128;
-      const uint64_t vd = tc::sdesc_sw128(sb + kOffV + sv * 2 * kSlab, kSlab, 1024);
-      if (leader) {
-        if (i < nt) {
-#pragma unroll 1
-          for (int k = 0; k < 4; ++k)
-            tc::mma_bf16_ts(to, pa + 8 * k, vd + ((k * 2048) >> 4), kIdTreePV, n > 0 || h > 0 || k > 0);
-        } else {
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            tc::mma_bf16_ts(to, pa + 8 * k, vd + (((4 * h + k) * 2048) >> 4), kIdPV, n > 0 || h > 0 || k > 0);
-        }
-        if (h == 1) tc::mma_commit(bar(&bars.v_empty[sv]));
-      }
+    // a block that the slot has no step in: released once its stages are this block's (an arrival
+    // must not count for an earlier one)
+    auto pass = [&](int i) {
+      ok = ok && wait_all(bar(&bars.k_full[i % kStK]), (i / kStK) & 1, abort);
+      if (ok && leader) tc::mbar_arrive(bar(&bars.k_empty[i % kStK]));
+      ok = ok && wait_all(bar(&bars.v_full[i % kStV]), (i / kStV) & 1, abort);
+      if (ok && leader) tc::mbar_arrive(bar(&bars.v_empty[i % kStV]));
       __syncwarp();
     };
-    if (t == 1 && cnt > 2) ok = wait_all(bar(&bars.go), 0, abort);
-    if (cnt > 0) wait_qk(0);
-    if (cnt > 0 && ok) {
-      tc::fence_after_sync();
-      qk(0);
-    }
-    for (int n = 0; ok && n < cnt; ++n) {
-      // PV as the halves of P arrive, then QK of the next block, whose operands have been
-      // waited for by then
-      const int i = block(n), sv = i % kStV;
-      const bool more = n + 1 < cnt;
-      ok = wait_all(bar(&bars.v_full[sv]), (i / kStV) & 1, abort) &&
-           wait_all(bar(&bars.p_full[t][0]), n & 1, abort);
+    // the tree, slot 0's: QK, then PV (P's second term lies where S was, so the next QK follows it)
+    if (nt > 0 && t == 0) ok = wait_all(bar(&bars.q16), 0, abort);
+#pragma unroll 1
+    for (int i = 0; ok && i < nt; ++i) {
+      const int sk = i % kStK, sv = i % kStV;
+      if (t == 1) {
+        pass(i);
+        continue;
+      }
+      ok = wait_all(bar(&bars.k_full[sk]), (i / kStK) & 1, abort);
       if (!ok) break;
       tc::fence_after_sync();
-      pv(n, 0);
-      if (more) wait_qk(n + 1);
-      ok = ok && wait_all(bar(&bars.p_full[t][1]), n & 1, abort);
+      if (leader) {
+        const uint64_t kd = tc::sdesc_sw128(sb + kOffK + sk * kSlab, 16, 1024);
+#pragma unroll 1
+        for (int k = 0; k < 8; ++k)
+          tc::mma_bf16_ts(ts, tmem + kColQ + 8 * k, kd + (((k >> 2) * kTreeSlab + (k & 3) * 32) >> 4), kIdTreeQK, k > 0);
+        tc::mma_commit(bar(&bars.s_full[0]));
+        tc::mma_commit(bar(&bars.k_empty[sk]));
+      }
+      __syncwarp();
+      ok = wait_all(bar(&bars.s_free[0]), n & 1, abort) && wait_all(bar(&bars.v_full[sv]), (i / kStV) & 1, abort) &&
+           wait_all(bar(&bars.p_full[0]), n & 1, abort);
       if (!ok) break;
       tc::fence_after_sync();
-      pv(n, 1);
-      if (more) qk(n + 1);
+      if (leader) {
+        const uint64_t vd = tc::sdesc_sw128(sb + kOffV + sv * 2 * kSlab, kSlab, 1024);
+#pragma unroll 1
+        for (int k = 0; k < 8; ++k)  // four steps of 16 nodes for each term
+          tc::mma_bf16_ts(to, (k < 4 ? tp : ts - 32) + 8 * k, vd + (((k & 3) * 2048) >> 4), kIdTreePV, n > 0 || k > 0);
+        tc::mma_commit(bar(&bars.pv_done[0]));
+        tc::mma_commit(bar(&bars.v_empty[sv]));
+      }
+      __syncwarp();
+      ++n;
     }
+    // the prefix
+    const int last = t == 0 || nb == nt || second(nb - 1) ? nb : nb - 1;  // (only the last block can lack a half)
+    if (ok && last > nt) {
+      ok = wait_all(bar(&bars.q8), 0, abort);
+      qk(nt);
+    }
+#pragma unroll 1
+    for (int i = nt; ok && i < last; ++i, ++n) {
+      const int sv = i % kStV;
+      ok = wait_all(bar(&bars.s_free[t]), n & 1, abort);
+      if (ok && i + 1 < last) qk(i + 1);
+      ok = ok && wait_all(bar(&bars.v_full[sv]), (i / kStV) & 1, abort) &&
+           wait_all(bar(&bars.p_full[t]), n & 1, abort);
+      if (!ok) break;
+      tc::fence_after_sync();
+      const uint64_t vd = tc::sdesc_sw128(sb + kOffV + sv * 2 * kSlab + t * (kStep * 128), kSlab, 1024);
+      if (leader) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) tc::mma_bf16_ts(to, tp + 8 * k, vd + ((k * 2048) >> 4), kIdPV, n > 0 || k > 0);
+        tc::mma_commit(bar(&bars.pv_done[t]));
+        tc::mma_commit(bar(&bars.v_empty[sv]));
+      }
+      __syncwarp();
+    }
+    if (ok && last < nb) pass(last);
     if (!ok && leader) report(p.status, SPEC_ERR_TIMEOUT);
     // every product issued has completed before O is read and TMEM released
     if (leader) tc::mma_commit(bar(&bars.o_full[t]));
@@ -504,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else {
         const int pg = sp.pg_lo + (i - nt) * kPages;
         const int nvalid = min(P, sp.pg_hi * 16) - pg * 16;  // rows past it may hold anything
-#pragma unroll
+#pragma unroll 4
         for (int it = 0; it < 8; ++it) {
           const int id = it * 128 + ct;
           const int r = (id & 7) | ((id >> 6) << 3), cc = (id >> 3) & 7;
@@ -532,265 +568,251 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp >= kSoft0) {
     regs_up();
     // ------------------------------------------------------------------ softmax
-    const int i0 = two ? 0 : slot;
-    const uint32_t ts = tmem + slot * 256 + ((uint32_t)((warp & 3) * 32) << 16), to = ts + 128;
-    uint8_t* q = smem + kOffQ + slot * kQTile;
+    const uint32_t quarter = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + kColS + kSlotCols * slot + quarter, tp = ts + kStep, to = tmem + 128 * slot + quarter;
+    const uint32_t tq = tmem + kColQ + quarter;
     const bool live = __any_sync(0xffffffffu, valid);  // a warp without rows only keeps step
-    const int last_tree = i0 < nt ? i0 + (nt - 1 - i0) / step * step : -1;
-    float qf = 0.f;  // the factor of the row's codes
-    uint64_t bits = 0ull;
     const uint64_t* mrow = p.mask + (size_t)(base + node) * p.mask_words;
     const float scale_log2 = p.scale_log2;
-    bool coded = false;  // q's row stands as codes
-    if (i0 < nb) {
+    float* factors = reinterpret_cast<float*>(smem + kOffJoin);  // [row], from slot 0 to slot 1
+    float qf = 0.f;  // the factor of the row's codes
+    int n = 0;       // the slot's steps so far
+    auto load_q = [&](uint32_t* w) {
       const uint4* src = reinterpret_cast<const uint4*>(p.q + orow * kD);
-      uint4 w[16];
 #pragma unroll
-      for (int k = 0; k < 16; ++k) w[k] = valid ? __ldg(src + k) : make_uint4(0, 0, 0, 0);
+      for (int k = 0; k < 16; ++k) {
+        const uint4 u = valid ? __ldg(src + k) : make_uint4(0, 0, 0, 0);
+        w[4 * k] = u.x, w[4 * k + 1] = u.y, w[4 * k + 2] = u.z, w[4 * k + 3] = u.w;
+      }
+    };
+    // A step begins with its S complete and ends with its P handed on. In between, M follows the
+    // row's maximum; where it moves, O is rescaled. PV of the step before is complete by then: it
+    // is waited for first, as this step's P overwrites what it read. (Warps without rows wait for
+    // it too, else their arrivals could run a step ahead of the others'.)
+    auto begin_step = [&]() {
+      ok = wait_all(bar(&bars.s_full[slot]), n & 1, abort);
+      tc::fence_after_sync();
+      return ok;
+    };
+    auto raise = [&](float mx) {
+      float alpha = 1.f;
+      bool rescale = false;
+      if (mx > -INFINITY && (m == -INFINITY || mx > m + kGrow)) {
+        alpha = m == -INFINITY ? 0.f : ex2_approx(m - mx);
+        m = mx;
+        l *= alpha;
+        rescale = n > 0;
+      }
+      if (n > 0) ok = wait_all(bar(&bars.pv_done[slot]), (n - 1) & 1, abort);
+      if (__any_sync(0xffffffffu, rescale)) {
+        tc::fence_after_sync();
+#pragma unroll 1
+        for (int ch = 0; ch < kD / 16; ++ch) {
+          float o[16];
+          tc::tmem_ld16(to + ch * 16, o);
+          tc::tmem_wait_ld();
+          const float f = rescale ? alpha : 1.f;
 #pragma unroll
-      for (int k = 0; k < 16; ++k) *reinterpret_cast<uint4*>(q + (k >> 3) * kSlab + swz(row, k & 7)) = w[k];
-      if (last_tree >= 0) {
-        tc::fence_proxy_async_smem();
-        warp_arrive(bar(&bars.q16[slot]));
-        pdl_wait();  // the mask may come from the kernel before
-        if (valid) bits = __ldcg(mrow + sp.tb_lo + i0);
+          for (int k = 0; k < 16; ++k) o[k] *= f;
+          tc::tmem_st16(to + ch * 16, o);
+        }
+      }
+      return m == -INFINITY ? 0.f : kShift - m;
+    };
+    auto dead_step = [&]() {
+      warp_arrive(bar(&bars.s_free[slot]));
+      if (n > 0) ok = wait_all(bar(&bars.pv_done[slot]), (n - 1) & 1, abort);
+    };
+    auto end_step = [&]() {
+      tc::fence_before_sync();
+      if (ok) warp_arrive(bar(&bars.p_full[slot]));
+      ++n;
+    };
+    if (slot == 0 && nt > 0) {
+      // the tree: q's row as it is, P as two bf16 terms
+      uint32_t w[64];
+      load_q(w);
+      tc::tmem_st32_u(tq, w);
+      tc::tmem_st32_u(tq + 32, w + 32);
+      tc::tmem_wait_st();
+      tc::fence_before_sync();
+      warp_arrive(bar(&bars.q16));
+      pdl_wait();  // the mask may come from the kernel before
+      uint64_t bits = valid ? __ldcg(mrow + sp.tb_lo) : 0ull;
+#pragma unroll 1
+      for (int i = 0; ok && i < nt; ++i) {
+        if (!begin_step()) break;
+        if (live) {
+          float s[kStep];
+          tc::tmem_ld32(ts, s);
+          tc::tmem_ld32(ts + 32, s + 32);
+          tc::tmem_wait_ld();
+          tc::fence_before_sync();
+          warp_arrive(bar(&bars.s_free[0]));
+          const uint64_t see = bits;
+          if (valid && i + 1 < nt) bits = __ldcg(mrow + sp.tb_lo + i + 1);
+          float mx = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < kStep; ++c) {
+            s[c] = ((see >> c) & 1ull) ? s[c] * scale_log2 : -INFINITY;
+            mx = fmaxf(mx, s[c]);
+          }
+          const float off = raise(mx);
+          float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            uint32_t hi[8], lo[8];
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              const float a = ex2_approx(s[16 * h + 2 * c] + off), d = ex2_approx(s[16 * h + 2 * c + 1] + off);
+              sum0 += a;
+              sum1 += d;
+              hi[c] = pack_bf16x2(a, d);
+              lo[c] = pack_bf16x2(a - __uint_as_float(hi[c] << 16), d - __uint_as_float(hi[c] & 0xFFFF0000u));
+            }
+            tc::tmem_st8_u(tp + 8 * h, hi);
+            tc::tmem_st8_u(ts + 8 * h, lo);
+          }
+          l += sum0 + sum1;
+          tc::tmem_wait_st();
+        } else {
+          dead_step();
+        }
+        end_step();
       }
     }
-    for (int i = i0, n = 0; i < nb; i += step, ++n) {
-      if (i >= nt && !coded) {
-        // (the slot's last tree block, if any, has its S: q's bf16 rows have been read)
-        qf = split_row(q, row);
-        coded = true;
-        tc::fence_proxy_async_smem();
-        warp_arrive(bar(&bars.q8[slot]));
+    if (ok && nb > nt) {
+      // the prefix: q as codes, from slot 0 (which has S of every tree block, so that the rows in
+      // their place have been read)
+      if (slot == 0) {
+        uint32_t w[64];
+        load_q(w);
+        qf = split_row(w, tq);
+        factors[row] = qf;
+        tc::tmem_wait_st();
+        tc::fence_before_sync();
+        warp_arrive(bar(&bars.q8));
+      } else {
+        ok = wait_all(bar(&bars.q8), 0, abort);
+        qf = factors[row];
       }
-      // the block's page scales, as factors, exponents and weights of the row sum (they are
-      // there before S is)
-      float pf[kPages], pe[kPages], pw[kPages];
-      int nvalid = kKeys;
-      if (i >= nt) {
-        const int j = i - nt;
+      const float rowf = scale_log2 * qf;
+      const int np = slot == 0 || second(nb - 1) ? nb - nt : nb - nt - 1;  // (only the last block can lack a half)
+#pragma unroll 1
+      for (int j = 0; ok && j < np; ++j) {
+        // the page scales of the slot's half, as factors, exponents and weights of the row sum:
+        // they are there before S is
         if (!wait_all(bar(&bars.sc_full[j % kScales]), (j / kScales) & 1, abort)) {
           ok = false;
           break;
         }
-        const float4* scale = reinterpret_cast<const float4*>(smem + kOffScale) + (j % kScales) * kPages;
+        const float4* scale = reinterpret_cast<const float4*>(smem + kOffScale) + (j % kScales) * kPages + 4 * slot;
+        float4 f[4];
 #pragma unroll
-        for (int pp = 0; pp < kPages; ++pp) {
-          const float4 f = scale[pp];
-          // (kept above 0, so that a key past the prefix stays at -inf; a score is 0 there all the same)
-          pf[pp] = fmaxf(scale_log2 * qf * f.x, 1e-37f);
-          pe[pp] = f.y;
-          pw[pp] = f.z;
-        }
-        nvalid = min(P, sp.pg_hi * 16) - (sp.pg_lo + j * kPages) * 16;
-      }
-      if (!wait_all(bar(&bars.s_full[slot]), n & 1, abort)) {
-        ok = false;
-        break;
-      }
-      tc::fence_after_sync();  // S of this block; O of all before
-      float alpha = 1.f;
-      bool rescale = false;
-      auto raise = [&](float mx) {
-        if (mx > -INFINITY && (m == -INFINITY || mx > m + kGrow)) {
-          alpha = m == -INFINITY ? 0.f : ex2_approx(m - mx);
-          m = mx;
-          l *= alpha;
-          rescale = n > 0;
-        }
-        if (__any_sync(0xffffffffu, rescale)) {
-#pragma unroll 1
-          for (int ch = 0; ch < kD / 32; ++ch) {
-            float o[32];
-            tc::tmem_ld32(to + ch * 32, o);
-            tc::tmem_wait_ld();
-            const float f = rescale ? alpha : 1.f;
-#pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] *= f;
-            tc::tmem_st32(to + ch * 32, o);
-          }
-        }
-      };
-      if (i < nt) {
+        for (int pp = 0; pp < 4; ++pp) f[pp] = scale[pp];
+        if (!begin_step()) break;
         if (live) {
-          float s[kTreeKeys];
+          float s[kStep];
           tc::tmem_ld32(ts, s);
           tc::tmem_ld32(ts + 32, s + 32);
           tc::tmem_wait_ld();
-          const uint64_t see = bits;
-          if (valid && i + step < nt) bits = __ldcg(mrow + sp.tb_lo + i + step);
-          float mx = -INFINITY;
+          tc::fence_before_sync();
+          warp_arrive(bar(&bars.s_free[slot]));  // QK of the next step may overwrite S
+          const int nvalid = min(P, sp.pg_hi * 16) - (sp.pg_lo + j * kPages) * 16 - kStep * slot;
+          if (nvalid < kStep) {
 #pragma unroll
-          for (int c = 0; c < kTreeKeys; ++c) {
-            s[c] = ((see >> c) & 1ull) ? s[c] * scale_log2 : -INFINITY;
-            mx = fmaxf(mx, s[c]);
+            for (int c = 0; c < kStep; ++c) s[c] = c < nvalid ? s[c] : -INFINITY;
           }
-          raise(mx);
-          const float off = m == -INFINITY ? 0.f : kShift - m;
-          uint32_t hi[kTreeKeys / 2], lo[kTreeKeys / 2];
-          float sum0 = 0.f, sum1 = 0.f;
+          float mx = -INFINITY;  // the largest x log2 e + log2 vs
 #pragma unroll
-          for (int c = 0; c < kTreeKeys; c += 2) {
-            const float a = ex2_approx(s[c] + off), d = ex2_approx(s[c + 1] + off);
-            sum0 += a;
-            sum1 += d;
-            const uint32_t h = pack_bf16x2(a, d);
-            hi[c >> 1] = h;
-            lo[c >> 1] = pack_bf16x2(a - __uint_as_float(h << 16), d - __uint_as_float(h & 0xFFFF0000u));
+          for (int pp = 0; pp < 4; ++pp) {
+            const float* v = s + 16 * pp;
+            float x = fmax3(v[0], v[1], v[2]);
+#pragma unroll
+            for (int c = 3; c < 15; c += 2) x = fmax3(x, v[c], v[c + 1]);
+            f[pp].x = factor(rowf, f[pp].x);
+            mx = fmaxf(mx, fmaf(fmaxf(x, v[15]), f[pp].x, f[pp].y));
           }
-          l += sum0 + sum1;
-          tc::tmem_st32_u(ts, hi);
-          tc::tmem_st32_u(ts + 32, lo);
-          tc::tmem_wait_st();
-        }
-        tc::fence_before_sync();
-        warp_arrive(bar(&bars.p_full[slot][0]));
-        warp_arrive(bar(&bars.p_full[slot][1]));
-        if (slot == 0 && n == 0) warp_arrive(bar(&bars.go));
-        continue;
-      }
-      if (live) {
-        float s[kKeys];
+          const float off = raise(mx);
 #pragma unroll
-        for (int h = 0; h < 4; ++h) tc::tmem_ld32(ts + 32 * h, s + 32 * h);
-        tc::tmem_wait_ld();
-        if (nvalid < kKeys) {
-#pragma unroll
-          for (int c = 0; c < kKeys; ++c) s[c] = c < nvalid ? s[c] : -INFINITY;
-        }
-        float mx = -INFINITY;  // the largest x log2 e + log2 vs
-#pragma unroll
-        for (int pp = 0; pp < kPages; ++pp) {
-          const float* v = s + 16 * pp;
-          float x = fmax3(v[0], v[1], v[2]);
-#pragma unroll
-          for (int c = 3; c < 15; c += 2) x = fmax3(x, v[c], v[c + 1]);
-          mx = fmaxf(mx, fmaf(fmaxf(x, v[15]), pf[pp], pe[pp]));
-        }
-        raise(mx);
-        const float off = m == -INFINITY ? 0.f : kShift - m;
-#pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          uint32_t pk[16];
-#pragma unroll
-          for (int pp = 0; pp < 2; ++pp) {
-            const float ff = pf[2 * h + pp], oo = off + pe[2 * h + pp];
-            const float2 f2 = make_float2(ff, ff), o2 = make_float2(oo, oo);
+          for (int pp = 0; pp < 4; ++pp) {
+            const float oo = off + f[pp].y;
+            const float2 f2 = make_float2(f[pp].x, f[pp].x), o2 = make_float2(oo, oo);
             float2 r0 = make_float2(0.f, 0.f), r1 = make_float2(0.f, 0.f);
+            uint32_t pk[8];
 #pragma unroll
-            for (int k = 0; k < 16; k += 4) {
-              const float* v = s + 32 * h + 16 * pp + k;
+            for (int c = 0; c < 16; c += 4) {
+              const float* v = s + 16 * pp + c;
               const float2 a = ffma2(make_float2(v[0], v[1]), f2, o2);
               const float2 d = ffma2(make_float2(v[2], v[3]), f2, o2);
               const float2 ea = make_float2(ex2_approx(a.x), ex2_approx(a.y));
               const float2 ed = make_float2(ex2_approx(d.x), ex2_approx(d.y));
               r0 = fadd2(r0, ea);
               r1 = fadd2(r1, ed);
-              pk[8 * pp + (k >> 1)] = pack_f16x2(ea.x, ea.y);
-              pk[8 * pp + (k >> 1) + 1] = pack_f16x2(ed.x, ed.y);
+              pk[c >> 1] = pack_f16x2(ea.x, ea.y);
+              pk[(c >> 1) + 1] = pack_f16x2(ed.x, ed.y);
             }
-            l = fmaf((r0.x + r0.y) + (r1.x + r1.y), pw[2 * h + pp], l);
+            l = fmaf((r0.x + r0.y) + (r1.x + r1.y), f[pp].z, l);
+            tc::tmem_st8_u(tp + 8 * pp, pk);
           }
-          tc::tmem_st16_u(ts + 16 * h, pk);
-          if (h == 1) {  // PV of the first 64 keys may start
-            tc::tmem_wait_st();
-            tc::fence_before_sync();
-            warp_arrive(bar(&bars.p_full[slot][0]));
-          }
+          tc::tmem_wait_st();
+        } else {
+          dead_step();
         }
-        tc::tmem_wait_st();
-      } else {
-        warp_arrive(bar(&bars.p_full[slot][0]));
+        end_step();
       }
-      tc::fence_before_sync();
-      warp_arrive(bar(&bars.p_full[slot][1]));
-      if (slot == 0 && n == 0) warp_arrive(bar(&bars.go));
     }
     if (!ok && lane == 0) report(p.status, SPEC_ERR_TIMEOUT);
 
     // -------------------------------------------------------------------- epilogue
+    // The slots' sums are joined: both hold the same rows, and each thread takes 64 columns of
+    // its row, from both O's.
     tc::fence_before_sync();
     cta_sync();  // every product is complete, every copy has landed
     tc::fence_after_sync();
-    // one tile: slot 1 hands its sums to slot 0 through shared memory (chunk of 4 columns,
-    // then row: consecutive lanes, consecutive 16 bytes)
-    float4* join = reinterpret_cast<float4*>(smem + kOffQ);
-    float2* join_ml = reinterpret_cast<float2*>(smem + kOffK);
-    if (!two) {
-      if (slot == 1 && live) {
-        if (valid) join_ml[row] = make_float2(m, l);
-        if (nb > 1) {
-#pragma unroll 1
-          for (int ch = 0; ch < kD / 32; ++ch) {
-            float o[32];
-            __syncwarp();
-            tc::tmem_ld32(to + ch * 32, o);
-            tc::tmem_wait_ld();
-            if (valid) {
-#pragma unroll
-              for (int k = 0; k < 8; ++k)
-                join[(ch * 8 + k) * kRows + row] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-            }
-          }
-        }
-      }
-      asm volatile("bar.sync 1, 256;" ::: "memory");
-    }
-    if (live && (two || slot == 0)) {
-      float w0 = 1.f, w1 = 0.f;
-      const bool joined = !two && nb > 1;
-      if (joined && valid) {
-        const float2 x = join_ml[row];
-        const float top = fmaxf(m, x.x);
-        w0 = m == -INFINITY ? 0.f : ex2_approx(m - top);
-        w1 = x.x == -INFINITY ? 0.f : ex2_approx(x.x - top);
-        l = l * w0 + x.y * w1;
-        m = top;
-      }
-      float inv = l == 0.f ? 0.f : 1.f / l;
+    float2* join = reinterpret_cast<float2*>(smem + kOffJoin);
+    join[slot * kRows + row] = make_float2(m, l);
+    soft_sync();
+    if (live) {
+      const float2 a = join[row], c = both ? join[kRows + row] : make_float2(-INFINITY, 0.f);
+      const float top = fmaxf(a.x, c.x);
+      const float w0 = a.x == -INFINITY ? 0.f : ex2_approx(a.x - top), w1 = c.x == -INFINITY ? 0.f : ex2_approx(c.x - top);
+      const float sum = a.y * w0 + c.y * w1;
+      float inv = sum == 0.f ? 0.f : 1.f / sum;
       // a tree node that this row sees holds an infinity or NaN in V
       for (int i = 0; i < nt; ++i) {
         const uint64_t bad = bars.bad[sp.tb_lo + i];
-        if (bad != 0 && valid && (__ldcg(p.mask + (size_t)(base + node) * p.mask_words + sp.tb_lo + i) & bad) != 0)
-          inv = __int_as_float(0x7FC00000);
+        if (bad != 0 && valid && (__ldcg(mrow + sp.tb_lo + i) & bad) != 0) inv = __int_as_float(0x7FC00000);
       }
       if (!ok || *abort) inv = 0.f;
+      const float i0 = inv * w0, i1 = inv * w1;
       pdl_wait();  // nothing is written before the kernel before has finished
-      const float lse2 = l == 0.f ? -INFINITY : m + log2f(l) - kShift;
+      const uint32_t o0 = tmem + 64 * slot + quarter, o1 = o0 + 128;
 #pragma unroll 1
-      for (int ch = 0; ch < kD / 32; ++ch) {
-        float o[32];
+      for (int ch = 0; ch < 4; ++ch) {
+        float x[16], y[16];
         __syncwarp();
-        tc::tmem_ld32(to + ch * 32, o);
+        tc::tmem_ld16(o0 + 16 * ch, x);
+        tc::tmem_ld16(o1 + 16 * ch, y);
         tc::tmem_wait_ld();
         if (!valid) continue;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          float4 x = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-          if (joined) {
-            const float4 y = join[(ch * 8 + k) * kRows + row];
-            x = make_float4(x.x * w0 + y.x * w1, x.y * w0 + y.y * w1, x.z * w0 + y.z * w1, x.w * w0 + y.w * w1);
-          }
-          o[4 * k] = x.x * inv;
-          o[4 * k + 1] = x.y * inv;
-          o[4 * k + 2] = x.z * inv;
-          o[4 * k + 3] = x.w * inv;
-        }
+        for (int k = 0; k < 16; ++k) x[k] = both ? x[k] * i0 + y[k] * i1 : x[k] * i0;
         if (p.splits == 1) {
-          uint4* dst = reinterpret_cast<uint4*>(p.out + orow * kD + ch * 32);
+          uint4* dst = reinterpret_cast<uint4*>(p.out + orow * kD + 64 * slot + 16 * ch);
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            dst[k] = make_uint4(pack_bf16x2(x[8 * k], x[8 * k + 1]), pack_bf16x2(x[8 * k + 2], x[8 * k + 3]),
+                                pack_bf16x2(x[8 * k + 4], x[8 * k + 5]), pack_bf16x2(x[8 * k + 6], x[8 * k + 7]));
+        } else {
+          float4* po = p.part_o + ((size_t)tile * p.splits + split) * (kRows * kD / 4) + 16 * slot * kRows + row;
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            dst[k] = make_uint4(pack_bf16x2(o[8 * k], o[8 * k + 1]), pack_bf16x2(o[8 * k + 2], o[8 * k + 3]),
-                                pack_bf16x2(o[8 * k + 4], o[8 * k + 5]), pack_bf16x2(o[8 * k + 6], o[8 * k + 7]));
-        } else {
-          float4* po = p.part_o + ((size_t)tile * p.splits + split) * (kRows * kD / 4);
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            po[(ch * 8 + k) * kRows + row] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+            po[(ch * 4 + k) * kRows] = make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
         }
       }
-      if (valid) {
+      if (valid && slot == 0) {
+        const float lse2 = sum == 0.f ? -INFINITY : top + log2f(sum) - kShift;
         if (p.splits > 1) p.part_lse[((size_t)tile * p.splits + split) * kRows + row] = lse2;
         else if (p.lse != nullptr) p.lse[orow] = lse2 * kLn2;
       }
@@ -867,13 +889,13 @@ __global__ void __launch_bounds__(kMergeThreads) attn_kv8p_merge_kernel(const Me
 
 static int tiles_of(int max_nodes, int npt) { return ceil_div(max_nodes, npt); }
 
-// Key splits per work item (sequence, KV head, pair of row tiles), from the sizes alone; one
+// Key splits per work item (sequence, KV head, row tile), from the sizes alone; one
 // CTA fits on an SM. Fewer items than SMs: the splits that cover the SMs. Otherwise the count
 // in 1..8 whose waves cost least (a CTA's fixed cost counted as two blocks), if that is at
 // least 8% below the unsplit cost (the merge kernel is not in the model).
 static int splits_of(int batch, int max_nodes, int hq, int hkv, int max_prefix) {
   const int npt = kRows / (hq / hkv);
-  const long items = (long)batch * hkv * ceil_div(tiles_of(max_nodes, npt), 2), sms = sm_count();
+  const long items = (long)batch * hkv * tiles_of(max_nodes, npt), sms = sm_count();
   const int blocks = ceil_div(max_prefix, kKeys) + ceil_div(max_nodes, kTreeKeys);
   long s = 1;
   if (items > 0 && items < sms) {
@@ -939,8 +961,12 @@ int launch_attn_kv8p(const void* q, const uint8_t* k_pool, const uint8_t* v_pool
   }
   static PerDevice smem_set;
   if (per_device(smem_set, [](int) {
-        return cudaFuncSetAttribute(attn_kv8p_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) ==
-                       cudaSuccess
+        // (the warpgroups' shares of the registers add up to what a launch starts with only if
+        // the kernel was built with that many)
+        cudaFuncAttributes a;
+        return cudaFuncGetAttributes(&a, attn_kv8p_kernel) == cudaSuccess && a.numRegs == kLaunchRegs &&
+                       cudaFuncSetAttribute(attn_kv8p_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) ==
+                           cudaSuccess
                    ? 1
                    : 0;
       }) == 0)
@@ -972,7 +998,10 @@ int launch_attn_kv8p(const void* q, const uint8_t* k_pool, const uint8_t* v_pool
   prm.part_o = prm.splits > 1 ? reinterpret_cast<float4*>(wb + w.o) : nullptr;
   prm.status = status;
   prm.early = early_reads() ? 1 : 0;
-  const dim3 grid(prm.splits, ceil_div(prm.mtiles, 2), batch * hkv);
+  prm.batch = batch;
+  // (past eight waves the last one is a small share of the grid)
+  prm.lpt = prm.splits == 1 && batch > 1 && batch <= kLptMax && tiles <= 8L * sm_count() ? 1 : 0;
+  const dim3 grid(prm.splits, prm.mtiles, batch * hkv);
   if (launch_pdl(attn_kv8p_kernel, grid, dim3(kThreads), kSmem, stream, tm_kp, tm_vp, tm_kt, tm_vt, prm) != cudaSuccess)
     return SPEC_ERR_CUDA;
   if (prm.splits > 1) {
