@@ -22,17 +22,16 @@
 //
 // A CTA = (key split, row tile, sequence x KV head). A row tile is 128 rows: 128 / G nodes
 // (rounded down) of G heads each. K/V come in blocks: first the split's tree blocks (64 nodes,
-// bf16), then its prefix blocks (128 keys, 8 pages, TMA page by page). Two slots work side by
-// side on the same rows, each with its own S (64 keys), P and O in TMEM, its MMA-issuing warp
-// and four softmax warps (one row per thread): slot 0 takes the tree and the first 64 keys of
-// every prefix block, slot 1 the other 64; their sums are joined at the end.
-//   - q stands in TMEM too (bf16 rows for the tree, codes for the prefix: 64 columns either
-//     way), the A operand of QK: read from shared memory for every product it took as much of
-//     that memory's bandwidth as K, and shared memory is what the other warps wait for.
-//   - S and P lie apart, so QK of a slot's next step runs as soon as the softmax has its scores
-//     in registers, under the exponentials; PV follows when P is there.
-// Warps (512 threads): 0 and 3 TMA producers (K, V), 1 and 2 MMA issuers (1 also allocates
-// TMEM), 4-7 and 8-11 softmax of slots 0 and 1, 12-15 V's converters. Every wait is bounded.
+// bf16), then its prefix blocks (128 keys, 8 pages, TMA page by page). Two groups of four softmax
+// warps (one row per thread) take the blocks in turn, each with its own O; the sums are joined at
+// the end. One S and one P serve both: a group has S in registers soon after it is complete, so QK
+// of the next block runs, for the other group, under this one's exponentials, and P is written
+// only when it is all there, then read by PV at once. The time a block takes is thus about half of
+// what one group needs for it, and every barrier is passed once for 128 keys.
+// q's codes stand in TMEM (64 columns), the A operand of QK: read from shared memory for every
+// product they took as much of that memory's bandwidth as K did.
+// Warps (512 threads): 0 and 3 TMA producers (K, V), 1 and 2 MMA issuers (QK; PV), 4-7 and
+// 8-11 softmax, 12-15 V's converters. Every wait is bounded.
 // Splits write O / l in fp32 and the log2-sum-exp, joined by a second kernel.
 #include "attn_common.cuh"
 #include "tc_host.cuh"
@@ -48,25 +47,25 @@ constexpr int kTreeKeys = 64;   // nodes of a tree block
 constexpr int kD = 128;
 constexpr int kThreads = 512;
 constexpr int kSoft0 = 4, kCvt = 12;         // first softmax warp, first converter warp
-constexpr int kStep = 64;                    // keys of a slot's step: half a prefix block, or a tree block
-constexpr int kStK = 4, kStC = 3, kStV = 3;  // stages: K, V codes, V in 16 bits
+constexpr int kStK = 4, kStC = 3, kStV = 2;  // stages: K, V codes, V in 16 bits
 constexpr uint32_t kSlab = 128 * 128;        // 128 rows of 128 bytes
 constexpr uint32_t kTreeSlab = kTreeKeys * 128;
 constexpr uint32_t kOffK = 0;
 constexpr uint32_t kOffC = kOffK + kStK * kSlab;
 constexpr uint32_t kOffV = kOffC + kStC * kSlab;
-constexpr uint32_t kOffBar = kOffV + kStV * 2 * kSlab;
-constexpr int kScales = 8;                   // blocks whose page scales are kept
+constexpr uint32_t kOffQ = kOffV + kStV * 2 * kSlab;   // q's bf16 rows, for the tree
+constexpr uint32_t kOffBar = kOffQ + 2 * kSlab;
+constexpr int kScales = 12;                  // blocks whose page scales are kept: three groups of four
 constexpr uint32_t kOffScale = kOffBar + 512;
-constexpr uint32_t kOffJoin = kOffScale + kScales * kPages * 16;      // float2 [slot][row]: maximum, sum
+constexpr uint32_t kOffJoin = kOffScale + kScales * kPages * 16;      // float2 [group][row]: maximum, sum
 constexpr uint32_t kSmem = kOffJoin + 2 * kRows * 8 + 1024;           // + alignment slack
 static_assert(kSmem <= 232448, "shared memory over the per-CTA limit");
-// TMEM columns: O of slot t at 128 t, q, then S and P of slot t
-constexpr uint32_t kTmemCols = 512, kColQ = 256, kColS = 320, kSlotCols = 96;  // P: 64 columns after S
+// TMEM columns: O of group t at 128 t, q, S, P
+constexpr uint32_t kTmemCols = 512, kColQ = 256, kColS = 320, kColP = 448;
 constexpr int kLptMax = 1024;                // sequences that are ranked by length
 constexpr float kShift = 11.f;               // log2 of the largest P when M is set
 constexpr float kGrow = 4.f;                 // growth of the largest score that M may lag behind
-constexpr uint32_t kIdQK = tc::idesc_e4m3(kRows, kStep);
+constexpr uint32_t kIdQK = tc::idesc_e4m3(kRows, kKeys);
 constexpr uint32_t kIdPV = tc::idesc_f16(kRows, kD, 1);
 constexpr uint32_t kIdTreeQK = tc::idesc_bf16(kRows, kTreeKeys, 0);
 constexpr uint32_t kIdTreePV = tc::idesc_bf16(kRows, kD, 1);
@@ -95,14 +94,15 @@ struct Params {
 };
 
 struct Bars {
-  uint64_t q16, q8;                           // q in bf16 / as two E4M3 terms
-  uint64_t k_full[kStK], k_empty[kStK], c_full[kStC], c_empty[kStC], v_full[kStV], v_empty[kStV];
-  uint64_t s_full[2], s_free[2], p_full[2], pv_done[2], o_full[2];  // [slot], one phase a step
-  uint64_t sc_full[kScales];
+  // one arrival a phase
+  uint64_t k_full[kStK], k_empty[kStK], c_full[kStC], v_empty[kStV], s_full[2], pv_done[2], all_done[2], sc_full[2];
+  // four: a warpgroup's warps
+  uint64_t q16, q8, c_empty[kStC], v_full[kStV], s_free, p_full;  // q in bf16 / as codes
   uint64_t bad[kMaxTreeBlocks];  // tree nodes whose V row holds an infinity or NaN
   uint32_t tmem;
   int abort;
 };
+constexpr int kBar1 = 2 * kStK + kStC + kStV + 8, kBarAll = kBar1 + 4 + kStC + kStV;
 static_assert(sizeof(Bars) <= 512, "barrier block over its reserved bytes");
 
 // The blocks of one key split: units are the tree blocks (4 each), then the prefix pages; a
@@ -141,10 +141,27 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return d;
 }
 
-// The whole warp waits together. (One lane waiting for the others, with its answer shuffled to
-// them, cost about 1000 cycles a wait to bring the warp back together.)
+// The whole warp waits for a phase, bounded: the hardware holds a try for microseconds before it
+// says no, so kTries of them are a second or so. (One lane waiting, with its answer shuffled to the
+// others, cost about 1000 cycles a wait to bring the warp back together.)
+constexpr int kTries = 1 << 18;
 __device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, volatile int* abort) {
-  return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, abort, kWaitLimit));
+  bool ok;
+  int i = 0;
+  do ok = tc::mbar_try_wait(bar, parity);
+  while (!ok && ++i < kTries && *abort == 0);
+  if (!ok) *abort = 1;
+  return __all_sync(0xffffffffu, ok);
+}
+
+// The same for one thread.
+__device__ __forceinline__ bool wait_one(uint32_t bar, uint32_t parity, volatile int* abort) {
+  bool ok;
+  int i = 0;
+  do ok = tc::mbar_try_wait(bar, parity);
+  while (!ok && ++i < kTries && *abort == 0);
+  if (!ok) *abort = 1;
+  return ok;
 }
 
 // One lane of a converged warp.
@@ -157,14 +174,14 @@ __device__ __forceinline__ bool elect_one() {
 // One arrival for a warp whose lanes have all done their part.
 __device__ __forceinline__ void warp_arrive(uint32_t bar) {
   __syncwarp();
-  if ((threadIdx.x & 31) == 0) tc::mbar_arrive(bar);
+  tc::mbar_arrive_if((threadIdx.x & 31) == 0, bar);
 }
 
-// Registers: 512 threads start with 128 each. The softmax warps (two warpgroups) take 168, the
-// other two warpgroups keep 88: 256 * (168 + 88) = 512 * 128.
+// Registers: 512 threads start with 128 each. The softmax warps (two warpgroups) take 200, the
+// other two warpgroups keep 56: 256 * (200 + 56) = 512 * 128.
 constexpr int kLaunchRegs = 128;
-__device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 168;"); }
-__device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 88;"); }
+__device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 200;"); }
+__device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 56;"); }
 
 // All threads, from their own roles' code.
 __device__ __forceinline__ void cta_sync() { asm volatile("bar.sync 0;" ::: "memory"); }
@@ -175,10 +192,13 @@ __device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, 256;" ::
 // 16-byte chunk c of row r of a 128-byte-row slab, in the 128-byte swizzle
 __device__ __forceinline__ uint32_t swz(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
 
-// A row of q (64 words of two bf16) to TMEM as hi and lo E4M3 codes (32 columns of four each);
+// A row of q (bf16) to TMEM as hi and lo E4M3 codes (32 columns of four each);
 // returns the factor that the codes have to be multiplied by. (A row with an infinity or NaN gets
 // a NaN code.)
-__device__ __forceinline__ float split_row(const uint32_t* w, uint32_t tq) {
+__device__ __forceinline__ float split_row(const uint4* row, uint32_t tq) {
+  uint32_t w[64];
+#pragma unroll
+  for (int k = 0; k < 16; ++k) w[4 * k] = row[k].x, w[4 * k + 1] = row[k].y, w[4 * k + 2] = row[k].z, w[4 * k + 3] = row[k].w;
   uint32_t top = 0;
 #pragma unroll
   for (int i = 0; i < 64; ++i) top = max(top, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
@@ -266,11 +286,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   const Split sp = split_of(P, N, p.splits, split);
   const int nb = sp.nb, nt = sp.nt;
-  // slot 0 takes every block (its first 64 keys), slot 1 the prefix blocks with more than 64
-  auto second = [&](int i) { return i >= nt && sp.pg_lo + (i - nt) * kPages + kPages / 2 < sp.pg_hi; };
-  const bool both = nb > nt && second(nt);  // slot 1 has work
+  const bool both = nb > 1;  // the second group has work
 
-  // softmax threads: slot, row, and what the row stands for
+  // softmax threads: group, row, and what the row stands for
   const int slot = warp >= 8 ? 1 : 0;
   const int row = threadIdx.x & 127;
   const int node = node0 + row / p.G;
@@ -290,36 +308,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto bar = [&](uint64_t* x) { return tc::smem_u32(x); };
   volatile int* abort = &bars.abort;
   if (warp == 0) {
-    if (lane == 0) {
-      tc::mbar_init(bar(&bars.q16), 4);
-      tc::mbar_init(bar(&bars.q8), 4);
-      for (int t = 0; t < 2; ++t) {
-        tc::mbar_init(bar(&bars.s_full[t]), 1);
-        tc::mbar_init(bar(&bars.s_free[t]), 4);  // one arrival per softmax warp
-        tc::mbar_init(bar(&bars.p_full[t]), 4);
-        tc::mbar_init(bar(&bars.pv_done[t]), 1);
-        tc::mbar_init(bar(&bars.o_full[t]), 1);
-      }
-      for (int s = 0; s < kStK; ++s) {
-        tc::mbar_init(bar(&bars.k_full[s]), 1);
-        tc::mbar_init(bar(&bars.k_empty[s]), 2);  // both issuers
-      }
-      for (int s = 0; s < kStC; ++s) {
-        tc::mbar_init(bar(&bars.c_full[s]), 1);
-        tc::mbar_init(bar(&bars.c_empty[s]), 4);
-      }
-      for (int s = 0; s < kStV; ++s) {
-        tc::mbar_init(bar(&bars.v_full[s]), 4);
-        tc::mbar_init(bar(&bars.v_empty[s]), 2);
-      }
-      for (int s = 0; s < kScales; ++s) tc::mbar_init(bar(&bars.sc_full[s]), 1);
-      for (int s = 0; s < kMaxTreeBlocks; ++s) bars.bad[s] = 0;
-      bars.abort = 0;
-      tc::mbar_fence_init();
-    }
+    uint64_t* all = reinterpret_cast<uint64_t*>(&bars);
+    for (int x = lane; x < kBarAll; x += 32) tc::mbar_init(bar(all + x), x < kBar1 ? 1 : 4);
+    if (lane < kMaxTreeBlocks) bars.bad[lane] = 0;
+    if (lane == 0) bars.abort = 0;
+    tc::mbar_fence_init();
   } else if (warp == 1) {
     tc::tmem_alloc(bar(reinterpret_cast<uint64_t*>(&bars.tmem)), kTmemCols);
     tc::tmem_relinquish();
+  }
+  // in flight over the setup: q's rows (to L2), the producers' first page ids
+  int ids0 = p.num_pages;
+  if (warp >= kSoft0 && warp < kCvt) {
+    if (valid) asm volatile("prefetch.global.L2 [%0];" ::"l"(p.q + orow * kD + 64 * slot));
+  } else if ((warp == 0 || warp == 3) && sp.pg_lo + lane < sp.pg_hi) {
+    ids0 = __ldg(p.page_table + (size_t)b * p.max_pages + sp.pg_lo + lane);
   }
   tc::fence_before_sync();
   __syncthreads();
@@ -328,186 +331,166 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   float m = -INFINITY, l = 0.f;  // softmax threads: running maximum and sum
   bool ok = true;
-
-  if (warp < kSoft0) regs_down();  // (by the whole warpgroup at once)
-  if (warp == 0 || warp == 3) {
-    // ------------------------------------------------------------------ TMA producers
-    // Warp 0 loads K and the pages' scales, warp 3 V's codes (one warp issuing all 16 copies of
-    // a block was the slowest of its parts). Page ids of four blocks at a time, one per lane,
-    // a batch ahead of their use; an id is checked when its batch comes up.
-    const bool isv = warp == 3;
-    const int kSt = isv ? kStC : kStK;
-    uint64_t* full = isv ? bars.c_full : bars.k_full;
-    uint64_t* empty = isv ? bars.c_empty : bars.k_empty;
-    const uint32_t ring = sb + (isv ? kOffC : kOffK);
-    const CUtensorMap* tm_tree = isv ? &tm_vt : &tm_kt;
-    const CUtensorMap* tm_pool = isv ? &tm_vp : &tm_kp;
-    auto ids_of = [&](int k) -> int {
-      const int lp = sp.pg_lo + 32 * k + lane;
-      return lp < sp.pg_hi ? __ldg(p.page_table + (size_t)b * p.max_pages + lp) : p.num_pages;
-    };
-    auto checked = [&](int page, int k) -> int {
-      if (page >= 0 && page < p.num_pages) return page;
-      if (!isv && sp.pg_lo + 32 * k + lane < sp.pg_hi) report(p.status, SPEC_ERR_PAGE);
-      return p.num_pages;  // out of range: TMA reads zeros
-    };
-    auto scale_of = [&](int page) {
-      return !isv && page < p.num_pages ? __ldg(p.kv_scale + (size_t)page * p.hkv + g) : make_float2(1.f, 1.f);
-    };
-    int ids = checked(ids_of(0), 0), ids_next = ids_of(1);
-    float2 sc = scale_of(ids), sc_next = make_float2(1.f, 1.f);
-    int done = 0;  // blocks whose copies were issued
-    for (int i = 0, st = 0, turn = 0; i < nb; ++i, ++st) {
-      if (st == kSt) st = 0, ++turn;
-      if (turn > 0 && !wait_all(bar(&empty[st]), (turn & 1) ^ 1, abort)) break;
-      const uint32_t dst = ring + st * kSlab;
-      if (lane == 0) tc::mbar_arrive_expect_tx(bar(&full[st]), kSlab);
-      __syncwarp();
-      if (i < nt) {
-        if (lane < 2)  // two 64-column halves
-          tc::tma_load_3d(dst + lane * kTreeSlab, tm_tree, bar(&full[st]), lane * 64, g,
-                          base + (sp.tb_lo + i) * kTreeKeys);
-      } else {
-        const int j = i - nt;
-        if (j > 0 && (j & 3) == 0) {
-          ids = ids_next;
-          sc = sc_next;
-          ids_next = ids_of((j >> 2) + 1);
-        }
-        const int from = (j & 3) * kPages + (lane & 7);
-        const int page = __shfl_sync(0xffffffffu, ids, from);
-        if (lane < kPages) tc::tma_load_4d(dst + lane * 2048, tm_pool, bar(&full[st]), 0, 0, g, page);
-        if ((j & 3) == 2) {
-          ids_next = checked(ids_next, (j >> 2) + 1);
-          sc_next = scale_of(ids_next);
-        }
-        if (!isv) {
-          const float ks = page_scale(__shfl_sync(0xffffffffu, sc.x, from));
-          const float vs = page_scale(__shfl_sync(0xffffffffu, sc.y, from));
-          if (lane < kPages)
-            *reinterpret_cast<float4*>(smem + kOffScale + ((j % kScales) * kPages + lane) * 16) =
-                make_float4(ks, log2f(vs), 1.f / vs, 0.f);
-          warp_arrive(bar(&bars.sc_full[j % kScales]));
-        }
-      }
-      done = i + 1;
-    }
-    if (done < nb && lane == 0) {  // given up: leave no copy in flight
-      report(p.status, SPEC_ERR_TIMEOUT);
-      int zero = 0;
-      for (int i = max(0, done - kSt); i < done; ++i)
-        tc::mbar_wait(bar(&full[i % kSt]), (i / kSt) & 1, &zero, kWaitLimit);
-    }
-    __syncwarp();
-  } else if (warp == 1 || warp == 2) {
-    // ------------------------------------------------------------------ MMA issuers
-    // One warp per slot and one step a block: QK of the next block once the softmax holds this
-    // one's scores, then PV as P arrives. A block the slot has no step in it only passes on.
-    const int t = warp - 1;
-    const bool leader = elect_one();
-    const uint32_t to = tmem + 128 * t, ts = tmem + kColS + kSlotCols * t, tp = ts + kStep;
-    int n = 0;  // the slot's steps so far
-    // QK of a prefix block into S
-    auto qk = [&](int i) {
-      const int sk = i % kStK;
-      ok = ok && wait_all(bar(&bars.k_full[sk]), (i / kStK) & 1, abort);
-      if (!ok) return;
-      tc::fence_after_sync();
-      const uint64_t kd = tc::sdesc_sw128(sb + kOffK + sk * kSlab + t * (kStep * 128), 16, 1024);
-      if (leader) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k)  // hi, then lo
-          tc::mma_f8_ts(ts, tmem + kColQ + 8 * k, kd + (((k & 3) * 32) >> 4), kIdQK, k > 0);
-        tc::mma_commit(bar(&bars.s_full[t]));
-        tc::mma_commit(bar(&bars.k_empty[sk]));
-      }
-      __syncwarp();
-    };
-    // a block that the slot has no step in: released once its stages are this block's (an arrival
-    // must not count for an earlier one)
-    auto pass = [&](int i) {
-      ok = ok && wait_all(bar(&bars.k_full[i % kStK]), (i / kStK) & 1, abort);
-      if (ok && leader) tc::mbar_arrive(bar(&bars.k_empty[i % kStK]));
-      ok = ok && wait_all(bar(&bars.v_full[i % kStV]), (i / kStV) & 1, abort);
-      if (ok && leader) tc::mbar_arrive(bar(&bars.v_empty[i % kStV]));
-      __syncwarp();
-    };
-    // the tree, slot 0's: QK, then PV (P's second term lies where S was, so the next QK follows it)
-    if (nt > 0 && t == 0) ok = wait_all(bar(&bars.q16), 0, abort);
-#pragma unroll 1
-    for (int i = 0; ok && i < nt; ++i) {
-      const int sk = i % kStK, sv = i % kStV;
-      if (t == 1) {
-        pass(i);
-        continue;
-      }
-      ok = wait_all(bar(&bars.k_full[sk]), (i / kStK) & 1, abort);
-      if (!ok) break;
-      tc::fence_after_sync();
-      if (leader) {
-        const uint64_t kd = tc::sdesc_sw128(sb + kOffK + sk * kSlab, 16, 1024);
-#pragma unroll 1
-        for (int k = 0; k < 8; ++k)
-          tc::mma_bf16_ts(ts, tmem + kColQ + 8 * k, kd + (((k >> 2) * kTreeSlab + (k & 3) * 32) >> 4), kIdTreeQK, k > 0);
-        tc::mma_commit(bar(&bars.s_full[0]));
-        tc::mma_commit(bar(&bars.k_empty[sk]));
-      }
-      __syncwarp();
-      ok = wait_all(bar(&bars.s_free[0]), n & 1, abort) && wait_all(bar(&bars.v_full[sv]), (i / kStV) & 1, abort) &&
-           wait_all(bar(&bars.p_full[0]), n & 1, abort);
-      if (!ok) break;
-      tc::fence_after_sync();
-      if (leader) {
-        const uint64_t vd = tc::sdesc_sw128(sb + kOffV + sv * 2 * kSlab, kSlab, 1024);
-#pragma unroll 1
-        for (int k = 0; k < 8; ++k)  // four steps of 16 nodes for each term
-          tc::mma_bf16_ts(to, (k < 4 ? tp : ts - 32) + 8 * k, vd + (((k & 3) * 2048) >> 4), kIdTreePV, n > 0 || k > 0);
-        tc::mma_commit(bar(&bars.pv_done[0]));
-        tc::mma_commit(bar(&bars.v_empty[sv]));
-      }
-      __syncwarp();
-      ++n;
-    }
-    // the prefix
-    const int last = t == 0 || nb == nt || second(nb - 1) ? nb : nb - 1;  // (only the last block can lack a half)
-    if (ok && last > nt) {
-      ok = wait_all(bar(&bars.q8), 0, abort);
-      qk(nt);
-    }
-#pragma unroll 1
-    for (int i = nt; ok && i < last; ++i, ++n) {
-      const int sv = i % kStV;
-      ok = wait_all(bar(&bars.s_free[t]), n & 1, abort);
-      if (ok && i + 1 < last) qk(i + 1);
-      ok = ok && wait_all(bar(&bars.v_full[sv]), (i / kStV) & 1, abort) &&
-           wait_all(bar(&bars.p_full[t]), n & 1, abort);
-      if (!ok) break;
-      tc::fence_after_sync();
-      const uint64_t vd = tc::sdesc_sw128(sb + kOffV + sv * 2 * kSlab + t * (kStep * 128), kSlab, 1024);
-      if (leader) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) tc::mma_bf16_ts(to, tp + 8 * k, vd + ((k * 2048) >> 4), kIdPV, n > 0 || k > 0);
-        tc::mma_commit(bar(&bars.pv_done[t]));
-        tc::mma_commit(bar(&bars.v_empty[sv]));
-      }
-      __syncwarp();
-    }
-    if (ok && last < nb) pass(last);
-    if (!ok && leader) report(p.status, SPEC_ERR_TIMEOUT);
-    // every product issued has completed before O is read and TMEM released
-    if (leader) tc::mma_commit(bar(&bars.o_full[t]));
+  // An issuer's end: every product it issued has completed before O is read and TMEM released.
+  auto finish = [&](int which) {
+    if (!ok) report(p.status, SPEC_ERR_TIMEOUT);
+    tc::mma_commit(bar(&bars.all_done[which]));
     int zero = 0;
-    tc::mbar_wait(bar(&bars.o_full[t]), 0, &zero, kWaitLimit);
-    __syncwarp();
+    tc::mbar_wait(bar(&bars.all_done[which]), 0, &zero, kWaitLimit);
+  };
+
+  if (warp < kSoft0) {
+    regs_down();  // (by the whole warpgroup at once)
+    if (warp == 0 || warp == 3) {
+      // ------------------------------------------------------------------ TMA producers
+      // Warp 0 loads K and the pages' scales, warp 3 V's codes (one warp issuing all 16 copies of
+      // a block was the slowest of its parts). Page ids of four blocks at a time, one per lane,
+      // a batch ahead of their use; an id is checked when its batch comes up.
+      const bool isv = warp == 3;
+      const uint32_t leader = elect_one();
+      const int kSt = isv ? kStC : kStK;
+      uint64_t* full = isv ? bars.c_full : bars.k_full;
+      uint64_t* empty = isv ? bars.c_empty : bars.k_empty;
+      const uint32_t ring = sb + (isv ? kOffC : kOffK);
+      const CUtensorMap* tm_tree = isv ? &tm_vt : &tm_kt;
+      const CUtensorMap* tm_pool = isv ? &tm_vp : &tm_kp;
+      auto ids_of = [&](int k) -> int {
+        const int lp = sp.pg_lo + 32 * k + lane;
+        return lp < sp.pg_hi ? __ldg(p.page_table + (size_t)b * p.max_pages + lp) : p.num_pages;
+      };
+      auto checked = [&](int page, int k) -> int {
+        if (page >= 0 && page < p.num_pages) return page;
+        if (!isv && sp.pg_lo + 32 * k + lane < sp.pg_hi) report(p.status, SPEC_ERR_PAGE);
+        return p.num_pages;  // out of range: TMA reads zeros
+      };
+      auto scale_of = [&](int page) {
+        return !isv && page < p.num_pages ? __ldg(p.kv_scale + (size_t)page * p.hkv + g) : make_float2(1.f, 1.f);
+      };
+      int ids = ids0, ids_next = ids_of(1);
+      float2 sc = make_float2(1.f, 1.f), sc_next = sc;
+      int done = 0;  // blocks whose copies were issued
+      for (int i = 0, st = 0, turn = 0; i < nb; ++i, ++st) {
+        if (st == kSt) st = 0, ++turn;
+        if (turn > 0 && !wait_all(bar(&empty[st]), (turn & 1) ^ 1, abort)) break;
+        const uint32_t dst = ring + st * kSlab;
+        // (one lane issues, the others' part predicated off: a copy by each of eight lanes cost about
+        // 60 cycles more a copy)
+        tc::expect_tx_if(leader, bar(&full[st]), kSlab);
+        if (i < nt) {
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h)  // two 64-column halves
+            tc::tma_load_3d_if(leader, dst + h * kTreeSlab, tm_tree, bar(&full[st]), h * 64, g,
+                               base + (sp.tb_lo + i) * kTreeKeys);
+        } else {
+          const int j = i - nt;
+          if (j == 0) {
+            ids = checked(ids, 0);
+            sc = scale_of(ids);
+          } else if ((j & 3) == 0) {
+            ids = ids_next;
+            sc = sc_next;
+            ids_next = ids_of((j >> 2) + 1);
+          }
+#pragma unroll 1
+          for (int pp = 0; pp < kPages; ++pp) {
+            const int page = __shfl_sync(0xffffffffu, ids, (j & 3) * kPages + pp);
+            tc::tma_load_4d_if(leader, dst + pp * 2048, tm_pool, bar(&full[st]), 0, 0, g, page);
+          }
+          if ((j & 3) == 2) {
+            ids_next = checked(ids_next, (j >> 2) + 1);
+            sc_next = scale_of(ids_next);
+          }
+          if (!isv && (j & 3) == 0) {
+            // the scales of these four blocks; what their places held, twelve to nine blocks ago, has
+            // been read: the stage just filled was released by QK of four blocks ago, which waited until
+            // S of five and of six blocks ago was in registers, one of each group
+            const float vs = page_scale(sc.y);
+            *reinterpret_cast<float4*>(smem + kOffScale + ((j % kScales) * kPages + lane) * 16) =
+                make_float4(page_scale(sc.x), log2f(vs), 1.f / vs, 0.f);
+            warp_arrive(bar(&bars.sc_full[(j >> 2) & 1]));
+          }
+        }
+        done = i + 1;
+      }
+      if (done < nb && lane == 0) {  // given up: leave no copy in flight
+        report(p.status, SPEC_ERR_TIMEOUT);
+        int zero = 0;
+        for (int i = max(0, done - kSt); i < done; ++i)
+          tc::mbar_wait(bar(&full[i % kSt]), (i / kSt) & 1, &zero, kWaitLimit);
+      }
+      __syncwarp();
+    } else if (warp == 1) {
+      // ------------------------------------------------------------------ MMA issuer: QK
+      // (A warp's instructions that follow its products wait until the tensor cores have taken
+      // those up: one warp issuing QK and PV in turn could not prepare the one under the other.)
+      if (elect_one()) {
+        const uint32_t ts = tmem + kColS;
+#pragma unroll 1
+        for (int i = 0; i < nb; ++i) {
+          const int sk = i % kStK;
+          if (i == 0 && nt > 0) ok = wait_one(bar(&bars.q16), 0, abort);
+          if (i == nt) ok = ok && wait_one(bar(&bars.q8), 0, abort);
+          ok = ok && wait_one(bar(&bars.k_full[sk]), (i / kStK) & 1, abort);
+          if (i > 0) ok = ok && wait_one(bar(&bars.s_free), (i - 1) & 1, abort);  // the block before has left S
+          if (!ok) break;
+          tc::fence_after_sync();
+          const uint64_t kd = tc::sdesc_sw128(sb + kOffK + sk * kSlab, 16, 1024);
+          if (i < nt) {
+            const uint64_t qd = tc::sdesc_sw128(sb + kOffQ, 16, 1024);
+#pragma unroll 1
+            for (int k = 0; k < 8; ++k)
+              tc::mma_bf16(ts, qd + (((k >> 2) * kSlab + (k & 3) * 32) >> 4),
+                           kd + (((k >> 2) * kTreeSlab + (k & 3) * 32) >> 4), kIdTreeQK, k > 0);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)  // hi, then lo
+              tc::mma_f8_ts(ts, tmem + kColQ + 8 * k, kd + (((k & 3) * 32) >> 4), kIdQK, k > 0);
+          }
+          tc::mma_commit(bar(&bars.s_full[i & 1]));
+          tc::mma_commit(bar(&bars.k_empty[sk]));
+        }
+        finish(0);
+      }
+      __syncwarp();
+    } else {
+      // ------------------------------------------------------------------ MMA issuer: PV
+      if (elect_one()) {
+        const uint32_t tp = tmem + kColP;
+#pragma unroll 1
+        for (int i = 0; i < nb; ++i) {
+          const int sv = i % kStV;
+          ok = wait_one(bar(&bars.v_full[sv]), (i / kStV) & 1, abort) && wait_one(bar(&bars.p_full), i & 1, abort);
+          if (!ok) break;
+          tc::fence_after_sync();
+          const uint64_t vd = tc::sdesc_sw128(sb + kOffV + sv * 2 * kSlab, kSlab, 1024);
+          const uint32_t to = tmem + 128 * (i & 1);
+          if (i < nt) {
+#pragma unroll 1
+            for (int k = 0; k < 8; ++k)  // P's two bf16 terms, four steps of 16 nodes each
+              tc::mma_bf16_ts(to, tp + 8 * k, vd + (((k & 3) * 2048) >> 4), kIdTreePV, i > 1 || k > 0);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) tc::mma_bf16_ts(to, tp + 8 * k, vd + ((k * 2048) >> 4), kIdPV, i > 1 || k > 0);
+          }
+          tc::mma_commit(bar(&bars.pv_done[i & 1]));
+          tc::mma_commit(bar(&bars.v_empty[sv]));
+        }
+        finish(1);
+      }
+      __syncwarp();
+    }
   } else if (warp >= kCvt) {
     regs_down();
     // ------------------------------------------------------------------ V converters
     const int ct = threadIdx.x - kCvt * 32;
+    const int r0 = (ct & 7) | ((ct >> 6) << 3), cc = (ct >> 3) & 7;
+    const uint32_t src0 = swz(r0, cc);
+    const uint32_t dst0 = (cc >> 2) * kSlab + swz(r0, (cc & 3) * 2), dst1 = (cc >> 2) * kSlab + swz(r0, (cc & 3) * 2 + 1);
+    const int tail = min(P, sp.pg_hi * 16) - (sp.pg_lo + (nb - 1 - nt) * kPages) * 16;  // rows of the last block
     for (int i = 0; i < nb; ++i) {
       const int sc_ = i % kStC, sv = i % kStV;
-      if (!wait_all(bar(&bars.c_full[sc_]), (i / kStC) & 1, abort) ||
-          (i >= kStV && !wait_all(bar(&bars.v_empty[sv]), ((i / kStV) & 1) ^ 1, abort))) {
-        if (lane == 0) report(p.status, SPEC_ERR_TIMEOUT);
+      if (!wait_all(bar(&bars.c_full[sc_]), (i / kStC) & 1, abort)) {
+        ok = false;
         break;
       }
       const uint8_t* src = smem + kOffC + sc_ * kSlab;
@@ -516,6 +499,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // bf16 rows as they are, but for rows past the tree and elements that are not finite
         // (a weight of 0 times either would reach rows whose mask leaves the node out)
         const int tb = sp.tb_lo + i, nvalid = N - tb * kTreeKeys;
+        if (i >= kStV) ok = wait_all(bar(&bars.v_empty[sv]), ((i / kStV) & 1) ^ 1, abort);
+        if (!ok) break;
 #pragma unroll 1
         for (int it = 0; it < 8; ++it) {
           const int id = it * 128 + ct, half = id >> 9, off = id & 511, r = off >> 3;
@@ -538,126 +523,143 @@ __global__ void __launch_bounds__(kThreads, 1)
           *reinterpret_cast<uint4*>(dst + half * kSlab + off * 16) = make_uint4(u[0], u[1], u[2], u[3]);
         }
       } else {
-        const int pg = sp.pg_lo + (i - nt) * kPages;
-        const int nvalid = min(P, sp.pg_hi * 16) - pg * 16;  // rows past it may hold anything
-#pragma unroll 4
-        for (int it = 0; it < 8; ++it) {
-          const int id = it * 128 + ct;
-          const int r = (id & 7) | ((id >> 6) << 3), cc = (id >> 3) & 7;
-          uint4 w = *reinterpret_cast<const uint4*>(src + swz(r, cc));
-          if (r >= nvalid) w = make_uint4(0, 0, 0, 0);
-          const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-          uint32_t h[8];
+        // 16 codes a piece: row r0 + 16 it, chunk cc (8 lanes take 8 rows, so that loads and stores
+        // meet 8 different 16-byte columns; the swizzle depends on r % 8 alone, the same in every
+        // piece of a thread)
+        if (i == nb - 1) {  // rows past the prefix may hold anything (each thread clears what it will read)
+#pragma unroll 1
+          for (int r = r0; r < kKeys; r += 16)
+            if (r >= tail) *reinterpret_cast<uint4*>(smem + kOffC + sc_ * kSlab + src0 + (r - r0) * 128) = make_uint4(0, 0, 0, 0);
+        }
+        if (i >= kStV) ok = wait_all(bar(&bars.v_empty[sv]), ((i / kStV) & 1) ^ 1, abort);
+        if (!ok) break;
+#pragma unroll 1
+        for (int part = 0; part < 8; part += 4) {
+          uint4 w[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            h[2 * k] = half2_of((uint16_t)(u[k] & 0xFFFFu));
-            h[2 * k + 1] = half2_of((uint16_t)(u[k] >> 16));
+          for (int it = 0; it < 4; ++it) w[it] = *reinterpret_cast<const uint4*>(src + src0 + (part + it) * 2048);
+#pragma unroll
+          for (int it = 0; it < 4; ++it) {
+            const uint32_t u[4] = {w[it].x, w[it].y, w[it].z, w[it].w};
+            uint32_t h[8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              h[2 * k] = half2_of((uint16_t)(u[k] & 0xFFFFu));
+              h[2 * k + 1] = half2_of((uint16_t)(u[k] >> 16));
+            }
+            *reinterpret_cast<uint4*>(dst + dst0 + (part + it) * 2048) = make_uint4(h[0], h[1], h[2], h[3]);
+            *reinterpret_cast<uint4*>(dst + dst1 + (part + it) * 2048) = make_uint4(h[4], h[5], h[6], h[7]);
           }
-          uint8_t* to = dst + (cc >> 2) * kSlab;
-          *reinterpret_cast<uint4*>(to + swz(r, (cc & 3) * 2)) = make_uint4(h[0], h[1], h[2], h[3]);
-          *reinterpret_cast<uint4*>(to + swz(r, (cc & 3) * 2 + 1)) = make_uint4(h[4], h[5], h[6], h[7]);
         }
       }
       tc::fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        tc::mbar_arrive(bar(&bars.v_full[sv]));
-        tc::mbar_arrive(bar(&bars.c_empty[sc_]));
-      }
+      warp_arrive(bar(&bars.v_full[sv]));
+      warp_arrive(bar(&bars.c_empty[sc_]));
     }
+    if (!ok && lane == 0) report(p.status, SPEC_ERR_TIMEOUT);
   } else if (warp >= kSoft0) {
     regs_up();
     // ------------------------------------------------------------------ softmax
     const uint32_t quarter = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t ts = tmem + kColS + kSlotCols * slot + quarter, tp = ts + kStep, to = tmem + 128 * slot + quarter;
+    const uint32_t ts = tmem + kColS + quarter, tp = tmem + kColP + quarter, to = tmem + 128 * slot + quarter;
     const uint32_t tq = tmem + kColQ + quarter;
     const bool live = __any_sync(0xffffffffu, valid);  // a warp without rows only keeps step
-    const uint64_t* mrow = p.mask + (size_t)(base + node) * p.mask_words;
     const float scale_log2 = p.scale_log2;
-    float* factors = reinterpret_cast<float*>(smem + kOffJoin);  // [row], from slot 0 to slot 1
-    float qf = 0.f;  // the factor of the row's codes
-    int n = 0;       // the slot's steps so far
-    auto load_q = [&](uint32_t* w) {
+    float* factors = reinterpret_cast<float*>(smem + kOffJoin);  // [row], from the second group to the first
+    auto load_q = [&](uint4* w) {
       const uint4* src = reinterpret_cast<const uint4*>(p.q + orow * kD);
 #pragma unroll
-      for (int k = 0; k < 16; ++k) {
-        const uint4 u = valid ? __ldg(src + k) : make_uint4(0, 0, 0, 0);
-        w[4 * k] = u.x, w[4 * k + 1] = u.y, w[4 * k + 2] = u.z, w[4 * k + 3] = u.w;
-      }
+      for (int k = 0; k < 16; ++k) w[k] = valid ? __ldg(src + k) : make_uint4(0, 0, 0, 0);
     };
     // A step begins with its S complete and ends with its P handed on. In between, M follows the
-    // row's maximum; where it moves, O is rescaled. PV of the step before is complete by then: it
-    // is waited for first, as this step's P overwrites what it read. (Warps without rows wait for
-    // it too, else their arrivals could run a step ahead of the others'.)
-    auto begin_step = [&]() {
-      ok = wait_all(bar(&bars.s_full[slot]), n & 1, abort);
+    // row's maximum, and O is rescaled where it moves, after this group's PV before. Before P is
+    // written, PV of the block before, the other group's, has to have read what stands there: as
+    // late as that goes. (Warps without rows wait for it too, else their arrivals could run a step
+    // ahead of the others'.)
+    auto begin_step = [&](int i) {
+      ok = wait_all(bar(&bars.s_full[slot]), (i >> 1) & 1, abort);
       tc::fence_after_sync();
       return ok;
     };
-    auto raise = [&](float mx) {
-      float alpha = 1.f;
-      bool rescale = false;
-      if (mx > -INFINITY && (m == -INFINITY || mx > m + kGrow)) {
-        alpha = m == -INFINITY ? 0.f : ex2_approx(m - mx);
-        m = mx;
-        l *= alpha;
-        rescale = n > 0;
-      }
-      if (n > 0) ok = wait_all(bar(&bars.pv_done[slot]), (n - 1) & 1, abort);
-      if (__any_sync(0xffffffffu, rescale)) {
-        tc::fence_after_sync();
+    auto s_loaded = [&]() {
+      tc::fence_before_sync();
+      warp_arrive(bar(&bars.s_free));  // QK of the next block may overwrite S
+    };
+    auto raise = [&](int i, float mx) {
+      const bool moves = mx > -INFINITY && (m == -INFINITY || mx > m + kGrow);
+      if (__any_sync(0xffffffffu, moves)) {
+        float alpha = 1.f;
+        if (moves) {
+          alpha = m == -INFINITY ? 0.f : ex2_approx(m - mx);
+          m = mx;
+          l *= alpha;
+        }
+        if (i > 1) {
+          ok = wait_all(bar(&bars.pv_done[slot]), ((i >> 1) - 1) & 1, abort) && ok;
+          tc::fence_after_sync();
 #pragma unroll 1
-        for (int ch = 0; ch < kD / 16; ++ch) {
-          float o[16];
-          tc::tmem_ld16(to + ch * 16, o);
-          tc::tmem_wait_ld();
-          const float f = rescale ? alpha : 1.f;
+          for (int ch = 0; ch < kD / 16; ++ch) {
+            float o[16];
+            tc::tmem_ld16(to + ch * 16, o);
+            tc::tmem_wait_ld();
 #pragma unroll
-          for (int k = 0; k < 16; ++k) o[k] *= f;
-          tc::tmem_st16(to + ch * 16, o);
+            for (int k = 0; k < 16; ++k) o[k] *= alpha;
+            tc::tmem_st16(to + ch * 16, o);
+          }
         }
       }
       return m == -INFINITY ? 0.f : kShift - m;
     };
-    auto dead_step = [&]() {
-      warp_arrive(bar(&bars.s_free[slot]));
-      if (n > 0) ok = wait_all(bar(&bars.pv_done[slot]), (n - 1) & 1, abort);
+    auto wait_p = [&](int i) {
+      if (i > 0) ok = wait_all(bar(&bars.pv_done[slot ^ 1]), ((i - 1) >> 1) & 1, abort) && ok;
+      tc::fence_after_sync();
     };
     auto end_step = [&]() {
       tc::fence_before_sync();
-      if (ok) warp_arrive(bar(&bars.p_full[slot]));
-      ++n;
+      if (ok) warp_arrive(bar(&bars.p_full));
     };
-    if (slot == 0 && nt > 0) {
-      // the tree: q's row as it is, P as two bf16 terms
-      uint32_t w[64];
-      load_q(w);
-      tc::tmem_st32_u(tq, w);
-      tc::tmem_st32_u(tq + 32, w + 32);
+    if (slot == 0 && nt > 0) {  // the tree's q: its rows as they are, from shared memory
+      uint4 qrow[16];
+      load_q(qrow);
+#pragma unroll
+      for (int k = 0; k < 16; ++k) *reinterpret_cast<uint4*>(smem + kOffQ + (k >> 3) * kSlab + swz(row, k & 7)) = qrow[k];
+      tc::fence_proxy_async_smem();
+      warp_arrive(bar(&bars.q16));
+    }
+    float qf = 0.f;  // the factor of the row's codes
+    if (slot == 1 && nb > nt) {  // the prefix's: as codes
+      uint4 qrow[16];
+      load_q(qrow);
+      qf = split_row(qrow, tq);
+      factors[row] = qf;
       tc::tmem_wait_st();
       tc::fence_before_sync();
-      warp_arrive(bar(&bars.q16));
+      warp_arrive(bar(&bars.q8));
+    }
+    int i = slot;
+    if (i < nt) {
       pdl_wait();  // the mask may come from the kernel before
-      uint64_t bits = valid ? __ldcg(mrow + sp.tb_lo) : 0ull;
+      const uint64_t* mrow = p.mask + (size_t)(base + node) * p.mask_words + sp.tb_lo;
+      uint64_t bits = valid ? __ldcg(mrow + i) : 0ull;
 #pragma unroll 1
-      for (int i = 0; ok && i < nt; ++i) {
-        if (!begin_step()) break;
+      for (; ok && i < nt; i += 2) {  // P as two bf16 terms
+        if (!begin_step(i)) break;
         if (live) {
-          float s[kStep];
+          float s[kTreeKeys];
           tc::tmem_ld32(ts, s);
           tc::tmem_ld32(ts + 32, s + 32);
           tc::tmem_wait_ld();
-          tc::fence_before_sync();
-          warp_arrive(bar(&bars.s_free[0]));
+          s_loaded();
           const uint64_t see = bits;
-          if (valid && i + 1 < nt) bits = __ldcg(mrow + sp.tb_lo + i + 1);
+          if (valid && i + 2 < nt) bits = __ldcg(mrow + i + 2);
           float mx = -INFINITY;
 #pragma unroll
-          for (int c = 0; c < kStep; ++c) {
+          for (int c = 0; c < kTreeKeys; ++c) {
             s[c] = ((see >> c) & 1ull) ? s[c] * scale_log2 : -INFINITY;
             mx = fmaxf(mx, s[c]);
           }
-          const float off = raise(mx);
+          const float off = raise(i, mx);
+          wait_p(i);
           float sum0 = 0.f, sum1 = 0.f;
 #pragma unroll
           for (int h = 0; h < 4; ++h) {
@@ -671,93 +673,91 @@ __global__ void __launch_bounds__(kThreads, 1)
               lo[c] = pack_bf16x2(a - __uint_as_float(hi[c] << 16), d - __uint_as_float(hi[c] & 0xFFFF0000u));
             }
             tc::tmem_st8_u(tp + 8 * h, hi);
-            tc::tmem_st8_u(ts + 8 * h, lo);
+            tc::tmem_st8_u(tp + 32 + 8 * h, lo);
           }
           l += sum0 + sum1;
           tc::tmem_wait_st();
         } else {
-          dead_step();
+          s_loaded();
+          wait_p(i);
         }
         end_step();
       }
     }
-    if (ok && nb > nt) {
-      // the prefix: q as codes, from slot 0 (which has S of every tree block, so that the rows in
-      // their place have been read)
+    if (ok && i < nb) {
       if (slot == 0) {
-        uint32_t w[64];
-        load_q(w);
-        qf = split_row(w, tq);
-        factors[row] = qf;
-        tc::tmem_wait_st();
-        tc::fence_before_sync();
-        warp_arrive(bar(&bars.q8));
-      } else {
         ok = wait_all(bar(&bars.q8), 0, abort);
         qf = factors[row];
       }
       const float rowf = scale_log2 * qf;
-      const int np = slot == 0 || second(nb - 1) ? nb - nt : nb - nt - 1;  // (only the last block can lack a half)
+      int left = min(P, sp.pg_hi * 16) - (sp.pg_lo + (i - nt) * kPages) * 16;  // keys from this block's first on
 #pragma unroll 1
-      for (int j = 0; ok && j < np; ++j) {
-        // the page scales of the slot's half, as factors, exponents and weights of the row sum:
-        // they are there before S is
-        if (!wait_all(bar(&bars.sc_full[j % kScales]), (j / kScales) & 1, abort)) {
+      for (; ok && i < nb; i += 2, left -= 2 * kKeys) {
+        // The page scales, as factors, exponents and weights of the row sum: they are there before S
+        // is, and read before it (shared memory answers late while the other warps keep it busy).
+        const int j = i - nt;
+        if ((j & 3) < 2 && !wait_all(bar(&bars.sc_full[(j >> 2) & 1]), (j >> 3) & 1, abort)) {
           ok = false;
           break;
         }
-        const float4* scale = reinterpret_cast<const float4*>(smem + kOffScale) + (j % kScales) * kPages + 4 * slot;
-        float4 f[4];
+        const float4* scale = reinterpret_cast<const float4*>(smem + kOffScale) + (j % kScales) * kPages;
+        float pf[kPages], pe[kPages];
 #pragma unroll
-        for (int pp = 0; pp < 4; ++pp) f[pp] = scale[pp];
-        if (!begin_step()) break;
+        for (int pp = 0; pp < kPages; ++pp) {
+          const float4 f = scale[pp];
+          pf[pp] = factor(rowf, f.x);
+          pe[pp] = f.y;
+        }
+        if (!begin_step(i)) break;
         if (live) {
-          float s[kStep];
-          tc::tmem_ld32(ts, s);
-          tc::tmem_ld32(ts + 32, s + 32);
-          tc::tmem_wait_ld();
-          tc::fence_before_sync();
-          warp_arrive(bar(&bars.s_free[slot]));  // QK of the next step may overwrite S
-          const int nvalid = min(P, sp.pg_hi * 16) - (sp.pg_lo + j * kPages) * 16 - kStep * slot;
-          if (nvalid < kStep) {
-#pragma unroll
-            for (int c = 0; c < kStep; ++c) s[c] = c < nvalid ? s[c] : -INFINITY;
+          if (left < kKeys) {  // the last block's keys past the prefix
+#pragma unroll 1
+            for (int c = left; c < kKeys; ++c) tc::tmem_st1_u(ts + c, 0xFF800000u);
+            tc::tmem_wait_st();
           }
+          float s[kKeys];
+#pragma unroll
+          for (int h = 0; h < 4; ++h) tc::tmem_ld32(ts + 32 * h, s + 32 * h);
+          tc::tmem_wait_ld();
+          s_loaded();
           float mx = -INFINITY;  // the largest x log2 e + log2 vs
 #pragma unroll
-          for (int pp = 0; pp < 4; ++pp) {
+          for (int pp = 0; pp < kPages; ++pp) {
             const float* v = s + 16 * pp;
             float x = fmax3(v[0], v[1], v[2]);
 #pragma unroll
             for (int c = 3; c < 15; c += 2) x = fmax3(x, v[c], v[c + 1]);
-            f[pp].x = factor(rowf, f[pp].x);
-            mx = fmaxf(mx, fmaf(fmaxf(x, v[15]), f[pp].x, f[pp].y));
+            mx = fmaxf(mx, fmaf(fmaxf(x, v[15]), pf[pp], pe[pp]));
           }
-          const float off = raise(mx);
+          const float off = raise(i, mx);
+          uint32_t pk[kKeys / 2];
 #pragma unroll
-          for (int pp = 0; pp < 4; ++pp) {
-            const float oo = off + f[pp].y;
-            const float2 f2 = make_float2(f[pp].x, f[pp].x), o2 = make_float2(oo, oo);
+          for (int pp = 0; pp < kPages; ++pp) {
+            const float oo = off + pe[pp];
+            const float2 f2 = make_float2(pf[pp], pf[pp]), o2 = make_float2(oo, oo);
             float2 r0 = make_float2(0.f, 0.f), r1 = make_float2(0.f, 0.f);
-            uint32_t pk[8];
 #pragma unroll
             for (int c = 0; c < 16; c += 4) {
               const float* v = s + 16 * pp + c;
+              uint32_t* to2 = pk + 8 * pp + (c >> 1);
               const float2 a = ffma2(make_float2(v[0], v[1]), f2, o2);
               const float2 d = ffma2(make_float2(v[2], v[3]), f2, o2);
               const float2 ea = make_float2(ex2_approx(a.x), ex2_approx(a.y));
               const float2 ed = make_float2(ex2_approx(d.x), ex2_approx(d.y));
               r0 = fadd2(r0, ea);
               r1 = fadd2(r1, ed);
-              pk[c >> 1] = pack_f16x2(ea.x, ea.y);
-              pk[(c >> 1) + 1] = pack_f16x2(ed.x, ed.y);
+              to2[0] = pack_f16x2(ea.x, ea.y);
+              to2[1] = pack_f16x2(ed.x, ed.y);
             }
-            l = fmaf((r0.x + r0.y) + (r1.x + r1.y), f[pp].z, l);
-            tc::tmem_st8_u(tp + 8 * pp, pk);
+            l = fmaf((r0.x + r0.y) + (r1.x + r1.y), scale[pp].z, l);
           }
+          wait_p(i);
+          tc::tmem_st32_u(tp, pk);
+          tc::tmem_st32_u(tp + 32, pk + 32);
           tc::tmem_wait_st();
         } else {
-          dead_step();
+          s_loaded();
+          wait_p(i);
         }
         end_step();
       }
@@ -770,11 +770,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::fence_before_sync();
     cta_sync();  // every product is complete, every copy has landed
     tc::fence_after_sync();
+    // (what the row stands for is worked out again rather than kept over the loop)
+    int trow = threadIdx.x & 127;
+    asm volatile("" : "+r"(trow));
+    const int enode = node0 + trow / p.G;
+    const bool evalid = trow < p.npt * p.G && enode < N;
+    const size_t erow = (size_t)(base + enode) * p.hq + g * p.G + trow % p.G;
     float2* join = reinterpret_cast<float2*>(smem + kOffJoin);
-    join[slot * kRows + row] = make_float2(m, l);
+    join[slot * kRows + trow] = make_float2(m, l);
     soft_sync();
     if (live) {
-      const float2 a = join[row], c = both ? join[kRows + row] : make_float2(-INFINITY, 0.f);
+      const float2 a = join[trow], c = both ? join[kRows + trow] : make_float2(-INFINITY, 0.f);
       const float top = fmaxf(a.x, c.x);
       const float w0 = a.x == -INFINITY ? 0.f : ex2_approx(a.x - top), w1 = c.x == -INFINITY ? 0.f : ex2_approx(c.x - top);
       const float sum = a.y * w0 + c.y * w1;
@@ -782,7 +788,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // a tree node that this row sees holds an infinity or NaN in V
       for (int i = 0; i < nt; ++i) {
         const uint64_t bad = bars.bad[sp.tb_lo + i];
-        if (bad != 0 && valid && (__ldcg(mrow + sp.tb_lo + i) & bad) != 0) inv = __int_as_float(0x7FC00000);
+        if (bad != 0 && evalid && (__ldcg(p.mask + (size_t)(base + enode) * p.mask_words + sp.tb_lo + i) & bad) != 0) inv = __int_as_float(0x7FC00000);
       }
       if (!ok || *abort) inv = 0.f;
       const float i0 = inv * w0, i1 = inv * w1;
@@ -795,26 +801,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::tmem_ld16(o0 + 16 * ch, x);
         tc::tmem_ld16(o1 + 16 * ch, y);
         tc::tmem_wait_ld();
-        if (!valid) continue;
+        if (!evalid) continue;
 #pragma unroll
         for (int k = 0; k < 16; ++k) x[k] = both ? x[k] * i0 + y[k] * i1 : x[k] * i0;
         if (p.splits == 1) {
-          uint4* dst = reinterpret_cast<uint4*>(p.out + orow * kD + 64 * slot + 16 * ch);
+          uint4* dst = reinterpret_cast<uint4*>(p.out + erow * kD + 64 * slot + 16 * ch);
 #pragma unroll
           for (int k = 0; k < 2; ++k)
             dst[k] = make_uint4(pack_bf16x2(x[8 * k], x[8 * k + 1]), pack_bf16x2(x[8 * k + 2], x[8 * k + 3]),
                                 pack_bf16x2(x[8 * k + 4], x[8 * k + 5]), pack_bf16x2(x[8 * k + 6], x[8 * k + 7]));
         } else {
-          float4* po = p.part_o + ((size_t)tile * p.splits + split) * (kRows * kD / 4) + 16 * slot * kRows + row;
+          float4* po = p.part_o + ((size_t)tile * p.splits + split) * (kRows * kD / 4) + 16 * slot * kRows + trow;
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             po[(ch * 4 + k) * kRows] = make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
         }
       }
-      if (valid && slot == 0) {
+      if (evalid && slot == 0) {
         const float lse2 = sum == 0.f ? -INFINITY : top + log2f(sum) - kShift;
-        if (p.splits > 1) p.part_lse[((size_t)tile * p.splits + split) * kRows + row] = lse2;
-        else if (p.lse != nullptr) p.lse[orow] = lse2 * kLn2;
+        if (p.splits > 1) p.part_lse[((size_t)tile * p.splits + split) * kRows + trow] = lse2;
+        else if (p.lse != nullptr) p.lse[erow] = lse2 * kLn2;
       }
     }
   }

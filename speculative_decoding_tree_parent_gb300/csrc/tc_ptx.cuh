@@ -80,6 +80,43 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
+// The same for a whole warp with one lane's `on` set: arrivals and copies without divergence.
+__device__ __forceinline__ void mbar_arrive_if(uint32_t on, uint32_t bar) {
+  asm volatile(
+      "{ .reg .pred e; .reg .b64 st; setp.ne.b32 e, %1, 0; "
+      "@e mbarrier.arrive.shared::cta.b64 st, [%0]; }" ::"r"(bar),
+      "r"(on)
+      : "memory");
+}
+
+__device__ __forceinline__ void expect_tx_if(uint32_t on, uint32_t bar, uint32_t bytes) {
+  asm volatile(
+      "{ .reg .pred e; .reg .b64 st; setp.ne.b32 e, %2, 0; "
+      "@e mbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1; }" ::"r"(bar),
+      "r"(bytes), "r"(on)
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_load_3d_if(uint32_t on, uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0,
+                                               int c1, int c2) {
+  asm volatile(
+      "{ .reg .pred e; setp.ne.b32 e, %6, 0; "
+      "@e cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], "
+      "[%2]; }" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(on)
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_load_4d_if(uint32_t on, uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0,
+                                               int c1, int c2, int c3) {
+  asm volatile(
+      "{ .reg .pred e; setp.ne.b32 e, %7, 0; "
+      "@e cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, "
+      "%6}], [%2]; }" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(on)
+      : "memory");
+}
+
 __device__ __forceinline__ void prefetch_tmap(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
@@ -245,6 +282,10 @@ __device__ __forceinline__ void tmem_st8_u(uint32_t taddr, const uint32_t* r) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
                "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                : "memory");
+}
+
+__device__ __forceinline__ void tmem_st1_u(uint32_t taddr, uint32_t r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(r) : "memory");
 }
 
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const float* v) {
