@@ -9,11 +9,12 @@
 //
 // Bound: latency on an accepted path (sizes and path -> rows -> maximum -> stores), HBM on a
 // prompt chunk (bf16 rows read once, codes written once).
-// Layout: one CTA per (sequence, touched page, KV head), half its threads for K, half for V;
+// Layout: a CTA per (sequence, touched page, share of the KV heads), half its threads for K, half for V;
 // a thread keeps its 16-element pieces of the page in registers from the maximum to the
 // store. No two CTAs write the same page and head, so nothing is exchanged between them; each
 // makes the sequence's checks itself and comes to the same verdict.
 #include "common.cuh"
+#include "tc_host.cuh"
 
 namespace specv {
 
@@ -35,15 +36,20 @@ struct CommitP8Args {
   int32_t* status;
 };
 
-// Largest finite magnitude (bf16 bits) among eight elements; infinities and NaN do not count.
-__device__ __forceinline__ uint32_t top8(const uint4& u) {
-  uint32_t m = 0;
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+// Largest finite magnitude (bf16 bits) among sixteen elements; infinities and NaN do not count.
+__device__ __forceinline__ uint32_t top16(const uint4& u, const uint4& v) {
+  const uint32_t w[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+  uint32_t m = 0;  // of the low and of the high halves
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t lo = w[i] & 0x7FFFu, hi = (w[i] >> 16) & 0x7FFFu;
-    if (lo < 0x7F80u) m = max(m, lo);
-    if (hi < 0x7F80u) m = max(m, hi);
+  for (int i = 0; i < 8; ++i) m = __vmaxu2(m, w[i] & 0x7FFF7FFFu);
+  m = max(m & 0xFFFFu, m >> 16);
+  if (m >= 0x7F80u) {
+    m = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const uint32_t x = (w[i >> 1] >> (16 * (i & 1))) & 0x7FFFu;
+      if (x < 0x7F80u) m = max(m, x);
+    }
   }
   return m;
 }
@@ -55,9 +61,23 @@ __device__ __forceinline__ uint32_t code4(float x0, float x1, float x2, float x3
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(x3), "f"(x2));
   return (uint32_t)lo | ((uint32_t)hi << 16);
 }
-__device__ __forceinline__ uint32_t code4(uint32_t a, uint32_t b, float s) {
-  return code4(__fdiv_rn(__uint_as_float(a << 16), s), __fdiv_rn(__uint_as_float(a & 0xFFFF0000u), s),
-               __fdiv_rn(__uint_as_float(b << 16), s), __fdiv_rn(__uint_as_float(b & 0xFFFF0000u), s));
+// Sixteen codes e4m3(x / s). Scales written here are powers of two, and then the product with
+// r = 1 / s is exactly the quotient; a scale that came with the page may be any number (r = 0).
+__device__ __forceinline__ uint32_t code4(uint32_t a, uint32_t b, float r) {
+  return code4(__uint_as_float(a << 16) * r, __uint_as_float(a & 0xFFFF0000u) * r, __uint_as_float(b << 16) * r,
+               __uint_as_float(b & 0xFFFF0000u) * r);
+}
+__device__ __noinline__ uint32_t code4_div(float x0, float x1, float x2, float x3, float s) {
+  return code4(__fdiv_rn(x0, s), __fdiv_rn(x1, s), __fdiv_rn(x2, s), __fdiv_rn(x3, s));
+}
+__device__ __forceinline__ uint32_t code4_div(uint32_t a, uint32_t b, float s) {
+  return code4_div(__uint_as_float(a << 16), __uint_as_float(a & 0xFFFF0000u), __uint_as_float(b << 16),
+                   __uint_as_float(b & 0xFFFF0000u), s);
+}
+// 1 / s for a power of two s (in [2^-50, 2^50]), else 0.
+__device__ __forceinline__ float exact_inverse(float s) {
+  const uint32_t u = __float_as_uint(s);
+  return (u & 0x7FFFFFu) == 0 ? __uint_as_float(0x7F000000u - u) : 0.f;
 }
 
 // The smallest power of two s in [2^-50, 2^50] with x <= 448 s (x >= 0 given by its bf16 bits;
@@ -71,16 +91,16 @@ __device__ __forceinline__ float scale_for(uint32_t bits) {
 // kPer: 16-element pieces of a page and head that a thread holds
 template <int kPer>
 __global__ void __launch_bounds__(2 * kQcHalf) kv_commit_kv8p_kernel(const CommitP8Args p) {
-  const int b = blockIdx.x, g = blockIdx.z;
+  const int b = blockIdx.x;
   const int half = threadIdx.x / kQcHalf, tid = threadIdx.x % kQcHalf;  // 0: K, 1: V
-  __shared__ uint32_t s_top[2][kQcHalf / 32];
+  __shared__ uint32_t s_top[2][2][kQcHalf / 32];  // [head of a pair][half][warp]
   pdl_wait();
   const int base = __ldg(p.qo + b), n = __ldg(p.qo + b + 1) - base;
   const int P = __ldg(p.prefix_len + b), L = __ldg(p.accept_len + b);
   const int ps = p.page_size;
   const int32_t* path = p.path + (size_t)b * p.path_cap;
   const int32_t* table = p.page_table + (size_t)b * p.max_pages;
-  const bool lead = blockIdx.y == 0 && g == 0;
+  const bool lead = blockIdx.y == 0 && blockIdx.z == 0;
   if (L < 0 || L >= p.path_cap || L >= n || P < 0 || P > 0x7FFFFFFF - p.path_cap) {
     if (lead && threadIdx.x == 0) report(p.status, SPEC_ERR_INDEX);
     return;
@@ -91,21 +111,30 @@ __global__ void __launch_bounds__(2 * kQcHalf) kv_commit_kv8p_kernel(const Commi
   const int shift = P - lp * ps;  // > 0 on the first page where it starts inside
   const int r0 = max(shift, 0), r1 = min(ps, shift + L + 1);
   const int pieces = p.d >> 4;
-  // this thread's new rows, loaded while the sequence is checked (a bad node is not followed)
-  uint4 x[kPer][2];
-  uint32_t top = 0;
+  // where this thread's new pieces come from (head 0), -1: an older row, none, or a bad node, which
+  // is not followed
+  long from[kPer];
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int e = tid + i * kQcHalf, r = e / pieces;
-    x[i][0] = x[i][1] = make_uint4(0, 0, 0, 0);
+    from[i] = -1;
     if (r < r0 || r >= r1) continue;
     const int node = __ldg(path + r - shift);
-    if (node < 0 || node >= n) continue;
-    const uint4* src = reinterpret_cast<const uint4*>(p.tree[half] + ((size_t)(base + node) * p.hkv + g) * p.d) +
-                       2 * (e - r * pieces);
-    x[i][0] = __ldg(src);
-    x[i][1] = __ldg(src + 1);
+    if (node >= 0 && node < n) from[i] = (long)(base + node) * p.hkv * p.d + 16 * (e - r * pieces);
   }
+  auto load = [&](int g, uint4 (&x)[kPer][2]) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      x[i][0] = x[i][1] = make_uint4(0, 0, 0, 0);
+      if (from[i] < 0) continue;
+      const uint4* src = reinterpret_cast<const uint4*>(p.tree[half] + from[i] + (long)g * p.d);
+      x[i][0] = __ldg(src);
+      x[i][1] = __ldg(src + 1);
+    }
+  };
+  // the first head's rows are on their way while the sequence is checked
+  uint4 x[kPer][2];
+  load(blockIdx.z, x);
   int bad = 0;
   for (int i = threadIdx.x; i <= L; i += 2 * kQcHalf) {
     const int node = __ldg(path + i);
@@ -119,45 +148,59 @@ __global__ void __launch_bounds__(2 * kQcHalf) kv_commit_kv8p_kernel(const Commi
     if (bad) break;
   }
   if (bad && lead) report(p.status, bad);
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) top = max(top, max(top8(x[i][0]), top8(x[i][1])));
-  top = __reduce_max_sync(0xffffffffu, top);
-  if ((tid & 31) == 0) s_top[half][tid >> 5] = top;
   if (__syncthreads_or(bad)) return;
+  const size_t page = (size_t)__ldg(table + lp);
+  int turn = 0;
+  for (int g = blockIdx.z; g < p.hkv; g += gridDim.z, turn ^= 1) {
+    const size_t unit = page * p.hkv + g;
+    float* sp = p.kv_scale + unit * 2 + half;
+    const float old = r0 > 0 ? *sp : 0.f;  // (read by every thread before the barrier, written after it)
+    uint32_t top = 0;
 #pragma unroll
-  for (int w = 0; w < kQcHalf / 32; ++w) top = max(top, s_top[half][w]);
-  const size_t unit = (size_t)__ldg(table + lp) * p.hkv + g;
-  float* sp = p.kv_scale + unit * 2 + half;
-  uint8_t* codes = p.pool[half] + unit * ps * p.d;
-  float now = scale_for(top);
-  float was = now;
-  if (r0 > 0) {
-    was = page_scale(*sp);
-    now = fmaxf(now, was);
-  }
-  __syncthreads();  // every thread has read the old scale
+    for (int i = 0; i < kPer; ++i) top = max(top, top16(x[i][0], x[i][1]));
+    top = __reduce_max_sync(0xffffffffu, top);
+    if ((tid & 31) == 0) s_top[turn][half][tid >> 5] = top;
+    // the next head's rows, while this one's are joined, turned into codes and stored
+    uint4 y[kPer][2];
+    if (g + gridDim.z < p.hkv) load(g + gridDim.z, y);
+    __syncthreads();
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int e = tid + i * kQcHalf, r = e / pieces;
-    if (r >= r1) continue;
-    uint4* dst = reinterpret_cast<uint4*>(codes) + e;  // rows are contiguous: piece e of the page
-    if (r >= r0) {
-      *dst = make_uint4(code4(x[i][0].x, x[i][0].y, now), code4(x[i][0].z, x[i][0].w, now),
-                        code4(x[i][1].x, x[i][1].y, now), code4(x[i][1].z, x[i][1].w, now));
-    } else if (now != was) {
-      const uint4 c = *dst;
-      const uint32_t in[4] = {c.x, c.y, c.z, c.w};
-      uint32_t out[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float4 v = e4m3x4_to_f32(in[k]);
-        out[k] = code4(__fdiv_rn(v.x * was, now), __fdiv_rn(v.y * was, now), __fdiv_rn(v.z * was, now),
-                       __fdiv_rn(v.w * was, now));
-      }
-      *dst = make_uint4(out[0], out[1], out[2], out[3]);
+    for (int w = 0; w < kQcHalf / 32; ++w) top = max(top, s_top[turn][half][w]);
+    uint8_t* codes = p.pool[half] + unit * ps * p.d;
+    float now = scale_for(top);
+    float was = now;
+    if (r0 > 0) {
+      was = page_scale(old);
+      now = fmaxf(now, was);
     }
+    const float inv = exact_inverse(now);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int e = tid + i * kQcHalf, r = e / pieces;
+      if (r >= r1) continue;
+      uint4* dst = reinterpret_cast<uint4*>(codes) + e;  // rows are contiguous: piece e of the page
+      if (r >= r0) {
+        *dst = inv != 0.f ? make_uint4(code4(x[i][0].x, x[i][0].y, inv), code4(x[i][0].z, x[i][0].w, inv),
+                                       code4(x[i][1].x, x[i][1].y, inv), code4(x[i][1].z, x[i][1].w, inv))
+                          : make_uint4(code4_div(x[i][0].x, x[i][0].y, now), code4_div(x[i][0].z, x[i][0].w, now),
+                                       code4_div(x[i][1].x, x[i][1].y, now), code4_div(x[i][1].z, x[i][1].w, now));
+      } else if (now != was) {
+        const uint4 c = *dst;
+        const uint32_t in[4] = {c.x, c.y, c.z, c.w};
+        uint32_t out[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float4 v = e4m3x4_to_f32(in[k]);
+          out[k] = inv != 0.f ? code4(v.x * was * inv, v.y * was * inv, v.z * was * inv, v.w * was * inv)
+                              : code4_div(v.x * was, v.y * was, v.z * was, v.w * was, now);
+        }
+        *dst = make_uint4(out[0], out[1], out[2], out[3]);
+      }
+    }
+    if (tid == 0) *sp = now;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) x[i][0] = y[i][0], x[i][1] = y[i][1];
   }
-  if (tid == 0) *sp = now;
   if (lead && threadIdx.x == 0 && p.seq_len_out != nullptr) p.seq_len_out[b] = P + L + 1;
 }
 
@@ -176,7 +219,12 @@ int launch_kv_commit_kv8p(const void* k_tree, const void* v_tree, const int32_t*
                        seq_len_out, {k_pool, v_pool}, kv_scale, hkv, d, status};
   // most pages a path of path_cap nodes touches; a tree holds at most kMaxTreeNodes nodes
   const int most = path_cap < kMaxTreeNodes ? path_cap : kMaxTreeNodes;
-  const dim3 grid(batch, ceil_div(most - 1, page_size) + 1, hkv), block(2 * kQcHalf);
+  // a CTA per head while they stand on the GPU at once (its longest chain is then the shortest),
+  // else as many heads a CTA as make it so: the checks and the chain before the rows are then made
+  // once for several heads, and a head's rows are loaded under the one before it
+  const int pages = ceil_div(most - 1, page_size) + 1;
+  const long share = 16L * sm_count() / ((long)batch * pages);
+  const dim3 grid(batch, pages, (unsigned)(share < 1 ? 1 : share < hkv ? share : hkv)), block(2 * kQcHalf);
   const int per = ceil_div(page_size * (d / 16), kQcHalf);
   const cudaError_t e = per <= 1   ? launch_pdl(kv_commit_kv8p_kernel<1>, grid, block, 0, stream, p)
                         : per <= 2 ? launch_pdl(kv_commit_kv8p_kernel<2>, grid, block, 0, stream, p)

@@ -15,7 +15,8 @@
 // pages straight from the rows that give them up (the ends of shrinking rows, which nobody
 // writes); returned pages are written to places from n_free on; grants go to the entries past
 // a growing row's end. Only the two counters could be overwritten too early where they are
-// updated in place, so a second kernel, which starts after the first has ended, writes them.
+// updated in place: where there is one CTA it writes them at its end, else a second kernel does,
+// which starts after the first has ended.
 // Bound: latency for a step; the 8-byte slots' stores for a batch of prompts.
 #include "common.cuh"
 
@@ -24,6 +25,7 @@ namespace specv {
 constexpr int kPageThreads = 512;
 constexpr int kPageMaxBatch = 4096;
 constexpr int kPagePer = kPageMaxBatch / kPageThreads;
+constexpr int kPageTok = 4;  // slots a thread writes at a time: a 32-byte sector
 
 struct PageArgs {
   const int32_t* seq_len;
@@ -138,6 +140,38 @@ __device__ __forceinline__ int page_granted(const PageArgs& p, const PagePlan& s
   return at < n0 ? __ldcg(p.free_pages + at) : page_returned(p, s, at - n0);
 }
 
+// Pages granted: whole sequences in order, while they last.
+__device__ __forceinline__ int page_grants(const PagePlan& s, int batch, int n1) {
+  if (s.grow[batch - 1] <= n1) return s.grow[batch - 1];
+  const int b = page_owner(s.grow, batch, n1);
+  return b > 0 ? s.grow[b - 1] : 0;
+}
+
+// A sequence for the slot map: pages [0, keeps) stand in its row, [held, ends) are granted now,
+// from place `from` of the grants on. len -1: sizes that name no page.
+struct PageSeq {
+  int len, held, keeps, ends, from;
+};
+__device__ __forceinline__ PageSeq page_seq(const PageArgs& p, const PagePlan& s, int b, bool sane, int granted) {
+  PageSeq q{__ldg(p.seq_len + b), __ldg(p.held + b), 0, 0, b > 0 ? s.grow[b - 1] : 0};
+  if (q.held < 0 || q.held > p.max_pages) q.len = -1;
+  q.keeps = sane ? q.held - (s.back[b] - (b > 0 ? s.back[b - 1] : 0)) : q.held;
+  // (a sequence grows or shrinks, not both: held = keeps where anything is granted)
+  q.ends = sane && s.grow[b] <= granted && s.grow[b] > q.from ? q.held + s.grow[b] - q.from : q.keeps;
+  return q;
+}
+
+// The counters after the call.
+__device__ __forceinline__ void page_count(const PageArgs& p, const PagePlan& s, int n0, bool sane, int granted) {
+  for (int b = threadIdx.x; b < p.batch; b += kPageThreads) {
+    const int g0 = b > 0 ? s.grow[b - 1] : 0, r0 = b > 0 ? s.back[b - 1] : 0;
+    int now = p.held[b];
+    if (sane) now += (s.grow[b] <= granted ? s.grow[b] - g0 : 0) - (s.back[b] - r0);
+    p.held_out[b] = now;
+  }
+  if (threadIdx.x == 0) *p.n_free_out = sane ? n0 + s.back[p.batch - 1] - granted : n0;
+}
+
 __global__ void __launch_bounds__(kPageThreads) page_table_kernel(const PageArgs p) {
   __shared__ PagePlan s;
   pdl_trigger();
@@ -152,13 +186,8 @@ __global__ void __launch_bounds__(kPageThreads) page_table_kernel(const PageArgs
     else if (asked > n1) report(p.status, SPEC_ERR_CAPACITY);
   }
   const int step = gridDim.x * kPageThreads, first = blockIdx.x * kPageThreads + threadIdx.x;
-  int granted = 0;
+  const int granted = sane ? page_grants(s, p.batch, n1) : 0;
   if (sane) {
-    granted = asked;
-    if (asked > n1) {  // in order, while they last
-      const int b = page_owner(s.grow, p.batch, n1);
-      granted = b > 0 ? s.grow[b - 1] : 0;
-    }
     for (int x = first; x < granted; x += step) {
       const int b = page_owner(s.grow, p.batch, x);
       const int j = x - (b > 0 ? s.grow[b - 1] : 0);
@@ -168,25 +197,55 @@ __global__ void __launch_bounds__(kPageThreads) page_table_kernel(const PageArgs
     }
     for (int r = first; r < back - granted; r += step) p.free_pages[n0 + r] = page_returned(p, s, r);
   }
-  if (p.slot_map == nullptr) return;
-  const int last = min(p.total_nodes, __ldg(p.qo + p.batch));  // rows behind the last sequence stay as they are
-  for (int t = first; t < last; t += step) {
-    const int b = seq_of_row(p.qo, p.batch, t);
-    const int lo = __ldg(p.qo + b), len = __ldg(p.seq_len + b), held = __ldg(p.held + b);
-    long long slot = -1;
-    int page = -1;
-    if (len >= 0 && t >= lo && held >= 0 && held <= p.max_pages) {
-      const long long at = (long long)len + (t - lo);
-      const long long lp = at / p.page_size;
-      const int g0 = b > 0 ? s.grow[b - 1] : 0, r0 = b > 0 ? s.back[b - 1] : 0;
-      const int keeps = sane ? held - (s.back[b] - r0) : held;
-      if (lp < keeps) page = __ldcg(p.page_table + (size_t)b * p.max_pages + lp);
-      else if (s.grow[b] <= granted && lp < (long long)held + s.grow[b] - g0)
-        page = page_granted(p, s, n0, n1, g0 + (int)(lp - held));
-      if (page >= 0 && page < p.num_pages) slot = (long long)page * p.page_size + at % p.page_size;
-      else if (lp < keeps) report(p.status, SPEC_ERR_PAGE);
+  if (p.slot_map != nullptr) {
+    const int last = min(p.total_nodes, __ldg(p.qo + p.batch));  // rows behind the last sequence stay as they are
+    for (int t0 = first * kPageTok; t0 < last; t0 += step * kPageTok) {
+      long long slots[kPageTok];
+      int b = seq_of_row(p.qo, p.batch, t0);
+      int lo = __ldg(p.qo + b), hi = __ldg(p.qo + b + 1);
+      PageSeq q = page_seq(p, s, b, sane, granted);
+      unsigned at_page = 0xFFFFFFFFu;
+      int page = -1;
+#pragma unroll
+      for (int k = 0; k < kPageTok; ++k) {
+        const int t = t0 + k;
+        slots[k] = -1;
+        if (t >= last) continue;
+        while (t >= hi && b + 1 < p.batch) {  // the next sequence that has nodes
+          ++b;
+          lo = hi;
+          hi = __ldg(p.qo + b + 1);
+          if (t < hi) q = page_seq(p, s, b, sane, granted);
+          at_page = 0xFFFFFFFFu;
+        }
+        if (q.len < 0 || t < lo) continue;
+        const unsigned at = (unsigned)q.len + (unsigned)(t - lo), lp = at / (unsigned)p.page_size;
+        if (lp != at_page) {
+          at_page = lp;
+          page = -1;
+          if (lp < (unsigned)q.keeps) page = __ldcg(p.page_table + (size_t)b * p.max_pages + lp);
+          else if (lp < (unsigned)q.ends) page = page_granted(p, s, n0, n1, q.from + (int)lp - q.held);
+          if (lp < (unsigned)q.ends && (page < 0 || page >= p.num_pages)) {
+            if (lp < (unsigned)q.keeps) report(p.status, SPEC_ERR_PAGE);
+            page = -1;
+          }
+        }
+        if (page >= 0) slots[k] = (long long)page * p.page_size + (at - lp * (unsigned)p.page_size);
+      }
+      if (t0 + kPageTok <= last && (reinterpret_cast<uintptr_t>(p.slot_map) & 15) == 0) {
+        longlong2* dst = reinterpret_cast<longlong2*>(p.slot_map + t0);
+#pragma unroll
+        for (int k = 0; k < kPageTok / 2; ++k) dst[k] = make_longlong2(slots[2 * k], slots[2 * k + 1]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < kPageTok; ++k)
+          if (t0 + k < last) p.slot_map[t0 + k] = slots[k];
+      }
     }
-    p.slot_map[t] = slot;
+  }
+  if (gridDim.x == 1) {
+    __syncthreads();  // every read of the counters
+    page_count(p, s, n0, sane, granted);
   }
 }
 
@@ -195,21 +254,9 @@ __global__ void __launch_bounds__(kPageThreads) page_count_kernel(const PageArgs
   pdl_wait();  // the kernel before has read the counters that this one may overwrite
   const int n0 = __ldg(p.n_free);
   page_plan(p, s, false);
-  const int asked = s.grow[p.batch - 1], back = s.back[p.batch - 1];
-  const int n1 = n0 + back;
+  const int n1 = n0 + s.back[p.batch - 1];
   const bool sane = n0 >= 0 && n1 <= p.num_pages;
-  int granted = sane ? asked : 0;
-  if (sane && asked > n1) {
-    const int b = page_owner(s.grow, p.batch, n1);
-    granted = b > 0 ? s.grow[b - 1] : 0;
-  }
-  for (int b = threadIdx.x; b < p.batch; b += kPageThreads) {
-    const int g0 = b > 0 ? s.grow[b - 1] : 0, r0 = b > 0 ? s.back[b - 1] : 0;
-    int now = p.held[b];
-    if (sane) now += (s.grow[b] <= granted ? s.grow[b] - g0 : 0) - (s.back[b] - r0);
-    p.held_out[b] = now;
-  }
-  if (threadIdx.x == 0) *p.n_free_out = sane ? n1 - granted : n0;
+  page_count(p, s, n0, sane, sane ? page_grants(s, p.batch, n1) : 0);
 }
 
 int launch_page_table(const int32_t* seq_len, const int32_t* qo, const int32_t* held, int32_t* page_table,
@@ -218,11 +265,11 @@ int launch_page_table(const int32_t* seq_len, const int32_t* qo, const int32_t* 
                       long long* slot_map, int32_t* status, cudaStream_t stream) {
   const PageArgs p{seq_len,  qo,    held,        page_table, free_pages, n_free,    held_out, n_free_out,
                    slot_map, batch, total_nodes, max_pages,  num_pages,  page_size, shrink,   status};
-  const int work = slot_map != nullptr && total_nodes > batch ? total_nodes : batch;
-  const int ctas = ceil_div(work, kPageThreads);
-  if (launch_pdl(page_table_kernel, dim3(ctas < 304 ? ctas : 304), dim3(kPageThreads), 0, stream, p) != cudaSuccess)
+  const int slots = slot_map != nullptr ? ceil_div(total_nodes, kPageTok) : 0;
+  const int ctas = ceil_div(slots > batch ? slots : batch, kPageThreads);
+  if (launch_pdl(page_table_kernel, dim3(ctas < 608 ? ctas : 608), dim3(kPageThreads), 0, stream, p) != cudaSuccess)
     return SPEC_ERR_CUDA;
-  if (launch_pdl(page_count_kernel, dim3(1), dim3(kPageThreads), 0, stream, p) != cudaSuccess) return SPEC_ERR_CUDA;
+  if (ctas > 1 && launch_pdl(page_count_kernel, dim3(1), dim3(kPageThreads), 0, stream, p) != cudaSuccess) return SPEC_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
 
