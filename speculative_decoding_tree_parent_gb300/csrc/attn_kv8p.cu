@@ -238,7 +238,7 @@ __device__ __forceinline__ float factor(float row, float ks) { return fmaxf(row 
 // the order of their index, so the longest are begun first and the last wave holds the shortest.
 __device__ __forceinline__ int nth_longest(const Params& p, int n, int* keys) {
   for (int t = threadIdx.x; t < p.batch; t += kThreads)
-    keys[t] = __ldg(p.prefix_len + t) + (__ldg(p.qo + t + 1) - __ldg(p.qo + t));
+    keys[t] = ld(p.prefix_len + t) + (ld(p.qo + t + 1) - ld(p.qo + t));
   int* found = keys + kLptMax;
   __syncthreads();
   for (int t = threadIdx.x; t < p.batch; t += kThreads) {
@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int b = bg / p.hkv;
   const int g = bg - b * p.hkv;
   if (p.lpt) b = nth_longest(p, b, reinterpret_cast<int*>(smem));
-  const int base = __ldg(p.qo + b), N = __ldg(p.qo + b + 1) - base, P = __ldg(p.prefix_len + b);
+  const int base = ld(p.qo + b), N = ld(p.qo + b + 1) - base, P = ld(p.prefix_len + b);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // (warp: uniform)
   const int node0 = blockIdx.y * p.npt;
   if (node0 >= N) return;
@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp >= kSoft0 && warp < kCvt) {
     if (valid) asm volatile("prefetch.global.L2 [%0];" ::"l"(p.q + orow * kD + 64 * slot));
   } else if ((warp == 0 || warp == 3) && sp.pg_lo + lane < sp.pg_hi) {
-    ids0 = __ldg(p.page_table + (size_t)b * p.max_pages + sp.pg_lo + lane);
+    ids0 = ld(p.page_table + (size_t)b * p.max_pages + sp.pg_lo + lane);
   }
   tc::fence_before_sync();
   __syncthreads();
@@ -356,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const CUtensorMap* tm_pool = isv ? &tm_vp : &tm_kp;
       auto ids_of = [&](int k) -> int {
         const int lp = sp.pg_lo + 32 * k + lane;
-        return lp < sp.pg_hi ? __ldg(p.page_table + (size_t)b * p.max_pages + lp) : p.num_pages;
+        return lp < sp.pg_hi ? ld(p.page_table + (size_t)b * p.max_pages + lp) : p.num_pages;
       };
       auto checked = [&](int page, int k) -> int {
         if (page >= 0 && page < p.num_pages) return page;
@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         return p.num_pages;  // out of range: TMA reads zeros
       };
       auto scale_of = [&](int page) {
-        return !isv && page < p.num_pages ? __ldg(p.kv_scale + (size_t)page * p.hkv + g) : make_float2(1.f, 1.f);
+        return !isv && page < p.num_pages ? ld(p.kv_scale + (size_t)page * p.hkv + g) : make_float2(1.f, 1.f);
       };
       int ids = ids0, ids_next = ids_of(1);
       float2 sc = make_float2(1.f, 1.f), sc_next = sc;
@@ -569,7 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto load_q = [&](uint4* w) {
       const uint4* src = reinterpret_cast<const uint4*>(p.q + orow * kD);
 #pragma unroll
-      for (int k = 0; k < 16; ++k) w[k] = valid ? __ldg(src + k) : make_uint4(0, 0, 0, 0);
+      for (int k = 0; k < 16; ++k) w[k] = valid ? ld(src + k) : make_uint4(0, 0, 0, 0);
     };
     // A step begins with its S complete and ends with its P handed on. In between, M follows the
     // row's maximum, and O is rescaled where it moves, after this group's PV before. Before P is
@@ -862,7 +862,7 @@ __global__ void __launch_bounds__(kMergeThreads) attn_kv8p_merge_kernel(const Me
   const int node = tt * p.npt + r / p.G;
   if (r >= p.npt * p.G) return;
   pdl_wait();  // the attention grid has finished: its partials are visible
-  const int base = __ldg(p.qo + b), N = __ldg(p.qo + b + 1) - base, P = __ldg(p.prefix_len + b);
+  const int base = ld(p.qo + b), N = ld(p.qo + b + 1) - base, P = ld(p.prefix_len + b);
   if (node >= N || N > p.mask_words * 64 || P < 0 || P > p.max_len) return;  // as the attention
   const float* ls = p.part_lse + (size_t)tile * p.splits * kRows + r;
   const float4* po = p.part_o + (size_t)tile * p.splits * (kRows * kD / 4) + c * kRows + r;

@@ -66,6 +66,13 @@ __device__ __forceinline__ float4 e4m3x4_to_f32(uint32_t w) {
 // pdl_wait(), whether or not it signals early.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+// A plain load, for what the kernel before may have written: __ldg promises the compiler that a
+// value never changes, and it may move such a load ahead of pdl_wait() (a captured step then
+// committed the path of the step before it).
+template <typename T>
+__device__ __forceinline__ T ld(const T* p) {
+  return *p;
+}
 
 // The process-wide choice of spec_set_early_reads, taken when a call is made: whether the
 // attention and the greedy walk may read their inputs before pdl_wait() (off: they wait first).

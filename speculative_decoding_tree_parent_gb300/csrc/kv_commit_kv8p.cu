@@ -95,8 +95,8 @@ __global__ void __launch_bounds__(2 * kQcHalf) kv_commit_kv8p_kernel(const Commi
   const int half = threadIdx.x / kQcHalf, tid = threadIdx.x % kQcHalf;  // 0: K, 1: V
   __shared__ uint32_t s_top[2][2][kQcHalf / 32];  // [head of a pair][half][warp]
   pdl_wait();
-  const int base = __ldg(p.qo + b), n = __ldg(p.qo + b + 1) - base;
-  const int P = __ldg(p.prefix_len + b), L = __ldg(p.accept_len + b);
+  const int base = ld(p.qo + b), n = ld(p.qo + b + 1) - base;
+  const int P = ld(p.prefix_len + b), L = ld(p.accept_len + b);
   const int ps = p.page_size;
   const int32_t* path = p.path + (size_t)b * p.path_cap;
   const int32_t* table = p.page_table + (size_t)b * p.max_pages;
@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(2 * kQcHalf) kv_commit_kv8p_kernel(const Commi
     const int e = tid + i * kQcHalf, r = e / pieces;
     from[i] = -1;
     if (r < r0 || r >= r1) continue;
-    const int node = __ldg(path + r - shift);
+    const int node = ld(path + r - shift);
     if (node >= 0 && node < n) from[i] = (long)(base + node) * p.hkv * p.d + 16 * (e - r * pieces);
   }
   auto load = [&](int g, uint4 (&x)[kPer][2]) {
@@ -128,8 +128,8 @@ __global__ void __launch_bounds__(2 * kQcHalf) kv_commit_kv8p_kernel(const Commi
       x[i][0] = x[i][1] = make_uint4(0, 0, 0, 0);
       if (from[i] < 0) continue;
       const uint4* src = reinterpret_cast<const uint4*>(p.tree[half] + from[i] + (long)g * p.d);
-      x[i][0] = __ldg(src);
-      x[i][1] = __ldg(src + 1);
+      x[i][0] = ld(src);
+      x[i][1] = ld(src + 1);
     }
   };
   // the first head's rows are on their way while the sequence is checked
@@ -137,19 +137,19 @@ __global__ void __launch_bounds__(2 * kQcHalf) kv_commit_kv8p_kernel(const Commi
   load(blockIdx.z, x);
   int bad = 0;
   for (int i = threadIdx.x; i <= L; i += 2 * kQcHalf) {
-    const int node = __ldg(path + i);
+    const int node = ld(path + i);
     const int q = (P + i) / ps;
     if (node < 0 || node >= n || (i == 0 && node != 0)) bad = SPEC_ERR_INDEX;
     else if (q >= p.max_pages) bad = SPEC_ERR_CAPACITY;
     else {
-      const int page = __ldg(table + q);
+      const int page = ld(table + q);
       if (page < 0 || page >= p.num_pages) bad = SPEC_ERR_PAGE;
     }
     if (bad) break;
   }
   if (bad && lead) report(p.status, bad);
   if (__syncthreads_or(bad)) return;
-  const size_t page = (size_t)__ldg(table + lp);
+  const size_t page = (size_t)ld(table + lp);
   int turn = 0;
   for (int g = blockIdx.z; g < p.hkv; g += gridDim.z, turn ^= 1) {
     const size_t unit = page * p.hkv + g;
@@ -221,7 +221,8 @@ int launch_kv_commit_kv8p(const void* k_tree, const void* v_tree, const int32_t*
   const int most = path_cap < kMaxTreeNodes ? path_cap : kMaxTreeNodes;
   // a CTA per head while they stand on the GPU at once (its longest chain is then the shortest),
   // else as many heads a CTA as make it so: the checks and the chain before the rows are then made
-  // once for several heads, and a head's rows are loaded under the one before it
+  // once for several heads, and a head's rows are loaded under the one before it (32 sequences of
+  // about 500 rows, 8 heads: a CTA per head 39 us; at most 8, 16, 32 CTAs an SM: 26.8, 24.8, 28.8)
   const int pages = ceil_div(most - 1, page_size) + 1;
   const long share = 16L * sm_count() / ((long)batch * pages);
   const dim3 grid(batch, pages, (unsigned)(share < 1 ? 1 : share < hkv ? share : hkv)), block(2 * kQcHalf);

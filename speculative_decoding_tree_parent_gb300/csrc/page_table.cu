@@ -47,7 +47,7 @@ struct PageWant {
   int grow, back;
 };
 __device__ __forceinline__ PageWant page_want(const PageArgs& p, int b, int* code) {
-  const int len = __ldg(p.seq_len + b), n = __ldg(p.qo + b + 1) - __ldg(p.qo + b), held = __ldg(p.held + b);
+  const int len = ld(p.seq_len + b), n = ld(p.qo + b + 1) - ld(p.qo + b), held = ld(p.held + b);
   *code = 0;
   if (len < 0 || n < 0 || held < 0 || held > p.max_pages) {
     *code = SPEC_ERR_INDEX;
@@ -59,6 +59,17 @@ __device__ __forceinline__ PageWant page_want(const PageArgs& p, int b, int* cod
     return PageWant{0, 0};
   }
   return PageWant{need > held ? (int)need - held : 0, p.shrink && need < held ? held - (int)need : 0};
+}
+
+// The sequence that owns row t: the last b with qo[b] <= t.
+__device__ __forceinline__ int page_seq_of(const int32_t* qo, int batch, int t) {
+  int lo = 0, hi = batch - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (ld(qo + mid) <= t) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
 }
 
 struct PagePlan {
@@ -132,7 +143,7 @@ __device__ __forceinline__ int page_owner(const int* sums, int batch, int x) {
 __device__ __forceinline__ int page_returned(const PageArgs& p, const PagePlan& s, int r) {
   const int b = page_owner(s.back, p.batch, r);
   // row b gives up its last back_b entries, in order
-  return __ldcg(p.page_table + (size_t)b * p.max_pages + __ldg(p.held + b) - (s.back[b] - r));
+  return __ldcg(p.page_table + (size_t)b * p.max_pages + ld(p.held + b) - (s.back[b] - r));
 }
 
 __device__ __forceinline__ int page_granted(const PageArgs& p, const PagePlan& s, int n0, int n1, int x) {
@@ -153,7 +164,7 @@ struct PageSeq {
   int len, held, keeps, ends, from;
 };
 __device__ __forceinline__ PageSeq page_seq(const PageArgs& p, const PagePlan& s, int b, bool sane, int granted) {
-  PageSeq q{__ldg(p.seq_len + b), __ldg(p.held + b), 0, 0, b > 0 ? s.grow[b - 1] : 0};
+  PageSeq q{ld(p.seq_len + b), ld(p.held + b), 0, 0, b > 0 ? s.grow[b - 1] : 0};
   if (q.held < 0 || q.held > p.max_pages) q.len = -1;
   q.keeps = sane ? q.held - (s.back[b] - (b > 0 ? s.back[b - 1] : 0)) : q.held;
   // (a sequence grows or shrinks, not both: held = keeps where anything is granted)
@@ -176,7 +187,7 @@ __global__ void __launch_bounds__(kPageThreads) page_table_kernel(const PageArgs
   __shared__ PagePlan s;
   pdl_trigger();
   pdl_wait();
-  const int n0 = __ldg(p.n_free);
+  const int n0 = ld(p.n_free);
   page_plan(p, s, blockIdx.x == 0);
   const int asked = s.grow[p.batch - 1], back = s.back[p.batch - 1];
   const int n1 = n0 + back;
@@ -193,16 +204,16 @@ __global__ void __launch_bounds__(kPageThreads) page_table_kernel(const PageArgs
       const int j = x - (b > 0 ? s.grow[b - 1] : 0);
       const int page = page_granted(p, s, n0, n1, x);
       if (page < 0 || page >= p.num_pages) report(p.status, SPEC_ERR_PAGE);
-      p.page_table[(size_t)b * p.max_pages + __ldg(p.held + b) + j] = page;
+      p.page_table[(size_t)b * p.max_pages + ld(p.held + b) + j] = page;
     }
     for (int r = first; r < back - granted; r += step) p.free_pages[n0 + r] = page_returned(p, s, r);
   }
   if (p.slot_map != nullptr) {
-    const int last = min(p.total_nodes, __ldg(p.qo + p.batch));  // rows behind the last sequence stay as they are
+    const int last = min(p.total_nodes, ld(p.qo + p.batch));  // rows behind the last sequence stay as they are
     for (int t0 = first * kPageTok; t0 < last; t0 += step * kPageTok) {
       long long slots[kPageTok];
-      int b = seq_of_row(p.qo, p.batch, t0);
-      int lo = __ldg(p.qo + b), hi = __ldg(p.qo + b + 1);
+      int b = page_seq_of(p.qo, p.batch, t0);
+      int lo = ld(p.qo + b), hi = ld(p.qo + b + 1);
       PageSeq q = page_seq(p, s, b, sane, granted);
       unsigned at_page = 0xFFFFFFFFu;
       int page = -1;
@@ -214,7 +225,7 @@ __global__ void __launch_bounds__(kPageThreads) page_table_kernel(const PageArgs
         while (t >= hi && b + 1 < p.batch) {  // the next sequence that has nodes
           ++b;
           lo = hi;
-          hi = __ldg(p.qo + b + 1);
+          hi = ld(p.qo + b + 1);
           if (t < hi) q = page_seq(p, s, b, sane, granted);
           at_page = 0xFFFFFFFFu;
         }
@@ -252,7 +263,7 @@ __global__ void __launch_bounds__(kPageThreads) page_table_kernel(const PageArgs
 __global__ void __launch_bounds__(kPageThreads) page_count_kernel(const PageArgs p) {
   __shared__ PagePlan s;
   pdl_wait();  // the kernel before has read the counters that this one may overwrite
-  const int n0 = __ldg(p.n_free);
+  const int n0 = ld(p.n_free);
   page_plan(p, s, false);
   const int n1 = n0 + s.back[p.batch - 1];
   const bool sane = n0 >= 0 && n1 <= p.num_pages;

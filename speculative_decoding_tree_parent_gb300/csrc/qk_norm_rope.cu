@@ -147,11 +147,11 @@ __global__ void __launch_bounds__(kRopeMaxWarps * 32, 2) qk_norm_rope_kernel(con
   // sequences, one of them owns the node.
   int lo = 0, hi = 0, len = 0;
   auto locate = [&](int t) -> int {
-    const int dep = p.depth != nullptr ? __ldg(p.depth + t) : 0;
+    const int dep = p.depth != nullptr ? ld(p.depth + t) : 0;
     if (t < lo || t >= hi) {
       int mlo = 0, mhi = 0, mlen = 0;
       for (int s = lane; s < p.batch; s += 32) {
-        const int a = __ldg(p.qo + s), b = __ldg(p.qo + s + 1), l = __ldg(p.prefix_len + s);
+        const int a = ld(p.qo + s), b = ld(p.qo + s + 1), l = ld(p.prefix_len + s);
         if (t >= a && t < b) mlo = a, mhi = b, mlen = l;
       }
       const unsigned who = __ballot_sync(0xffffffffu, mhi > mlo);

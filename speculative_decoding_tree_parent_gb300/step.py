@@ -23,9 +23,13 @@ class DeviceBatch:
 
     def __init__(self, inp, device="cuda", mode=None, kv_fp8=False):
         """kv_fp8: hold the paged pool as E4M3 codes with per-KV-head scales
-        (workloads.fp8_pool) and run the FP8-cache attention and commit calls."""
+        (workloads.fp8_pool) and run the FP8-cache attention and commit calls; "page": with a
+        scale per page and KV head (workloads.fp8_page_pool), and those calls."""
+        if kv_fp8 not in (False, True, "page"):
+            raise ValueError('kv_fp8: False, True or "page" expected')
         self.inp = inp
         self.kv_fp8 = bool(kv_fp8)
+        self.kv_page = kv_fp8 == "page"
         self.device = device
         fdt = torch.float32 if inp.dtype == "f32" else torch.bfloat16
         self.fdt = fdt
@@ -38,8 +42,8 @@ class DeviceBatch:
         self.k_tree = _t(inp.k_tree, fdt, dev)
         self.v_tree = _t(inp.v_tree, fdt, dev)
         if self.kv_fp8:
-            from .workloads import fp8_pool
-            kc, vc, sc = fp8_pool(inp)
+            from .workloads import fp8_page_pool, fp8_pool
+            kc, vc, sc = fp8_page_pool(inp) if self.kv_page else fp8_pool(inp)
             self.k_pool = _t(kc, torch.uint8, dev)
             self.v_pool = _t(vc, torch.uint8, dev)
             self.kv_scale = _t(sc, torch.float32, dev)
@@ -69,7 +73,7 @@ class DeviceBatch:
         self.flags = torch.zeros(Bn, dtype=torch.uint8, device=dev)
         self.seq_len = torch.zeros(Bn, dtype=torch.int32, device=dev)
         self.status = torch.zeros(1, dtype=torch.int32, device=dev)
-        attn_ws = B.spec_workspace_size(B.SPEC_OP_ATTN, Bn, T, self.max_nodes, inp.hq, inp.hkv, inp.d,
+        attn_ws = B.spec_workspace_size(B.SPEC_OP_ATTN_KV8P if self.kv_page else B.SPEC_OP_ATTN, Bn, T, self.max_nodes, inp.hq, inp.hkv, inp.d,
                                         self.max_prefix, 0)
         acc_ws = B.spec_workspace_size(B.SPEC_OP_ACCEPT, Bn, T, self.max_nodes, 0, 0, 0, 0, inp.vocab)
         self.attn_ws = torch.zeros(max(attn_ws, 256), dtype=torch.uint8, device=dev)
@@ -105,6 +109,11 @@ class DeviceBatch:
                                       stream)
 
     def attention(self, stream=None, sm_scale=0.0):
+        if self.kv_page:
+            return B.spec_tree_verify_attn_kv8p(self.q, self.k_pool, self.v_pool, self.kv_scale, self.page_table,
+                                                self.prefix_len, self.max_prefix, self.k_tree, self.v_tree,
+                                                self.mask, self.qo, self.max_nodes, self.out, self.lse, self.attn_ws,
+                                                sm_scale, self.status, stream)
         if self.kv_fp8:
             return B.spec_tree_verify_attn_kv8(self.q, self.k_pool, self.v_pool, self.kv_scale, self.page_table,
                                                self.prefix_len, self.max_prefix, self.k_tree, self.v_tree,
@@ -136,6 +145,10 @@ class DeviceBatch:
                              flags=self.flags, dev_status=self.status, stream=stream)
 
     def commit(self, stream=None):
+        if self.kv_page:
+            return B.spec_kv_commit_kv8p(self.k_tree, self.v_tree, self.path, self.accept_len, self.qo,
+                                         self.page_table, self.prefix_len, self.k_pool, self.v_pool, self.kv_scale,
+                                         self.seq_len, self.status, stream)
         if self.kv_fp8:
             return B.spec_kv_commit_kv8(self.k_tree, self.v_tree, self.kv_scale, self.path, self.accept_len, self.qo,
                                         self.page_table, self.prefix_len, self.k_pool, self.v_pool, self.seq_len,
@@ -179,8 +192,13 @@ class DeviceBatch:
         split), then accept 1 (greedy) or 2 (stochastic) and commit 1 -- except that the fused
         greedy call of up to 4 sequences commits inside its acceptance kernel (bf16 cache)."""
         mode = mode or self.mode
-        splits, _ = self.attn_plan()
-        attn = 2 if splits > 1 else 1
+        if self.kv_page:   # (a workspace is asked for exactly where the keys are split)
+            inp = self.inp
+            attn = 2 if B.spec_workspace_size(B.SPEC_OP_ATTN_KV8P, self.B, self.T, self.max_nodes, inp.hq, inp.hkv,
+                                              inp.d, self.max_prefix, 0) else 1
+        else:
+            splits, _ = self.attn_plan()
+            attn = 2 if splits > 1 else 1
         acc = 2 if mode == "stochastic" else 1
         commit = 0 if (fused and mode != "stochastic" and self.B <= 4 and not self.kv_fp8) else 1
         mask = 0 if (fuse_mask and self.fused_mask_ok()) else 1

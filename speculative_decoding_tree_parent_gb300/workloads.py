@@ -451,3 +451,20 @@ def fp8_pool(inp: VerifyInputs):
         codes.append(x.clamp(-448.0, 448.0).to(torch.float8_e4m3fn).view(torch.uint8).numpy())
         scales.append(s)
     return codes[0], codes[1], np.stack(scales).astype(np.float32)
+
+
+def fp8_page_pool(inp: VerifyInputs):
+    """Input for the calls over page scales: (k_codes, v_codes, kv_scale) drawn from the
+    workload's own pool. kv_scale float32 [num_pages, Hkv, 2] (K, then V) is for each page and
+    KV head the smallest power of two that holds its largest |value| in 448 steps; the codes
+    are laid out as in fp8_pool."""
+    import torch
+
+    scales, codes = [], []
+    for pool in (inp.k_pool, inp.v_pool):
+        amax = np.abs(pool).max(axis=(2, 3)).astype(np.float64)
+        s = np.exp2(np.ceil(np.log2(np.where(amax > 0, amax / 448.0, 1.0)))).astype(np.float32)
+        x = torch.from_numpy(np.ascontiguousarray(pool, np.float32) / s[:, :, None, None])
+        codes.append(x.clamp(-448.0, 448.0).to(torch.float8_e4m3fn).view(torch.uint8).numpy())
+        scales.append(s)
+    return codes[0], codes[1], np.stack(scales, axis=-1).astype(np.float32)
