@@ -195,37 +195,45 @@ __device__ __forceinline__ uint32_t swz(int r, int c) { return (uint32_t)(r * 12
 // A row of q (bf16) to TMEM as hi and lo E4M3 codes (32 columns of four each);
 // returns the factor that the codes have to be multiplied by. (A row with an infinity or NaN gets
 // a NaN code.)
-__device__ __forceinline__ float split_row(const uint4* row, uint32_t tq) {
-  uint32_t w[64];
+// The row is read twice, the second time from the cache: short loops, as this runs once a CTA and
+// its code comes from afar.
+__device__ __forceinline__ float split_row(const uint4* row, bool valid, uint32_t tq) {
+  uint32_t m = 0;  // the largest magnitude, of the low and of the high halves
 #pragma unroll
-  for (int k = 0; k < 16; ++k) w[4 * k] = row[k].x, w[4 * k + 1] = row[k].y, w[4 * k + 2] = row[k].z, w[4 * k + 3] = row[k].w;
-  uint32_t top = 0;
-#pragma unroll
-  for (int i = 0; i < 64; ++i) top = max(top, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
+  for (int k = 0; k < 16; ++k) {
+    const uint4 v = valid ? ld(row + k) : make_uint4(0, 0, 0, 0);
+    m = __vmaxu2(__vmaxu2(m, v.x & 0x7FFF7FFFu), __vmaxu2(v.y & 0x7FFF7FFFu, __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
+  }
+  const uint32_t top = max(m & 0xFFFFu, m >> 16);
   const int e = max((int)(top >> 7), 1);       // exponent field of the largest element
   // up * 2^(e - 134) = 1: q * up has its largest element in [2^7, 2^8). Both factors are made
   // of two powers of two, as one may leave fp32's range.
   const int sh = 134 - e;                      // in [-121, 133]
   const float up0 = __uint_as_float((uint32_t)(127 + sh / 2) << 23);
   const float up1 = __uint_as_float((uint32_t)(127 + sh - sh / 2) << 23);
+#pragma unroll 1
+  for (int h = 0; h < 4; ++h) {
+    uint32_t hi[8], lo[8];
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    uint32_t hi[16], lo[16];
+    for (int i = 0; i < 4; ++i) {
+      const uint4 v = valid ? ld(row + 4 * h + i) : make_uint4(0, 0, 0, 0);
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const uint32_t a = w[32 * h + 2 * i], b = w[32 * h + 2 * i + 1];
-      const float x0 = __uint_as_float(a << 16) * up0 * up1, x1 = __uint_as_float(a & 0xFFFF0000u) * up0 * up1;
-      const float x2 = __uint_as_float(b << 16) * up0 * up1, x3 = __uint_as_float(b & 0xFFFF0000u) * up0 * up1;
-      const uint16_t h01 = e4m3x2(x0, x1), h23 = e4m3x2(x2, x3);
-      const uint32_t f01 = half2_of(h01), f23 = half2_of(h23);
-      const float2 g01 = __half22float2(*reinterpret_cast<const __half2*>(&f01));
-      const float2 g23 = __half22float2(*reinterpret_cast<const __half2*>(&f23));
-      hi[i] = h01 | ((uint32_t)h23 << 16);
-      lo[i] = e4m3x2(x0 - g01.x, x1 - g01.y) | ((uint32_t)e4m3x2(x2 - g23.x, x3 - g23.y) << 16);
+      for (int k = 0; k < 2; ++k) {
+        const uint32_t a = w[2 * k], b = w[2 * k + 1];
+        const float x0 = __uint_as_float(a << 16) * up0 * up1, x1 = __uint_as_float(a & 0xFFFF0000u) * up0 * up1;
+        const float x2 = __uint_as_float(b << 16) * up0 * up1, x3 = __uint_as_float(b & 0xFFFF0000u) * up0 * up1;
+        const uint16_t h01 = e4m3x2(x0, x1), h23 = e4m3x2(x2, x3);
+        const uint32_t f01 = half2_of(h01), f23 = half2_of(h23);
+        const float2 g01 = __half22float2(*reinterpret_cast<const __half2*>(&f01));
+        const float2 g23 = __half22float2(*reinterpret_cast<const __half2*>(&f23));
+        hi[2 * i + k] = h01 | ((uint32_t)h23 << 16);
+        lo[2 * i + k] = e4m3x2(x0 - g01.x, x1 - g01.y) | ((uint32_t)e4m3x2(x2 - g23.x, x3 - g23.y) << 16);
+      }
     }
     if (h == 0 && top >= 0x7F80u) hi[0] |= 0x7Fu;
-    tc::tmem_st16_u(tq + 16 * h, hi);
-    tc::tmem_st16_u(tq + 32 + 16 * h, lo);
+    tc::tmem_st8_u(tq + 8 * h, hi);
+    tc::tmem_st8_u(tq + 32 + 8 * h, lo);
   }
   return __uint_as_float((uint32_t)(127 - sh / 2) << 23) * __uint_as_float((uint32_t)(127 - (sh - sh / 2)) << 23);
 }
@@ -237,13 +245,16 @@ __device__ __forceinline__ float factor(float row, float ks) { return fmaxf(row 
 // The sequence with the n-th most keys (ties: the lower first), from the lengths: CTAs start in
 // the order of their index, so the longest are begun first and the last wave holds the shortest.
 __device__ __forceinline__ int nth_longest(const Params& p, int n, int* keys) {
+#pragma unroll 1
   for (int t = threadIdx.x; t < p.batch; t += kThreads)
     keys[t] = ld(p.prefix_len + t) + (ld(p.qo + t + 1) - ld(p.qo + t));
   int* found = keys + kLptMax;
   __syncthreads();
+#pragma unroll 1
   for (int t = threadIdx.x; t < p.batch; t += kThreads) {
     const int k = keys[t];
     int r = 0;
+#pragma unroll 4
     for (int u = 0; u < p.batch; ++u) r += keys[u] > k || (keys[u] == k && u < t) ? 1 : 0;
     if (r == n) *found = t;  // ranks are distinct: exactly one thread writes
   }
@@ -566,11 +577,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool live = __any_sync(0xffffffffu, valid);  // a warp without rows only keeps step
     const float scale_log2 = p.scale_log2;
     float* factors = reinterpret_cast<float*>(smem + kOffJoin);  // [row], from the second group to the first
-    auto load_q = [&](uint4* w) {
-      const uint4* src = reinterpret_cast<const uint4*>(p.q + orow * kD);
-#pragma unroll
-      for (int k = 0; k < 16; ++k) w[k] = valid ? ld(src + k) : make_uint4(0, 0, 0, 0);
-    };
     // A step begins with its S complete and ends with its P handed on. In between, M follows the
     // row's maximum, and O is rescaled where it moves, after this group's PV before. Before P is
     // written, PV of the block before, the other group's, has to have read what stands there: as
@@ -619,18 +625,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ok) warp_arrive(bar(&bars.p_full));
     };
     if (slot == 0 && nt > 0) {  // the tree's q: its rows as they are, from shared memory
-      uint4 qrow[16];
-      load_q(qrow);
+      const uint4* src = reinterpret_cast<const uint4*>(p.q + orow * kD);
 #pragma unroll
-      for (int k = 0; k < 16; ++k) *reinterpret_cast<uint4*>(smem + kOffQ + (k >> 3) * kSlab + swz(row, k & 7)) = qrow[k];
+      for (int k = 0; k < 16; ++k) {
+        const uint4 v = valid ? ld(src + k) : make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint4*>(smem + kOffQ + (k >> 3) * kSlab + swz(row, k & 7)) = v;
+      }
       tc::fence_proxy_async_smem();
       warp_arrive(bar(&bars.q16));
     }
     float qf = 0.f;  // the factor of the row's codes
     if (slot == 1 && nb > nt) {  // the prefix's: as codes
-      uint4 qrow[16];
-      load_q(qrow);
-      qf = split_row(qrow, tq);
+      qf = split_row(reinterpret_cast<const uint4*>(p.q + orow * kD), valid, tq);
       factors[row] = qf;
       tc::tmem_wait_st();
       tc::fence_before_sync();
@@ -645,28 +651,33 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (; ok && i < nt; i += 2) {  // P as two bf16 terms
         if (!begin_step(i)) break;
         if (live) {
-          float s[kTreeKeys];
-          tc::tmem_ld32(ts, s);
-          tc::tmem_ld32(ts + 32, s + 32);
-          tc::tmem_wait_ld();
-          s_loaded();
           const uint64_t see = bits;
           if (valid && i + 2 < nt) bits = __ldcg(mrow + i + 2);
           float mx = -INFINITY;
+#pragma unroll 1
+          for (int h = 0; h < 4; ++h) {  // (two passes over S in short loops: a tree is few blocks)
+            float s[16];
+            tc::tmem_ld16(ts + 16 * h, s);
+            tc::tmem_wait_ld();
+            const uint32_t in = (uint32_t)(see >> (16 * h));
 #pragma unroll
-          for (int c = 0; c < kTreeKeys; ++c) {
-            s[c] = ((see >> c) & 1ull) ? s[c] * scale_log2 : -INFINITY;
-            mx = fmaxf(mx, s[c]);
+            for (int c = 0; c < 16; ++c) mx = fmaxf(mx, ((in >> c) & 1u) ? s[c] * scale_log2 : -INFINITY);
           }
           const float off = raise(i, mx);
           wait_p(i);
           float sum0 = 0.f, sum1 = 0.f;
-#pragma unroll
+#pragma unroll 1
           for (int h = 0; h < 4; ++h) {
+            float s[16];
+            tc::tmem_ld16(ts + 16 * h, s);
+            tc::tmem_wait_ld();
+            const uint32_t in = (uint32_t)(see >> (16 * h));
             uint32_t hi[8], lo[8];
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
-              const float a = ex2_approx(s[16 * h + 2 * c] + off), d = ex2_approx(s[16 * h + 2 * c + 1] + off);
+              const float x = ((in >> (2 * c)) & 1u) ? s[2 * c] * scale_log2 : -INFINITY;
+              const float y = ((in >> (2 * c + 1)) & 1u) ? s[2 * c + 1] * scale_log2 : -INFINITY;
+              const float a = ex2_approx(x + off), d = ex2_approx(y + off);
               sum0 += a;
               sum1 += d;
               hi[c] = pack_bf16x2(a, d);
@@ -675,6 +686,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::tmem_st8_u(tp + 8 * h, hi);
             tc::tmem_st8_u(tp + 32 + 8 * h, lo);
           }
+          s_loaded();
           l += sum0 + sum1;
           tc::tmem_wait_st();
         } else {
