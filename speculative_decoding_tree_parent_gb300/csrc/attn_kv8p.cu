@@ -41,27 +41,25 @@ namespace specv {
 namespace kv8p {
 
 constexpr int kRows = 128;      // rows of a tile
-constexpr int kKeys = 128;      // keys of a prefix block
+constexpr int kKeys = 64;       // keys of a prefix block
 constexpr int kPages = kKeys / 16;
 constexpr int kTreeKeys = 64;   // nodes of a tree block
 constexpr int kD = 128;
-constexpr int kThreads = 512;
-constexpr int kSoft0 = 4, kCvt = 12;         // first softmax warp, first converter warp
-constexpr int kStK = 4, kStC = 3, kStV = 2;  // stages: K, V codes, V in 16 bits
-constexpr uint32_t kSlab = 128 * 128;        // 128 rows of 128 bytes
+constexpr int kThreads = 480;
+constexpr int kSoft0 = 2, kMma1 = 10;        // first softmax warp; tile 1's MMA issuer
+constexpr int kStK = 3, kStC = 3, kStV = 3;  // stages: K, V codes, V in 16 bits
+constexpr uint32_t kSlab = 128 * 128;        // 16 KB: a stage, half a tile of q
+constexpr uint32_t kVSlab = kKeys * 128;     // half a stage of V: 64 rows of 64 elements
 constexpr uint32_t kTreeSlab = kTreeKeys * 128;
-constexpr uint32_t kOffK = 0;
+constexpr uint32_t kOffQ = 0;                // two tiles: hi and lo codes, then the tree's bf16 rows
+constexpr uint32_t kOffK = kOffQ + 4 * kSlab;
 constexpr uint32_t kOffC = kOffK + kStK * kSlab;
 constexpr uint32_t kOffV = kOffC + kStC * kSlab;
-constexpr uint32_t kOffQ = kOffV + kStV * 2 * kSlab;   // q's bf16 rows, for the tree
-constexpr uint32_t kOffBar = kOffQ + 2 * kSlab;
-constexpr int kScales = 12;                  // blocks whose page scales are kept: three groups of four
-constexpr uint32_t kOffScale = kOffBar + 512;
-constexpr uint32_t kOffJoin = kOffScale + kScales * kPages * 16;      // float2 [group][row]: maximum, sum
-constexpr uint32_t kSmem = kOffJoin + 2 * kRows * 8 + 1024;           // + alignment slack
+constexpr uint32_t kOffBar = kOffV + kStV * kSlab;
+constexpr uint32_t kOffScale = kOffBar + 640;                 // page scales of two times eight blocks
+constexpr uint32_t kSmem = kOffScale + 64 * 16 + 1024;        // + alignment slack
 static_assert(kSmem <= 232448, "shared memory over the per-CTA limit");
-// TMEM columns: O of group t at 128 t, q, S, P
-constexpr uint32_t kTmemCols = 512, kColQ = 256, kColS = 320, kColP = 448;
+constexpr uint32_t kTmemCols = 512;          // a tile: S (and P) of even and of odd blocks, O
 constexpr int kLptMax = 1024;                // sequences that are ranked by length
 constexpr float kShift = 11.f;               // log2 of the largest P when M is set
 constexpr float kGrow = 4.f;                 // growth of the largest score that M may lag behind
@@ -95,33 +93,37 @@ struct Params {
 
 struct Bars {
   // one arrival a phase
-  uint64_t k_full[kStK], k_empty[kStK], c_full[kStC], v_empty[kStV], s_full[2], pv_done[2], all_done[2], sc_full[2];
+  uint64_t k_full[kStK], c_full[kStC], s_full[2][2], pv_done[2][2], fin[2], sc_full[2];
   // four: a warpgroup's warps
-  uint64_t q16, q8, c_empty[kStC], v_full[kStV], s_free, p_full;  // q in bf16 / as codes
+  uint64_t q16[2], q8[2], c_empty[kStC], v_full[kStV], p_full[2][2];  // q in bf16 / as codes
+  // one a tile
+  uint64_t k_empty[kStK], v_empty[kStV];
   uint64_t bad[kMaxTreeBlocks];  // tree nodes whose V row holds an infinity or NaN
   uint32_t tmem;
   int abort;
 };
-constexpr int kBar1 = 2 * kStK + kStC + kStV + 8, kBarAll = kBar1 + 4 + kStC + kStV;
+constexpr int kBar1 = kStK + kStC + 12, kBar4 = kBar1 + 8 + kStC + kStV, kBarAll = kBar4 + kStK + kStV;
 static_assert(sizeof(Bars) <= 512, "barrier block over its reserved bytes");
 
-// The blocks of one key split: units are the tree blocks (4 each), then the prefix pages; a
+// The blocks of one key split: units are the prefix pages, then the tree blocks (4 each); a
 // split takes a contiguous run of units, a tree block goes to the split of its first unit.
 struct Split {
-  int tb_lo, nt;      // tree blocks
   int pg_lo, pg_hi;   // prefix pages
+  int np;             // prefix blocks
+  int tb_lo;          // first tree block
   int nb;             // blocks in all
 };
 __device__ __forceinline__ Split split_of(int P, int N, int splits, int s) {
-  const int np = (P + 15) >> 4, nt = (N + kTreeKeys - 1) / kTreeKeys;
-  const long units = 4L * nt + np;
+  const int pages = (P + 15) >> 4, nt = (N + kTreeKeys - 1) / kTreeKeys;
+  const long units = pages + 4L * nt;
   const int lo = (int)(s * units / splits), hi = (int)((s + 1) * units / splits);
   Split r;
-  r.tb_lo = min(nt, (lo + 3) >> 2);
-  r.nt = min(nt, (hi + 3) >> 2) - r.tb_lo;
-  r.pg_lo = max(lo - 4 * nt, 0);
-  r.pg_hi = max(hi - 4 * nt, 0);
-  r.nb = r.nt + (r.pg_hi - r.pg_lo + kPages - 1) / kPages;
+  r.pg_lo = min(lo, pages);
+  r.pg_hi = min(hi, pages);
+  r.np = (r.pg_hi - r.pg_lo + kPages - 1) / kPages;
+  r.tb_lo = lo <= pages ? 0 : (lo - pages + 3) >> 2;
+  const int tb_hi = hi <= pages ? 0 : min(nt, (hi - pages + 3) >> 2);
+  r.nb = r.np + max(0, tb_hi - r.tb_lo);
   return r;
 }
 
@@ -177,31 +179,18 @@ __device__ __forceinline__ void warp_arrive(uint32_t bar) {
   tc::mbar_arrive_if((threadIdx.x & 31) == 0, bar);
 }
 
-// Registers: 512 threads start with 128 each. The softmax warps (two warpgroups) take 200, the
-// other two warpgroups keep 56: 256 * (200 + 56) = 512 * 128.
-constexpr int kLaunchRegs = 128;
-__device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 200;"); }
-__device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 56;"); }
-
-// All threads, from their own roles' code.
-__device__ __forceinline__ void cta_sync() { asm volatile("bar.sync 0;" ::: "memory"); }
-
-// The softmax warps of both slots.
-__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
-
 // 16-byte chunk c of row r of a 128-byte-row slab, in the 128-byte swizzle
 __device__ __forceinline__ uint32_t swz(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
 
-// A row of q (bf16) to TMEM as hi and lo E4M3 codes (32 columns of four each);
+// A row of q (bf16) to shared memory as hi and lo E4M3 codes (a slab of 128-byte rows each);
 // returns the factor that the codes have to be multiplied by. (A row with an infinity or NaN gets
-// a NaN code.)
-// The row is read twice, the second time from the cache: short loops, as this runs once a CTA and
-// its code comes from afar.
-__device__ __forceinline__ float split_row(const uint4* row, bool valid, uint32_t tq) {
+// a NaN code.) The row is read twice, the second time from the cache: short loops, as this runs
+// once a CTA and its code comes from afar.
+__device__ __forceinline__ float split_row(const uint4* src, bool valid, uint8_t* qs, int row) {
   uint32_t m = 0;  // the largest magnitude, of the low and of the high halves
 #pragma unroll
   for (int k = 0; k < 16; ++k) {
-    const uint4 v = valid ? ld(row + k) : make_uint4(0, 0, 0, 0);
+    const uint4 v = valid ? ld(src + k) : make_uint4(0, 0, 0, 0);
     m = __vmaxu2(__vmaxu2(m, v.x & 0x7FFF7FFFu), __vmaxu2(v.y & 0x7FFF7FFFu, __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
   }
   const uint32_t top = max(m & 0xFFFFu, m >> 16);
@@ -212,11 +201,11 @@ __device__ __forceinline__ float split_row(const uint4* row, bool valid, uint32_
   const float up0 = __uint_as_float((uint32_t)(127 + sh / 2) << 23);
   const float up1 = __uint_as_float((uint32_t)(127 + sh - sh / 2) << 23);
 #pragma unroll 1
-  for (int h = 0; h < 4; ++h) {
-    uint32_t hi[8], lo[8];
+  for (int h = 0; h < 8; ++h) {  // 16 elements, a 16-byte chunk of each
+    uint32_t hi[4], lo[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint4 v = valid ? ld(row + 4 * h + i) : make_uint4(0, 0, 0, 0);
+    for (int i = 0; i < 2; ++i) {
+      const uint4 v = valid ? ld(src + 2 * h + i) : make_uint4(0, 0, 0, 0);
       const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
@@ -232,8 +221,8 @@ __device__ __forceinline__ float split_row(const uint4* row, bool valid, uint32_
       }
     }
     if (h == 0 && top >= 0x7F80u) hi[0] |= 0x7Fu;
-    tc::tmem_st8_u(tq + 8 * h, hi);
-    tc::tmem_st8_u(tq + 32 + 8 * h, lo);
+    *reinterpret_cast<uint4*>(qs + swz(row, h)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    *reinterpret_cast<uint4*>(qs + kSlab + swz(row, h)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
   }
   return __uint_as_float((uint32_t)(127 - sh / 2) << 23) * __uint_as_float((uint32_t)(127 - (sh - sh / 2)) << 23);
 }
@@ -286,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (p.lpt) b = nth_longest(p, b, reinterpret_cast<int*>(smem));
   const int base = ld(p.qo + b), N = ld(p.qo + b + 1) - base, P = ld(p.prefix_len + b);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // (warp: uniform)
-  const int node0 = blockIdx.y * p.npt;
+  const int node0 = 2 * blockIdx.y * p.npt;
   if (node0 >= N) return;
   if (N > p.mask_words * 64 || P < 0 || P > p.max_len) {
     if (threadIdx.x == 0 && split == 0) {
@@ -295,23 +284,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     return;
   }
+  const int ntiles = node0 + p.npt < N ? 2 : 1;
   const Split sp = split_of(P, N, p.splits, split);
-  const int nb = sp.nb, nt = sp.nt;
-  const bool both = nb > 1;  // the second group has work
+  const int nb = sp.nb, np = sp.np;
 
-  // softmax threads: group, row, and what the row stands for
-  const int slot = warp >= 8 ? 1 : 0;
-  const int row = threadIdx.x & 127;
-  const int node = node0 + row / p.G;
+  // softmax threads: tile, row (its TMEM lane), and what the row stands for
+  const bool soft = warp >= kSoft0 && warp < kMma1;
+  const int tile = warp >= kSoft0 + 4 ? 1 : 0;
+  const int row = (warp & 3) * 32 + lane;
+  const int node = node0 + tile * p.npt + row / p.G;
   const int head = g * p.G + row % p.G;
-  const bool valid = row < p.npt * p.G && node < N;
+  const bool valid = soft && row < p.npt * p.G && node < N;
   const size_t orow = (size_t)(base + node) * p.hq + head;
-  const int tile = blockIdx.y + p.mtiles * (b * p.hkv + g);
+  const int group = 2 * blockIdx.y + tile + p.mtiles * (b * p.hkv + g);
 
   if (nb == 0) {  // an empty key split: nothing for the merge
-    if (warp >= kSoft0 && warp < 8) {
+    if (soft) {
       pdl_wait();
-      if (valid) p.part_lse[((size_t)tile * p.splits + split) * kRows + row] = -INFINITY;
+      if (valid) p.part_lse[((size_t)group * p.splits + split) * kRows + row] = -INFINITY;
     }
     return;
   }
@@ -320,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort = &bars.abort;
   if (warp == 0) {
     uint64_t* all = reinterpret_cast<uint64_t*>(&bars);
-    for (int x = lane; x < kBarAll; x += 32) tc::mbar_init(bar(all + x), x < kBar1 ? 1 : 4);
+    for (int x = lane; x < kBarAll; x += 32) tc::mbar_init(bar(all + x), x < kBar1 ? 1 : x < kBar4 ? 4 : ntiles);
     if (lane < kMaxTreeBlocks) bars.bad[lane] = 0;
     if (lane == 0) bars.abort = 0;
     tc::mbar_fence_init();
@@ -328,194 +318,184 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::tmem_alloc(bar(reinterpret_cast<uint64_t*>(&bars.tmem)), kTmemCols);
     tc::tmem_relinquish();
   }
-  // in flight over the setup: q's rows (to L2), the producers' first page ids
+  // in flight over the setup: q's rows (to L2), the producer's first page ids
   int ids0 = p.num_pages;
-  if (warp >= kSoft0 && warp < kCvt) {
-    if (valid) asm volatile("prefetch.global.L2 [%0];" ::"l"(p.q + orow * kD + 64 * slot));
-  } else if ((warp == 0 || warp == 3) && sp.pg_lo + lane < sp.pg_hi) {
+  if (valid) {
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p.q + orow * kD));
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p.q + orow * kD + 64));
+  } else if (warp == 0 && sp.pg_lo + lane < sp.pg_hi) {
     ids0 = ld(p.page_table + (size_t)b * p.max_pages + sp.pg_lo + lane);
   }
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = bars.tmem;
-
-  float m = -INFINITY, l = 0.f;  // softmax threads: running maximum and sum
   bool ok = true;
-  // An issuer's end: every product it issued has completed before O is read and TMEM released.
-  auto finish = [&](int which) {
-    if (!ok) report(p.status, SPEC_ERR_TIMEOUT);
-    tc::mma_commit(bar(&bars.all_done[which]));
-    int zero = 0;
-    tc::mbar_wait(bar(&bars.all_done[which]), 0, &zero, kWaitLimit);
-  };
 
-  if (warp < kSoft0) {
-    regs_down();  // (by the whole warpgroup at once)
-    if (warp == 0 || warp == 3) {
-      // ------------------------------------------------------------------ TMA producers
-      // Warp 0 loads K and the pages' scales, warp 3 V's codes (one warp issuing all 16 copies of
-      // a block was the slowest of its parts). Page ids of four blocks at a time, one per lane,
-      // a batch ahead of their use; an id is checked when its batch comes up.
-      const bool isv = warp == 3;
-      const uint32_t leader = elect_one();
-      const int kSt = isv ? kStC : kStK;
-      uint64_t* full = isv ? bars.c_full : bars.k_full;
-      uint64_t* empty = isv ? bars.c_empty : bars.k_empty;
-      const uint32_t ring = sb + (isv ? kOffC : kOffK);
-      const CUtensorMap* tm_tree = isv ? &tm_vt : &tm_kt;
-      const CUtensorMap* tm_pool = isv ? &tm_vp : &tm_kp;
-      auto ids_of = [&](int k) -> int {
-        const int lp = sp.pg_lo + 32 * k + lane;
-        return lp < sp.pg_hi ? ld(p.page_table + (size_t)b * p.max_pages + lp) : p.num_pages;
-      };
-      auto checked = [&](int page, int k) -> int {
-        if (page >= 0 && page < p.num_pages) return page;
-        if (!isv && sp.pg_lo + 32 * k + lane < sp.pg_hi) report(p.status, SPEC_ERR_PAGE);
-        return p.num_pages;  // out of range: TMA reads zeros
-      };
-      auto scale_of = [&](int page) {
-        return !isv && page < p.num_pages ? ld(p.kv_scale + (size_t)page * p.hkv + g) : make_float2(1.f, 1.f);
-      };
-      int ids = ids0, ids_next = ids_of(1);
-      float2 sc = make_float2(1.f, 1.f), sc_next = sc;
-      int done = 0;  // blocks whose copies were issued
-      for (int i = 0, st = 0, turn = 0; i < nb; ++i, ++st) {
-        if (st == kSt) st = 0, ++turn;
-        if (turn > 0 && !wait_all(bar(&empty[st]), (turn & 1) ^ 1, abort)) break;
-        const uint32_t dst = ring + st * kSlab;
-        // (one lane issues, the others' part predicated off: a copy by each of eight lanes cost about
-        // 60 cycles more a copy)
-        tc::expect_tx_if(leader, bar(&full[st]), kSlab);
-        if (i < nt) {
+  if (warp == 0) {
+    // ------------------------------------------------------------------ TMA producer
+    // Page ids of eight blocks at a time, one per lane, a batch ahead of their use; an id is
+    // checked when its batch comes up.
+    const uint32_t leader = elect_one();
+    auto ids_of = [&](int k) -> int {
+      const int lp = sp.pg_lo + 32 * k + lane;
+      return lp < sp.pg_hi ? ld(p.page_table + (size_t)b * p.max_pages + lp) : p.num_pages;
+    };
+    auto checked = [&](int page, int k) -> int {
+      if (page >= 0 && page < p.num_pages) return page;
+      if (sp.pg_lo + 32 * k + lane < sp.pg_hi) report(p.status, SPEC_ERR_PAGE);
+      return p.num_pages;  // out of range: TMA reads zeros
+    };
+    auto scale_of = [&](int page) {
+      return page < p.num_pages ? ld(p.kv_scale + (size_t)page * p.hkv + g) : make_float2(1.f, 1.f);
+    };
+    int ids = checked(ids0, 0), ids_next = ids_of(1);
+    float2 sc = scale_of(ids), sc_next = sc;
+    int k_done = 0, c_done = 0;  // blocks whose copies were issued
 #pragma unroll 1
-          for (int h = 0; h < 2; ++h)  // two 64-column halves
-            tc::tma_load_3d_if(leader, dst + h * kTreeSlab, tm_tree, bar(&full[st]), h * 64, g,
-                               base + (sp.tb_lo + i) * kTreeKeys);
-        } else {
-          const int j = i - nt;
-          if (j == 0) {
-            ids = checked(ids, 0);
-            sc = scale_of(ids);
-          } else if ((j & 3) == 0) {
-            ids = ids_next;
-            sc = sc_next;
-            ids_next = ids_of((j >> 2) + 1);
-          }
-#pragma unroll 1
-          for (int pp = 0; pp < kPages; ++pp) {
-            const int page = __shfl_sync(0xffffffffu, ids, (j & 3) * kPages + pp);
-            tc::tma_load_4d_if(leader, dst + pp * 2048, tm_pool, bar(&full[st]), 0, 0, g, page);
-          }
-          if ((j & 3) == 2) {
-            ids_next = checked(ids_next, (j >> 2) + 1);
-            sc_next = scale_of(ids_next);
-          }
-          if (!isv && (j & 3) == 0) {
-            // the scales of these four blocks; what their places held, twelve to nine blocks ago, has
-            // been read: the stage just filled was released by QK of four blocks ago, which waited until
-            // S of five and of six blocks ago was in registers, one of each group
-            const float vs = page_scale(sc.y);
-            *reinterpret_cast<float4*>(smem + kOffScale + ((j % kScales) * kPages + lane) * 16) =
-                make_float4(page_scale(sc.x), log2f(vs), 1.f / vs, 0.f);
-            warp_arrive(bar(&bars.sc_full[(j >> 2) & 1]));
-          }
+    for (int j = 0; j < nb; ++j) {
+      const int sk = j % kStK, sc_ = j % kStC;
+      if (j < np && (j & 7) == 0) {
+        if (j > 0) {
+          ids = ids_next;
+          sc = sc_next;
+          ids_next = ids_of((j >> 3) + 1);
         }
-        done = i + 1;
+        // The scales of these eight blocks. What their places held, sixteen to nine blocks ago, has
+        // been read: the code stage of three blocks ago was filled after the converters' wait for the
+        // PV of three before that, which follows both tiles' softmax of that block.
+        const float vs = page_scale(sc.y);
+        *reinterpret_cast<float4*>(smem + kOffScale + (((j >> 3) & 1) * 32 + lane) * 16) =
+            make_float4(page_scale(sc.x), log2f(vs), 1.f / vs, 0.f);
+        warp_arrive(bar(&bars.sc_full[(j >> 3) & 1]));
       }
-      if (done < nb && lane == 0) {  // given up: leave no copy in flight
-        report(p.status, SPEC_ERR_TIMEOUT);
-        int zero = 0;
-        for (int i = max(0, done - kSt); i < done; ++i)
-          tc::mbar_wait(bar(&full[i % kSt]), (i / kSt) & 1, &zero, kWaitLimit);
-      }
-      __syncwarp();
-    } else if (warp == 1) {
-      // ------------------------------------------------------------------ MMA issuer: QK
-      // (A warp's instructions that follow its products wait until the tensor cores have taken
-      // those up: one warp issuing QK and PV in turn could not prepare the one under the other.)
-      if (elect_one()) {
-        const uint32_t ts = tmem + kColS;
-#pragma unroll 1
-        for (int i = 0; i < nb; ++i) {
-          const int sk = i % kStK;
-          if (i == 0 && nt > 0) ok = wait_one(bar(&bars.q16), 0, abort);
-          if (i == nt) ok = ok && wait_one(bar(&bars.q8), 0, abort);
-          ok = ok && wait_one(bar(&bars.k_full[sk]), (i / kStK) & 1, abort);
-          if (i > 0) ok = ok && wait_one(bar(&bars.s_free), (i - 1) & 1, abort);  // the block before has left S
-          if (!ok) break;
-          tc::fence_after_sync();
-          const uint64_t kd = tc::sdesc_sw128(sb + kOffK + sk * kSlab, 16, 1024);
-          if (i < nt) {
-            const uint64_t qd = tc::sdesc_sw128(sb + kOffQ, 16, 1024);
-#pragma unroll 1
-            for (int k = 0; k < 8; ++k)
-              tc::mma_bf16(ts, qd + (((k >> 2) * kSlab + (k & 3) * 32) >> 4),
-                           kd + (((k >> 2) * kTreeSlab + (k & 3) * 32) >> 4), kIdTreeQK, k > 0);
-          } else {
+      if (j >= kStK && !wait_all(bar(&bars.k_empty[sk]), ((j / kStK) & 1) ^ 1, abort)) break;
+      const uint32_t kdst = sb + kOffK + sk * kSlab, cdst = sb + kOffC + sc_ * kSlab;
+      // (one lane issues, the others' part predicated off: a copy by each of eight lanes cost about
+      // 60 cycles more a copy)
+      const uint32_t bytes = j < np ? kKeys * 128 : 2 * kTreeSlab;
+      tc::expect_tx_if(leader, bar(&bars.k_full[sk]), bytes);
+      if (j < np) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k)  // hi, then lo
-              tc::mma_f8_ts(ts, tmem + kColQ + 8 * k, kd + (((k & 3) * 32) >> 4), kIdQK, k > 0);
-          }
-          tc::mma_commit(bar(&bars.s_full[i & 1]));
-          tc::mma_commit(bar(&bars.k_empty[sk]));
-        }
-        finish(0);
-      }
-      __syncwarp();
-    } else {
-      // ------------------------------------------------------------------ MMA issuer: PV
-      if (elect_one()) {
-        const uint32_t tp = tmem + kColP;
-#pragma unroll 1
-        for (int i = 0; i < nb; ++i) {
-          const int sv = i % kStV;
-          ok = wait_one(bar(&bars.v_full[sv]), (i / kStV) & 1, abort) && wait_one(bar(&bars.p_full), i & 1, abort);
-          if (!ok) break;
-          tc::fence_after_sync();
-          const uint64_t vd = tc::sdesc_sw128(sb + kOffV + sv * 2 * kSlab, kSlab, 1024);
-          const uint32_t to = tmem + 128 * (i & 1);
-          if (i < nt) {
-#pragma unroll 1
-            for (int k = 0; k < 8; ++k)  // P's two bf16 terms, four steps of 16 nodes each
-              tc::mma_bf16_ts(to, tp + 8 * k, vd + (((k & 3) * 2048) >> 4), kIdTreePV, i > 1 || k > 0);
-          } else {
+        for (int pp = 0; pp < kPages; ++pp)
+          tc::tma_load_4d_if(leader, kdst + pp * 2048, &tm_kp, bar(&bars.k_full[sk]), 0, 0, g,
+                             __shfl_sync(0xffffffffu, ids, (j & 7) * kPages + pp));
+      } else {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) tc::mma_bf16_ts(to, tp + 8 * k, vd + ((k * 2048) >> 4), kIdPV, i > 1 || k > 0);
-          }
-          tc::mma_commit(bar(&bars.pv_done[i & 1]));
-          tc::mma_commit(bar(&bars.v_empty[sv]));
-        }
-        finish(1);
+        for (int h = 0; h < 2; ++h)  // two 64-column halves
+          tc::tma_load_3d_if(leader, kdst + h * kTreeSlab, &tm_kt, bar(&bars.k_full[sk]), h * 64, g,
+                             base + (sp.tb_lo + j - np) * kTreeKeys);
       }
-      __syncwarp();
+      k_done = j + 1;
+      if (j >= kStC && !wait_all(bar(&bars.c_empty[sc_]), ((j / kStC) & 1) ^ 1, abort)) break;
+      tc::expect_tx_if(leader, bar(&bars.c_full[sc_]), bytes);
+      if (j < np) {
+#pragma unroll
+        for (int pp = 0; pp < kPages; ++pp)
+          tc::tma_load_4d_if(leader, cdst + pp * 2048, &tm_vp, bar(&bars.c_full[sc_]), 0, 0, g,
+                             __shfl_sync(0xffffffffu, ids, (j & 7) * kPages + pp));
+      } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          tc::tma_load_3d_if(leader, cdst + h * kTreeSlab, &tm_vt, bar(&bars.c_full[sc_]), h * 64, g,
+                             base + (sp.tb_lo + j - np) * kTreeKeys);
+      }
+      c_done = j + 1;
+      if (j < np && (j & 7) == 4) {
+        ids_next = checked(ids_next, (j >> 3) + 1);
+        sc_next = scale_of(ids_next);
+      }
     }
-  } else if (warp >= kCvt) {
-    regs_down();
+    if (c_done < nb && lane == 0) {  // given up: leave no copy in flight
+      report(p.status, SPEC_ERR_TIMEOUT);
+      int zero = 0;
+      for (int j = max(0, k_done - kStK); j < k_done; ++j)
+        tc::mbar_wait(bar(&bars.k_full[j % kStK]), (j / kStK) & 1, &zero, kWaitLimit);
+      for (int j = max(0, c_done - kStC); j < c_done; ++j)
+        tc::mbar_wait(bar(&bars.c_full[j % kStC]), (j / kStC) & 1, &zero, kWaitLimit);
+    }
+    __syncwarp();
+  } else if (warp == 1 || warp == kMma1) {
+    // ------------------------------------------------------------------ MMA issuers, one a tile
+    const int t = warp == 1 ? 0 : 1;
+    if (t < ntiles && elect_one()) {
+      const uint32_t ts = tmem + 256 * t, to = ts + 128;
+      const uint32_t qb = sb + kOffQ + t * 2 * kSlab;
+      auto qk = [&](int j) {
+        const int sk = j % kStK;
+        if (j == 0 && np > 0) ok = wait_one(bar(&bars.q8[t]), 0, abort);
+        if (j == np) ok = ok && wait_one(bar(&bars.q16[t]), 0, abort);
+        ok = ok && wait_one(bar(&bars.k_full[sk]), (j / kStK) & 1, abort);
+        if (!ok) return;
+        tc::fence_after_sync();
+        const uint32_t kb = sb + kOffK + sk * kSlab, d = ts + 64 * (j & 1);
+        const uint64_t qd = tc::sdesc_sw128(qb, 16, 1024), kd = tc::sdesc_sw128(kb, 16, 1024);
+        if (j < np) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)  // hi, then lo
+            tc::mma_f8(d, qd + (((k >> 2) * kSlab + (k & 3) * 32) >> 4), kd + (((k & 3) * 32) >> 4), kIdQK, k > 0);
+        } else {
+#pragma unroll 1
+          for (int k = 0; k < 8; ++k)
+            tc::mma_bf16(d, qd + (((k >> 2) * kSlab + (k & 3) * 32) >> 4),
+                         kd + (((k >> 2) * kTreeSlab + (k & 3) * 32) >> 4), kIdTreeQK, k > 0);
+        }
+        tc::mma_commit(bar(&bars.s_full[t][j & 1]));
+        tc::mma_commit(bar(&bars.k_empty[sk]));
+      };
+      qk(0);
+#pragma unroll 1
+      for (int j = 0; ok && j < nb; ++j) {
+        if (j + 1 < nb) qk(j + 1);  // S of the next block while the softmax works on this one
+        const int sv = j % kStV;
+        ok = ok && wait_one(bar(&bars.v_full[sv]), (j / kStV) & 1, abort) &&
+             wait_one(bar(&bars.p_full[t][j & 1]), (j >> 1) & 1, abort);
+        if (!ok) break;
+        tc::fence_after_sync();
+        // P stands where its S stood; the QK that next overwrites it follows this PV in order
+        const uint64_t vd = tc::sdesc_sw128(sb + kOffV + sv * kSlab, kVSlab, 1024);
+        const uint32_t tp = ts + 64 * (j & 1);
+        if (j < np) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) tc::mma_bf16_ts(to, tp + 8 * k, vd + ((k * 2048) >> 4), kIdPV, j > 0 || k > 0);
+        } else {
+#pragma unroll 1
+          for (int k = 0; k < 8; ++k)  // P's two bf16 terms, four steps of 16 nodes each
+            tc::mma_bf16_ts(to, tp + 8 * k, vd + (((k & 3) * 2048) >> 4), kIdTreePV, j > 0 || k > 0);
+        }
+        tc::mma_commit(bar(&bars.pv_done[t][j & 1]));
+        tc::mma_commit(bar(&bars.v_empty[sv]));
+      }
+      if (!ok) report(p.status, SPEC_ERR_TIMEOUT);
+      // every product issued has completed before TMEM is released
+      tc::mma_commit(bar(&bars.fin[t]));
+      int zero = 0;
+      tc::mbar_wait(bar(&bars.fin[t]), 0, &zero, kWaitLimit);
+    }
+    __syncwarp();
+  } else if (warp > kMma1) {
     // ------------------------------------------------------------------ V converters
-    const int ct = threadIdx.x - kCvt * 32;
+    const int ct = threadIdx.x - (kMma1 + 1) * 32;
     const int r0 = (ct & 7) | ((ct >> 6) << 3), cc = (ct >> 3) & 7;
     const uint32_t src0 = swz(r0, cc);
-    const uint32_t dst0 = (cc >> 2) * kSlab + swz(r0, (cc & 3) * 2), dst1 = (cc >> 2) * kSlab + swz(r0, (cc & 3) * 2 + 1);
-    const int tail = min(P, sp.pg_hi * 16) - (sp.pg_lo + (nb - 1 - nt) * kPages) * 16;  // rows of the last block
-    for (int i = 0; i < nb; ++i) {
-      const int sc_ = i % kStC, sv = i % kStV;
-      if (!wait_all(bar(&bars.c_full[sc_]), (i / kStC) & 1, abort)) {
-        ok = false;
-        break;
-      }
-      const uint8_t* src = smem + kOffC + sc_ * kSlab;
-      uint8_t* dst = smem + kOffV + sv * 2 * kSlab;
-      if (i < nt) {
+    const uint32_t dst0 = (cc >> 2) * kVSlab + swz(r0, (cc & 3) * 2), dst1 = (cc >> 2) * kVSlab + swz(r0, (cc & 3) * 2 + 1);
+    const int tail = min(P, sp.pg_hi * 16) - (sp.pg_lo + (np - 1) * kPages) * 16;  // rows of the last prefix block
+#pragma unroll 1
+    for (int j = 0; j < nb; ++j) {
+      const int sc_ = j % kStC, sv = j % kStV;
+      ok = wait_all(bar(&bars.c_full[sc_]), (j / kStC) & 1, abort);
+      if (j >= kStV) ok = ok && wait_all(bar(&bars.v_empty[sv]), ((j / kStV) & 1) ^ 1, abort);
+      if (!ok) break;
+      uint8_t* src = smem + kOffC + sc_ * kSlab;
+      uint8_t* dst = smem + kOffV + sv * kSlab;
+      if (j >= np) {
         // bf16 rows as they are, but for rows past the tree and elements that are not finite
         // (a weight of 0 times either would reach rows whose mask leaves the node out)
-        const int tb = sp.tb_lo + i, nvalid = N - tb * kTreeKeys;
-        if (i >= kStV) ok = wait_all(bar(&bars.v_empty[sv]), ((i / kStV) & 1) ^ 1, abort);
-        if (!ok) break;
+        const int tb = sp.tb_lo + j - np, nvalid = N - tb * kTreeKeys;
 #pragma unroll 1
         for (int it = 0; it < 8; ++it) {
           const int id = it * 128 + ct, half = id >> 9, off = id & 511, r = off >> 3;
-          uint4 w = *reinterpret_cast<const uint4*>(src + half * kTreeSlab + off * 16);
+          const uint4 w = *reinterpret_cast<const uint4*>(src + half * kTreeSlab + off * 16);
           uint32_t u[4] = {w.x, w.y, w.z, w.w};
           bool bad = false;
 #pragma unroll
@@ -531,36 +511,31 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           if (bad) atomicOr(reinterpret_cast<unsigned long long*>(&bars.bad[tb]), 1ull << r);
-          *reinterpret_cast<uint4*>(dst + half * kSlab + off * 16) = make_uint4(u[0], u[1], u[2], u[3]);
+          *reinterpret_cast<uint4*>(dst + half * kVSlab + off * 16) = make_uint4(u[0], u[1], u[2], u[3]);
         }
       } else {
         // 16 codes a piece: row r0 + 16 it, chunk cc (8 lanes take 8 rows, so that loads and stores
         // meet 8 different 16-byte columns; the swizzle depends on r % 8 alone, the same in every
         // piece of a thread)
-        if (i == nb - 1) {  // rows past the prefix may hold anything (each thread clears what it will read)
+        if (j == np - 1) {  // rows past the prefix may hold anything (each thread clears what it will read)
 #pragma unroll 1
           for (int r = r0; r < kKeys; r += 16)
-            if (r >= tail) *reinterpret_cast<uint4*>(smem + kOffC + sc_ * kSlab + src0 + (r - r0) * 128) = make_uint4(0, 0, 0, 0);
+            if (r >= tail) *reinterpret_cast<uint4*>(src + src0 + (r - r0) * 128) = make_uint4(0, 0, 0, 0);
         }
-        if (i >= kStV) ok = wait_all(bar(&bars.v_empty[sv]), ((i / kStV) & 1) ^ 1, abort);
-        if (!ok) break;
-#pragma unroll 1
-        for (int part = 0; part < 8; part += 4) {
-          uint4 w[4];
+        uint4 w[4];
 #pragma unroll
-          for (int it = 0; it < 4; ++it) w[it] = *reinterpret_cast<const uint4*>(src + src0 + (part + it) * 2048);
+        for (int it = 0; it < 4; ++it) w[it] = *reinterpret_cast<const uint4*>(src + src0 + it * 2048);
 #pragma unroll
-          for (int it = 0; it < 4; ++it) {
-            const uint32_t u[4] = {w[it].x, w[it].y, w[it].z, w[it].w};
-            uint32_t h[8];
+        for (int it = 0; it < 4; ++it) {
+          const uint32_t u[4] = {w[it].x, w[it].y, w[it].z, w[it].w};
+          uint32_t h[8];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              h[2 * k] = half2_of((uint16_t)(u[k] & 0xFFFFu));
-              h[2 * k + 1] = half2_of((uint16_t)(u[k] >> 16));
-            }
-            *reinterpret_cast<uint4*>(dst + dst0 + (part + it) * 2048) = make_uint4(h[0], h[1], h[2], h[3]);
-            *reinterpret_cast<uint4*>(dst + dst1 + (part + it) * 2048) = make_uint4(h[4], h[5], h[6], h[7]);
+          for (int k = 0; k < 4; ++k) {
+            h[2 * k] = half2_of((uint16_t)(u[k] & 0xFFFFu));
+            h[2 * k + 1] = half2_of((uint16_t)(u[k] >> 16));
           }
+          *reinterpret_cast<uint4*>(dst + dst0 + it * 2048) = make_uint4(h[0], h[1], h[2], h[3]);
+          *reinterpret_cast<uint4*>(dst + dst1 + it * 2048) = make_uint4(h[4], h[5], h[6], h[7]);
         }
       }
       tc::fence_proxy_async_smem();
@@ -568,30 +543,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       warp_arrive(bar(&bars.c_empty[sc_]));
     }
     if (!ok && lane == 0) report(p.status, SPEC_ERR_TIMEOUT);
-  } else if (warp >= kSoft0) {
-    regs_up();
+  } else if (tile < ntiles) {
     // ------------------------------------------------------------------ softmax
-    const uint32_t quarter = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t ts = tmem + kColS + quarter, tp = tmem + kColP + quarter, to = tmem + 128 * slot + quarter;
-    const uint32_t tq = tmem + kColQ + quarter;
+    const uint32_t ts = tmem + 256 * tile + ((uint32_t)((warp & 3) * 32) << 16), to = ts + 128;
     const bool live = __any_sync(0xffffffffu, valid);  // a warp without rows only keeps step
     const float scale_log2 = p.scale_log2;
-    float* factors = reinterpret_cast<float*>(smem + kOffJoin);  // [row], from the second group to the first
-    // A step begins with its S complete and ends with its P handed on. In between, M follows the
-    // row's maximum, and O is rescaled where it moves, after this group's PV before. Before P is
-    // written, PV of the block before, the other group's, has to have read what stands there: as
-    // late as that goes. (Warps without rows wait for it too, else their arrivals could run a step
-    // ahead of the others'.)
-    auto begin_step = [&](int i) {
-      ok = wait_all(bar(&bars.s_full[slot]), (i >> 1) & 1, abort);
-      tc::fence_after_sync();
-      return ok;
-    };
-    auto s_loaded = [&]() {
-      tc::fence_before_sync();
-      warp_arrive(bar(&bars.s_free));  // QK of the next block may overwrite S
-    };
-    auto raise = [&](int i, float mx) {
+    const uint4* qrow = reinterpret_cast<const uint4*>(p.q + orow * kD);
+    uint8_t* qs = smem + kOffQ + tile * 2 * kSlab;
+    float m = -INFINITY, l = 0.f;  // running maximum and sum
+    // M follows the row's maximum, and O is rescaled where it moves
+    auto raise = [&](int j, float mx) {
       const bool moves = mx > -INFINITY && (m == -INFINITY || mx > m + kGrow);
       if (__any_sync(0xffffffffu, moves)) {
         float alpha = 1.f;
@@ -600,8 +561,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           m = mx;
           l *= alpha;
         }
-        if (i > 1) {
-          ok = wait_all(bar(&bars.pv_done[slot]), ((i >> 1) - 1) & 1, abort) && ok;
+        if (j > 0) {  // O is complete up to the block before
+          ok = wait_all(bar(&bars.pv_done[tile][(j - 1) & 1]), ((j - 1) >> 1) & 1, abort) && ok;
           tc::fence_after_sync();
 #pragma unroll 1
           for (int ch = 0; ch < kD / 16; ++ch) {
@@ -616,229 +577,178 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       return m == -INFINITY ? 0.f : kShift - m;
     };
-    auto wait_p = [&](int i) {
-      if (i > 0) ok = wait_all(bar(&bars.pv_done[slot ^ 1]), ((i - 1) >> 1) & 1, abort) && ok;
-      tc::fence_after_sync();
-    };
-    auto end_step = [&]() {
-      tc::fence_before_sync();
-      if (ok) warp_arrive(bar(&bars.p_full));
-    };
-    if (slot == 0 && nt > 0) {  // the tree's q: its rows as they are, from shared memory
-      const uint4* src = reinterpret_cast<const uint4*>(p.q + orow * kD);
+    // the tree's q: its rows as they are, where the codes stood
+    auto store_q16 = [&]() {
+#pragma unroll 1
+      for (int k = 0; k < 16; k += 4) {
+        uint4 v[4];
 #pragma unroll
-      for (int k = 0; k < 16; ++k) {
-        const uint4 v = valid ? ld(src + k) : make_uint4(0, 0, 0, 0);
-        *reinterpret_cast<uint4*>(smem + kOffQ + (k >> 3) * kSlab + swz(row, k & 7)) = v;
+        for (int e = 0; e < 4; ++e) v[e] = valid ? ld(qrow + k + e) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) *reinterpret_cast<uint4*>(qs + (k >> 3) * kSlab + swz(row, (k + e) & 7)) = v[e];
       }
       tc::fence_proxy_async_smem();
-      warp_arrive(bar(&bars.q16));
+      warp_arrive(bar(&bars.q16[tile]));
+    };
+    float rowf = scale_log2;
+    if (np > 0) {
+      rowf *= split_row(qrow, valid, qs, row);
+      tc::fence_proxy_async_smem();
+      warp_arrive(bar(&bars.q8[tile]));
+    } else {
+      store_q16();
     }
-    float qf = 0.f;  // the factor of the row's codes
-    if (slot == 1 && nb > nt) {  // the prefix's: as codes
-      qf = split_row(reinterpret_cast<const uint4*>(p.q + orow * kD), valid, tq);
-      factors[row] = qf;
-      tc::tmem_wait_st();
+    int left = min(P, sp.pg_hi * 16) - sp.pg_lo * 16;  // prefix keys from this block's first on
+#pragma unroll 1
+    for (int j = 0; ok && j < np; ++j, left -= kKeys) {
+      if ((j & 7) == 0) ok = wait_all(bar(&bars.sc_full[(j >> 3) & 1]), (j >> 4) & 1, abort);
+      const float4* scale = reinterpret_cast<const float4*>(smem + kOffScale) + (j & 15) * kPages;
+      float4 f[kPages];
+#pragma unroll
+      for (int pp = 0; pp < kPages; ++pp) f[pp] = scale[pp];
+      ok = ok && wait_all(bar(&bars.s_full[tile][j & 1]), (j >> 1) & 1, abort);
+      if (!ok) break;
+      tc::fence_after_sync();
+      if (j == np - 1 && nb > np) store_q16();  // (every QK over the codes is complete)
+      const uint32_t tj = ts + 64 * (j & 1);
+      if (live) {
+        if (left < kKeys) {  // the last block's keys past the prefix
+#pragma unroll 1
+          for (int c = left; c < kKeys; ++c) tc::tmem_st1_u(tj + c, 0xFF800000u);
+          tc::tmem_wait_st();
+        }
+        float s[kKeys];
+        tc::tmem_ld32(tj, s);
+        tc::tmem_ld32(tj + 32, s + 32);
+        tc::tmem_wait_ld();
+        float mx = -INFINITY;  // the largest x log2 e + log2 vs
+#pragma unroll
+        for (int pp = 0; pp < kPages; ++pp) {
+          const float* v = s + 16 * pp;
+          float x = fmax3(v[0], v[1], v[2]);
+#pragma unroll
+          for (int c = 3; c < 15; c += 2) x = fmax3(x, v[c], v[c + 1]);
+          f[pp].x = factor(rowf, f[pp].x);
+          mx = fmaxf(mx, fmaf(fmaxf(x, v[15]), f[pp].x, f[pp].y));
+        }
+        const float off = raise(j, mx);
+        uint32_t pk[kKeys / 2];
+#pragma unroll
+        for (int pp = 0; pp < kPages; ++pp) {
+          const float oo = off + f[pp].y;
+          const float2 f2 = make_float2(f[pp].x, f[pp].x), o2 = make_float2(oo, oo);
+          float2 s0 = make_float2(0.f, 0.f), s1 = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int c = 0; c < 16; c += 4) {
+            const float* v = s + 16 * pp + c;
+            uint32_t* to2 = pk + 8 * pp + (c >> 1);
+            const float2 a = ffma2(make_float2(v[0], v[1]), f2, o2);
+            const float2 d = ffma2(make_float2(v[2], v[3]), f2, o2);
+            const float2 ea = make_float2(ex2_approx(a.x), ex2_approx(a.y));
+            const float2 ed = make_float2(ex2_approx(d.x), ex2_approx(d.y));
+            s0 = fadd2(s0, ea);
+            s1 = fadd2(s1, ed);
+            to2[0] = pack_f16x2(ea.x, ea.y);
+            to2[1] = pack_f16x2(ed.x, ed.y);
+          }
+          l = fmaf((s0.x + s0.y) + (s1.x + s1.y), f[pp].z, l);
+        }
+        tc::tmem_st32_u(tj, pk);
+        tc::tmem_wait_st();
+      }
       tc::fence_before_sync();
-      warp_arrive(bar(&bars.q8));
+      if (ok) warp_arrive(bar(&bars.p_full[tile][j & 1]));
     }
-    int i = slot;
-    if (i < nt) {
+    if (ok && nb > np) {
       pdl_wait();  // the mask may come from the kernel before
       const uint64_t* mrow = p.mask + (size_t)(base + node) * p.mask_words + sp.tb_lo;
-      uint64_t bits = valid ? __ldcg(mrow + i) : 0ull;
+      uint64_t bits = valid ? __ldcg(mrow) : 0ull;
 #pragma unroll 1
-      for (; ok && i < nt; i += 2) {  // P as two bf16 terms
-        if (!begin_step(i)) break;
+      for (int j = np; ok && j < nb; ++j) {  // P as two bf16 terms
+        ok = wait_all(bar(&bars.s_full[tile][j & 1]), (j >> 1) & 1, abort);
+        if (!ok) break;
+        tc::fence_after_sync();
+        const uint32_t tj = ts + 64 * (j & 1);
         if (live) {
           const uint64_t see = bits;
-          if (valid && i + 2 < nt) bits = __ldcg(mrow + i + 2);
+          if (valid && j + 1 < nb) bits = __ldcg(mrow + j + 1 - np);
+          float s[kTreeKeys];
+          tc::tmem_ld32(tj, s);
+          tc::tmem_ld32(tj + 32, s + 32);
+          tc::tmem_wait_ld();
           float mx = -INFINITY;
-#pragma unroll 1
-          for (int h = 0; h < 4; ++h) {  // (two passes over S in short loops: a tree is few blocks)
-            float s[16];
-            tc::tmem_ld16(ts + 16 * h, s);
-            tc::tmem_wait_ld();
-            const uint32_t in = (uint32_t)(see >> (16 * h));
 #pragma unroll
-            for (int c = 0; c < 16; ++c) mx = fmaxf(mx, ((in >> c) & 1u) ? s[c] * scale_log2 : -INFINITY);
+          for (int c = 0; c < kTreeKeys; ++c) {
+            s[c] = ((see >> c) & 1ull) ? s[c] * scale_log2 : -INFINITY;
+            mx = fmaxf(mx, s[c]);
           }
-          const float off = raise(i, mx);
-          wait_p(i);
+          const float off = raise(j, mx);
           float sum0 = 0.f, sum1 = 0.f;
-#pragma unroll 1
+#pragma unroll
           for (int h = 0; h < 4; ++h) {
-            float s[16];
-            tc::tmem_ld16(ts + 16 * h, s);
-            tc::tmem_wait_ld();
-            const uint32_t in = (uint32_t)(see >> (16 * h));
             uint32_t hi[8], lo[8];
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
-              const float x = ((in >> (2 * c)) & 1u) ? s[2 * c] * scale_log2 : -INFINITY;
-              const float y = ((in >> (2 * c + 1)) & 1u) ? s[2 * c + 1] * scale_log2 : -INFINITY;
-              const float a = ex2_approx(x + off), d = ex2_approx(y + off);
+              const float a = ex2_approx(s[16 * h + 2 * c] + off), d = ex2_approx(s[16 * h + 2 * c + 1] + off);
               sum0 += a;
               sum1 += d;
               hi[c] = pack_bf16x2(a, d);
               lo[c] = pack_bf16x2(a - __uint_as_float(hi[c] << 16), d - __uint_as_float(hi[c] & 0xFFFF0000u));
             }
-            tc::tmem_st8_u(tp + 8 * h, hi);
-            tc::tmem_st8_u(tp + 32 + 8 * h, lo);
+            tc::tmem_st8_u(tj + 8 * h, hi);
+            tc::tmem_st8_u(tj + 32 + 8 * h, lo);
           }
-          s_loaded();
           l += sum0 + sum1;
           tc::tmem_wait_st();
-        } else {
-          s_loaded();
-          wait_p(i);
         }
-        end_step();
+        tc::fence_before_sync();
+        if (ok) warp_arrive(bar(&bars.p_full[tile][j & 1]));
       }
     }
-    if (ok && i < nb) {
-      if (slot == 0) {
-        ok = wait_all(bar(&bars.q8), 0, abort);
-        qf = factors[row];
-      }
-      const float rowf = scale_log2 * qf;
-      int left = min(P, sp.pg_hi * 16) - (sp.pg_lo + (i - nt) * kPages) * 16;  // keys from this block's first on
-#pragma unroll 1
-      for (; ok && i < nb; i += 2, left -= 2 * kKeys) {
-        // The page scales, as factors, exponents and weights of the row sum: they are there before S
-        // is, and read before it (shared memory answers late while the other warps keep it busy).
-        const int j = i - nt;
-        if ((j & 3) < 2 && !wait_all(bar(&bars.sc_full[(j >> 2) & 1]), (j >> 3) & 1, abort)) {
-          ok = false;
-          break;
-        }
-        const float4* scale = reinterpret_cast<const float4*>(smem + kOffScale) + (j % kScales) * kPages;
-        float pf[kPages], pe[kPages];
-#pragma unroll
-        for (int pp = 0; pp < kPages; ++pp) {
-          const float4 f = scale[pp];
-          pf[pp] = factor(rowf, f.x);
-          pe[pp] = f.y;
-        }
-        if (!begin_step(i)) break;
-        if (live) {
-          if (left < kKeys) {  // the last block's keys past the prefix
-#pragma unroll 1
-            for (int c = left; c < kKeys; ++c) tc::tmem_st1_u(ts + c, 0xFF800000u);
-            tc::tmem_wait_st();
-          }
-          float s[kKeys];
-#pragma unroll
-          for (int h = 0; h < 4; ++h) tc::tmem_ld32(ts + 32 * h, s + 32 * h);
-          tc::tmem_wait_ld();
-          s_loaded();
-          float mx = -INFINITY;  // the largest x log2 e + log2 vs
-#pragma unroll
-          for (int pp = 0; pp < kPages; ++pp) {
-            const float* v = s + 16 * pp;
-            float x = fmax3(v[0], v[1], v[2]);
-#pragma unroll
-            for (int c = 3; c < 15; c += 2) x = fmax3(x, v[c], v[c + 1]);
-            mx = fmaxf(mx, fmaf(fmaxf(x, v[15]), pf[pp], pe[pp]));
-          }
-          const float off = raise(i, mx);
-          uint32_t pk[kKeys / 2];
-#pragma unroll
-          for (int pp = 0; pp < kPages; ++pp) {
-            const float oo = off + pe[pp];
-            const float2 f2 = make_float2(pf[pp], pf[pp]), o2 = make_float2(oo, oo);
-            float2 r0 = make_float2(0.f, 0.f), r1 = make_float2(0.f, 0.f);
-#pragma unroll
-            for (int c = 0; c < 16; c += 4) {
-              const float* v = s + 16 * pp + c;
-              uint32_t* to2 = pk + 8 * pp + (c >> 1);
-              const float2 a = ffma2(make_float2(v[0], v[1]), f2, o2);
-              const float2 d = ffma2(make_float2(v[2], v[3]), f2, o2);
-              const float2 ea = make_float2(ex2_approx(a.x), ex2_approx(a.y));
-              const float2 ed = make_float2(ex2_approx(d.x), ex2_approx(d.y));
-              r0 = fadd2(r0, ea);
-              r1 = fadd2(r1, ed);
-              to2[0] = pack_f16x2(ea.x, ea.y);
-              to2[1] = pack_f16x2(ed.x, ed.y);
-            }
-            l = fmaf((r0.x + r0.y) + (r1.x + r1.y), scale[pp].z, l);
-          }
-          wait_p(i);
-          tc::tmem_st32_u(tp, pk);
-          tc::tmem_st32_u(tp + 32, pk + 32);
-          tc::tmem_wait_st();
-        } else {
-          s_loaded();
-          wait_p(i);
-        }
-        end_step();
-      }
-    }
+    ok = ok && wait_all(bar(&bars.pv_done[tile][(nb - 1) & 1]), ((nb - 1) >> 1) & 1, abort);
     if (!ok && lane == 0) report(p.status, SPEC_ERR_TIMEOUT);
+    tc::fence_after_sync();
 
     // -------------------------------------------------------------------- epilogue
-    // The slots' sums are joined: both hold the same rows, and each thread takes 64 columns of
-    // its row, from both O's.
-    tc::fence_before_sync();
-    cta_sync();  // every product is complete, every copy has landed
-    tc::fence_after_sync();
-    // (what the row stands for is worked out again rather than kept over the loop)
-    int trow = threadIdx.x & 127;
-    asm volatile("" : "+r"(trow));
-    const int enode = node0 + trow / p.G;
-    const bool evalid = trow < p.npt * p.G && enode < N;
-    const size_t erow = (size_t)(base + enode) * p.hq + g * p.G + trow % p.G;
-    float2* join = reinterpret_cast<float2*>(smem + kOffJoin);
-    join[slot * kRows + trow] = make_float2(m, l);
-    soft_sync();
+    pdl_wait();  // nothing is written before the kernel before has finished
     if (live) {
-      const float2 a = join[trow], c = both ? join[kRows + trow] : make_float2(-INFINITY, 0.f);
-      const float top = fmaxf(a.x, c.x);
-      const float w0 = a.x == -INFINITY ? 0.f : ex2_approx(a.x - top), w1 = c.x == -INFINITY ? 0.f : ex2_approx(c.x - top);
-      const float sum = a.y * w0 + c.y * w1;
-      float inv = sum == 0.f ? 0.f : 1.f / sum;
+      float inv = l == 0.f ? 0.f : 1.f / l;
       // a tree node that this row sees holds an infinity or NaN in V
-      for (int i = 0; i < nt; ++i) {
+      for (int i = 0; i < nb - np; ++i) {
         const uint64_t bad = bars.bad[sp.tb_lo + i];
-        if (bad != 0 && evalid && (__ldcg(p.mask + (size_t)(base + enode) * p.mask_words + sp.tb_lo + i) & bad) != 0) inv = __int_as_float(0x7FC00000);
+        if (bad != 0 && valid && (__ldcg(p.mask + (size_t)(base + node) * p.mask_words + sp.tb_lo + i) & bad) != 0)
+          inv = __int_as_float(0x7FC00000);
       }
-      if (!ok || *abort) inv = 0.f;
-      const float i0 = inv * w0, i1 = inv * w1;
-      pdl_wait();  // nothing is written before the kernel before has finished
-      const uint32_t o0 = tmem + 64 * slot + quarter, o1 = o0 + 128;
+      if (!ok) inv = 0.f;
+      float4* po = p.part_o + ((size_t)group * p.splits + split) * (kRows * kD / 4) + row;
 #pragma unroll 1
       for (int ch = 0; ch < 4; ++ch) {
-        float x[16], y[16];
+        float x[32];
         __syncwarp();
-        tc::tmem_ld16(o0 + 16 * ch, x);
-        tc::tmem_ld16(o1 + 16 * ch, y);
+        tc::tmem_ld32(to + 32 * ch, x);
         tc::tmem_wait_ld();
-        if (!evalid) continue;
+        if (!valid) continue;
 #pragma unroll
-        for (int k = 0; k < 16; ++k) x[k] = both ? x[k] * i0 + y[k] * i1 : x[k] * i0;
+        for (int k = 0; k < 32; ++k) x[k] *= inv;
         if (p.splits == 1) {
-          uint4* dst = reinterpret_cast<uint4*>(p.out + erow * kD + 64 * slot + 16 * ch);
+          uint4* dst = reinterpret_cast<uint4*>(p.out + orow * kD + 32 * ch);
 #pragma unroll
-          for (int k = 0; k < 2; ++k)
+          for (int k = 0; k < 4; ++k)
             dst[k] = make_uint4(pack_bf16x2(x[8 * k], x[8 * k + 1]), pack_bf16x2(x[8 * k + 2], x[8 * k + 3]),
                                 pack_bf16x2(x[8 * k + 4], x[8 * k + 5]), pack_bf16x2(x[8 * k + 6], x[8 * k + 7]));
         } else {
-          float4* po = p.part_o + ((size_t)tile * p.splits + split) * (kRows * kD / 4) + 16 * slot * kRows + trow;
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            po[(ch * 4 + k) * kRows] = make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+          for (int k = 0; k < 8; ++k)
+            po[(ch * 8 + k) * kRows] = make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
         }
       }
-      if (evalid && slot == 0) {
-        const float lse2 = sum == 0.f ? -INFINITY : top + log2f(sum) - kShift;
-        if (p.splits > 1) p.part_lse[((size_t)tile * p.splits + split) * kRows + trow] = lse2;
-        else if (p.lse != nullptr) p.lse[erow] = lse2 * kLn2;
+      if (valid) {
+        const float lse2 = l == 0.f ? -INFINITY : m + log2f(l) - kShift;
+        if (p.splits > 1) p.part_lse[((size_t)group * p.splits + split) * kRows + row] = lse2;
+        else if (p.lse != nullptr) p.lse[orow] = lse2 * kLn2;
       }
     }
-  }
-  if (warp < kSoft0 || warp >= kCvt) {
-    tc::fence_before_sync();
-    cta_sync();
+    __syncwarp();
   }
   tc::fence_before_sync();
   __syncthreads();
@@ -907,13 +817,13 @@ __global__ void __launch_bounds__(kMergeThreads) attn_kv8p_merge_kernel(const Me
 
 static int tiles_of(int max_nodes, int npt) { return ceil_div(max_nodes, npt); }
 
-// Key splits per work item (sequence, KV head, row tile), from the sizes alone; one
+// Key splits per work item (sequence, KV head, two row tiles), from the sizes alone; one
 // CTA fits on an SM. Fewer items than SMs: the splits that cover the SMs. Otherwise the count
-// in 1..8 whose waves cost least (a CTA's fixed cost counted as two blocks), if that is at
+// in 1..8 whose waves cost least (a CTA's fixed cost counted as six blocks), if that is at
 // least 8% below the unsplit cost (the merge kernel is not in the model).
 static int splits_of(int batch, int max_nodes, int hq, int hkv, int max_prefix) {
   const int npt = kRows / (hq / hkv);
-  const long items = (long)batch * hkv * tiles_of(max_nodes, npt), sms = sm_count();
+  const long items = (long)batch * hkv * ceil_div(tiles_of(max_nodes, npt), 2), sms = sm_count();
   const int blocks = ceil_div(max_prefix, kKeys) + ceil_div(max_nodes, kTreeKeys);
   long s = 1;
   if (items > 0 && items < sms) {
@@ -921,13 +831,13 @@ static int splits_of(int batch, int max_nodes, int hq, int hkv, int max_prefix) 
   } else if (items > 0) {
     long best = -1;
     for (long c = 1; c <= 8; ++c) {
-      const long cost = ((items * c + sms - 1) / sms) * ((blocks + c - 1) / c + 2);
+      const long cost = ((items * c + sms - 1) / sms) * ((blocks + c - 1) / c + 6);
       if (best < 0 || cost < best) {
         best = cost;
         s = c;
       }
     }
-    if (s > 1 && best * 100 > ((items + sms - 1) / sms) * (blocks + 2) * 92) s = 1;
+    if (s > 1 && best * 100 > ((items + sms - 1) / sms) * (blocks + 6) * 92) s = 1;
   }
   if (s > blocks) s = blocks;
   if (s > kMaxSplits) s = kMaxSplits;
@@ -979,12 +889,7 @@ int launch_attn_kv8p(const void* q, const uint8_t* k_pool, const uint8_t* v_pool
   }
   static PerDevice smem_set;
   if (per_device(smem_set, [](int) {
-        // (the warpgroups' shares of the registers add up to what a launch starts with only if
-        // the kernel was built with that many)
-        cudaFuncAttributes a;
-        return cudaFuncGetAttributes(&a, attn_kv8p_kernel) == cudaSuccess && a.numRegs == kLaunchRegs &&
-                       cudaFuncSetAttribute(attn_kv8p_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) ==
-                           cudaSuccess
+        return cudaFuncSetAttribute(attn_kv8p_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) == cudaSuccess
                    ? 1
                    : 0;
       }) == 0)
@@ -1018,8 +923,8 @@ int launch_attn_kv8p(const void* q, const uint8_t* k_pool, const uint8_t* v_pool
   prm.early = early_reads() ? 1 : 0;
   prm.batch = batch;
   // (past eight waves the last one is a small share of the grid)
-  prm.lpt = prm.splits == 1 && batch > 1 && batch <= kLptMax && tiles <= 8L * sm_count() ? 1 : 0;
-  const dim3 grid(prm.splits, prm.mtiles, batch * hkv);
+  prm.lpt = prm.splits == 1 && batch > 1 && batch <= kLptMax && tiles <= 16L * sm_count() ? 1 : 0;
+  const dim3 grid(prm.splits, ceil_div(prm.mtiles, 2), batch * hkv);
   if (launch_pdl(attn_kv8p_kernel, grid, dim3(kThreads), kSmem, stream, tm_kp, tm_vp, tm_kt, tm_vt, prm) != cudaSuccess)
     return SPEC_ERR_CUDA;
   if (prm.splits > 1) {
