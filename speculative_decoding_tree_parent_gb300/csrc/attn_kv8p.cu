@@ -43,21 +43,28 @@ namespace kv8p {
 constexpr int kRows = 128;      // rows of a tile
 constexpr int kKeys = 64;       // keys of a prefix block
 constexpr int kPages = kKeys / 16;
-constexpr int kTreeKeys = 64;   // nodes of a tree block
+constexpr int kTreeKeys = 32;   // nodes of a tree block (as many bytes as a prefix block)
 constexpr int kD = 128;
-constexpr int kThreads = 480;
-constexpr int kSoft0 = 2, kMma1 = 10;        // first softmax warp; tile 1's MMA issuer
-constexpr int kStK = 3, kStC = 3, kStV = 3;  // stages: K, V codes, V in 16 bits
-constexpr uint32_t kSlab = 128 * 128;        // 16 KB: a stage, half a tile of q
+constexpr int kThreads = 512;
+constexpr int kSoft0 = 2, kMma1 = 10, kVProd = 15;  // first softmax warp, slot 1's MMA issuer, V's producer
+// stages: K, V codes, V in 16 bits; K's and V's even, so that a slot that takes every other block
+// finds its blocks in stages of its own and sees each phase of their barriers
+constexpr int kStK = 8, kStC = 6, kStV = 2;
+static_assert(kStK % 2 == 0 && kStV % 2 == 0, "a stage has to belong to one slot");
+constexpr uint32_t kSlab = 128 * 128;        // 16 KB: half a tile of q, a stage of V
+constexpr uint32_t kStage = kKeys * 128;      // 8 KB: a stage of K or of V's codes
 constexpr uint32_t kVSlab = kKeys * 128;     // half a stage of V: 64 rows of 64 elements
 constexpr uint32_t kTreeSlab = kTreeKeys * 128;
-constexpr uint32_t kOffQ = 0;                // two tiles: hi and lo codes, then the tree's bf16 rows
+constexpr uint32_t kOffQ = 0;                // two tiles: hi and lo codes, then the tree's bf16 rows; or one: codes, rows
 constexpr uint32_t kOffK = kOffQ + 4 * kSlab;
-constexpr uint32_t kOffC = kOffK + kStK * kSlab;
-constexpr uint32_t kOffV = kOffC + kStC * kSlab;
+constexpr uint32_t kOffC = kOffK + kStK * kStage;
+constexpr uint32_t kOffV = kOffC + kStC * kStage;
+static_assert(2 * kTreeSlab == kStage, "a tree block fills a stage");
 constexpr uint32_t kOffBar = kOffV + kStV * kSlab;
-constexpr uint32_t kOffScale = kOffBar + 640;                 // page scales of two times eight blocks
-constexpr uint32_t kSmem = kOffScale + 64 * 16 + 1024;        // + alignment slack
+constexpr int kScales = 32;                  // blocks whose page scales are kept: four groups of eight
+constexpr uint32_t kOffScale = kOffBar + 640;
+constexpr uint32_t kOffJoin = kOffScale + kScales * kPages * 16;            // float2 [slot][row]: M, sum
+constexpr uint32_t kSmem = kOffJoin + 2 * kRows * 8 + 1024;   // + alignment slack
 static_assert(kSmem <= 232448, "shared memory over the per-CTA limit");
 constexpr uint32_t kTmemCols = 512;          // a tile: S (and P) of even and of odd blocks, O
 constexpr int kLptMax = 1024;                // sequences that are ranked by length
@@ -68,7 +75,7 @@ constexpr uint32_t kIdPV = tc::idesc_f16(kRows, kD, 1);
 constexpr uint32_t kIdTreeQK = tc::idesc_bf16(kRows, kTreeKeys, 0);
 constexpr uint32_t kIdTreePV = tc::idesc_bf16(kRows, kD, 1);
 constexpr int kMaxSplits = 32;
-constexpr int kMaxTreeBlocks = kMaxTreeNodes / kTreeKeys;
+constexpr int kMaxTreeWords = kMaxTreeNodes / 64;
 
 struct Params {
   const __nv_bfloat16* q;
@@ -82,6 +89,7 @@ struct Params {
   const int32_t* qo;
   int hq, hkv, G, npt;  // npt: nodes of a row tile
   int splits, mtiles, batch, lpt;
+  int per_cta;  // row tiles of a CTA: 1 or 2
   float scale_log2;
   __nv_bfloat16* out;
   float* lse;
@@ -98,14 +106,14 @@ struct Bars {
   uint64_t q16[2], q8[2], c_empty[kStC], v_full[kStV], p_full[2][2];  // q in bf16 / as codes
   // one a tile
   uint64_t k_empty[kStK], v_empty[kStV];
-  uint64_t bad[kMaxTreeBlocks];  // tree nodes whose V row holds an infinity or NaN
+  uint64_t bad[kMaxTreeWords];  // tree nodes whose V row holds an infinity or NaN
   uint32_t tmem;
   int abort;
 };
 constexpr int kBar1 = kStK + kStC + 12, kBar4 = kBar1 + 8 + kStC + kStV, kBarAll = kBar4 + kStK + kStV;
-static_assert(sizeof(Bars) <= 512, "barrier block over its reserved bytes");
+static_assert(sizeof(Bars) <= 640, "barrier block over its reserved bytes");
 
-// The blocks of one key split: units are the prefix pages, then the tree blocks (4 each); a
+// The blocks of one key split: units are the prefix pages, then the tree blocks (2 each); a
 // split takes a contiguous run of units, a tree block goes to the split of its first unit.
 struct Split {
   int pg_lo, pg_hi;   // prefix pages
@@ -115,14 +123,14 @@ struct Split {
 };
 __device__ __forceinline__ Split split_of(int P, int N, int splits, int s) {
   const int pages = (P + 15) >> 4, nt = (N + kTreeKeys - 1) / kTreeKeys;
-  const long units = pages + 4L * nt;
+  const long units = pages + 2L * nt;
   const int lo = (int)(s * units / splits), hi = (int)((s + 1) * units / splits);
   Split r;
   r.pg_lo = min(lo, pages);
   r.pg_hi = min(hi, pages);
   r.np = (r.pg_hi - r.pg_lo + kPages - 1) / kPages;
-  r.tb_lo = lo <= pages ? 0 : (lo - pages + 3) >> 2;
-  const int tb_hi = hi <= pages ? 0 : min(nt, (hi - pages + 3) >> 2);
+  r.tb_lo = lo <= pages ? 0 : (lo - pages + 1) >> 1;
+  const int tb_hi = hi <= pages ? 0 : min(nt, (hi - pages + 1) >> 1);
   r.nb = r.np + max(0, tb_hi - r.tb_lo);
   return r;
 }
@@ -178,6 +186,9 @@ __device__ __forceinline__ void warp_arrive(uint32_t bar) {
   __syncwarp();
   tc::mbar_arrive_if((threadIdx.x & 31) == 0, bar);
 }
+
+// The softmax warps of both slots.
+__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
 // 16-byte chunk c of row r of a 128-byte-row slab, in the 128-byte swizzle
 __device__ __forceinline__ uint32_t swz(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
@@ -275,7 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (p.lpt) b = nth_longest(p, b, reinterpret_cast<int*>(smem));
   const int base = ld(p.qo + b), N = ld(p.qo + b + 1) - base, P = ld(p.prefix_len + b);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // (warp: uniform)
-  const int node0 = 2 * blockIdx.y * p.npt;
+  const int node0 = p.per_cta * blockIdx.y * p.npt;
   if (node0 >= N) return;
   if (N > p.mask_words * 64 || P < 0 || P > p.max_len) {
     if (threadIdx.x == 0 && split == 0) {
@@ -284,24 +295,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     return;
   }
-  const int ntiles = node0 + p.npt < N ? 2 : 1;
+  const int ntiles = p.per_cta == 2 && node0 + p.npt < N ? 2 : 1;
   const Split sp = split_of(P, N, p.splits, split);
   const int nb = sp.nb, np = sp.np;
 
-  // softmax threads: tile, row (its TMEM lane), and what the row stands for
+  // softmax threads: slot, tile, row (its TMEM lane), and what the row stands for
   const bool soft = warp >= kSoft0 && warp < kMma1;
-  const int tile = warp >= kSoft0 + 4 ? 1 : 0;
+  // (two tiles: a slot has one of them and every block; one tile: the slots take its blocks in turn)
+  const int slot = warp >= kSoft0 + 4 ? 1 : 0, tile = ntiles == 2 ? slot : 0;
+  const int step = ntiles == 2 ? 1 : 2;
   const int row = (warp & 3) * 32 + lane;
   const int node = node0 + tile * p.npt + row / p.G;
   const int head = g * p.G + row % p.G;
   const bool valid = soft && row < p.npt * p.G && node < N;
   const size_t orow = (size_t)(base + node) * p.hq + head;
-  const int group = 2 * blockIdx.y + tile + p.mtiles * (b * p.hkv + g);
+  const int group = p.per_cta * blockIdx.y + tile + p.mtiles * (b * p.hkv + g);
 
   if (nb == 0) {  // an empty key split: nothing for the merge
     if (soft) {
       pdl_wait();
-      if (valid) p.part_lse[((size_t)group * p.splits + split) * kRows + row] = -INFINITY;
+      if (valid && (ntiles == 2 || slot == 0)) p.part_lse[((size_t)group * p.splits + split) * kRows + row] = -INFINITY;
     }
     return;
   }
@@ -311,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) {
     uint64_t* all = reinterpret_cast<uint64_t*>(&bars);
     for (int x = lane; x < kBarAll; x += 32) tc::mbar_init(bar(all + x), x < kBar1 ? 1 : x < kBar4 ? 4 : ntiles);
-    if (lane < kMaxTreeBlocks) bars.bad[lane] = 0;
+    if (lane < kMaxTreeWords) bars.bad[lane] = 0;
     if (lane == 0) bars.abort = 0;
     tc::mbar_fence_init();
   } else if (warp == 1) {
@@ -323,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (valid) {
     asm volatile("prefetch.global.L2 [%0];" ::"l"(p.q + orow * kD));
     asm volatile("prefetch.global.L2 [%0];" ::"l"(p.q + orow * kD + 64));
-  } else if (warp == 0 && sp.pg_lo + lane < sp.pg_hi) {
+  } else if ((warp == 0 || warp == kVProd) && sp.pg_lo + lane < sp.pg_hi) {
     ids0 = ld(p.page_table + (size_t)b * p.max_pages + sp.pg_lo + lane);
   }
   tc::fence_before_sync();
@@ -332,138 +345,133 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = bars.tmem;
   bool ok = true;
 
-  if (warp == 0) {
-    // ------------------------------------------------------------------ TMA producer
-    // Page ids of eight blocks at a time, one per lane, a batch ahead of their use; an id is
-    // checked when its batch comes up.
+  if (warp == 0 || warp == kVProd) {
+    // ------------------------------------------------------------------ TMA producers
+    // Warp 0 loads K and the pages' scales, the last one V's codes (one warp issuing all copies of
+    // a block took longer than its products). Page ids of eight blocks at a time, one per lane, a
+    // batch ahead of their use; an id is checked when its batch comes up.
+    const bool isv = warp == kVProd;
     const uint32_t leader = elect_one();
+    const int kSt = isv ? kStC : kStK;
+    uint64_t* full = isv ? bars.c_full : bars.k_full;
+    uint64_t* empty = isv ? bars.c_empty : bars.k_empty;
+    const uint32_t ring = sb + (isv ? kOffC : kOffK);
+    const CUtensorMap* tm_tree = isv ? &tm_vt : &tm_kt;
+    const CUtensorMap* tm_pool = isv ? &tm_vp : &tm_kp;
     auto ids_of = [&](int k) -> int {
       const int lp = sp.pg_lo + 32 * k + lane;
       return lp < sp.pg_hi ? ld(p.page_table + (size_t)b * p.max_pages + lp) : p.num_pages;
     };
     auto checked = [&](int page, int k) -> int {
       if (page >= 0 && page < p.num_pages) return page;
-      if (sp.pg_lo + 32 * k + lane < sp.pg_hi) report(p.status, SPEC_ERR_PAGE);
+      if (!isv && sp.pg_lo + 32 * k + lane < sp.pg_hi) report(p.status, SPEC_ERR_PAGE);
       return p.num_pages;  // out of range: TMA reads zeros
     };
     auto scale_of = [&](int page) {
-      return page < p.num_pages ? ld(p.kv_scale + (size_t)page * p.hkv + g) : make_float2(1.f, 1.f);
+      return !isv && page < p.num_pages ? ld(p.kv_scale + (size_t)page * p.hkv + g) : make_float2(1.f, 1.f);
     };
     int ids = checked(ids0, 0), ids_next = ids_of(1);
     float2 sc = scale_of(ids), sc_next = sc;
-    int k_done = 0, c_done = 0;  // blocks whose copies were issued
+    int done = 0;  // blocks whose copies were issued
 #pragma unroll 1
-    for (int j = 0; j < nb; ++j) {
-      const int sk = j % kStK, sc_ = j % kStC;
-      if (j < np && (j & 7) == 0) {
-        if (j > 0) {
+    for (int j = 0, st = 0, turn = 0; j < nb; ++j, ++st) {
+      if (st == kSt) st = 0, ++turn;
+      if (turn > 0 && !wait_all(bar(&empty[st]), (turn & 1) ^ 1, abort)) break;
+      const uint32_t dst = ring + st * kStage;
+      // (one lane issues, the others' part predicated off: a copy by each of eight lanes cost about
+      // 60 cycles more a copy)
+      tc::expect_tx_if(leader, bar(&full[st]), j < np ? kKeys * 128 : 2 * kTreeSlab);
+      if (j < np) {
+        if ((j & 7) == 0 && j > 0) {
           ids = ids_next;
           sc = sc_next;
           ids_next = ids_of((j >> 3) + 1);
         }
-        // The scales of these eight blocks. What their places held, sixteen to nine blocks ago, has
-        // been read: the code stage of three blocks ago was filled after the converters' wait for the
-        // PV of three before that, which follows both tiles' softmax of that block.
-        const float vs = page_scale(sc.y);
-        *reinterpret_cast<float4*>(smem + kOffScale + (((j >> 3) & 1) * 32 + lane) * 16) =
-            make_float4(page_scale(sc.x), log2f(vs), 1.f / vs, 0.f);
-        warp_arrive(bar(&bars.sc_full[(j >> 3) & 1]));
-      }
-      if (j >= kStK && !wait_all(bar(&bars.k_empty[sk]), ((j / kStK) & 1) ^ 1, abort)) break;
-      const uint32_t kdst = sb + kOffK + sk * kSlab, cdst = sb + kOffC + sc_ * kSlab;
-      // (one lane issues, the others' part predicated off: a copy by each of eight lanes cost about
-      // 60 cycles more a copy)
-      const uint32_t bytes = j < np ? kKeys * 128 : 2 * kTreeSlab;
-      tc::expect_tx_if(leader, bar(&bars.k_full[sk]), bytes);
-      if (j < np) {
 #pragma unroll
         for (int pp = 0; pp < kPages; ++pp)
-          tc::tma_load_4d_if(leader, kdst + pp * 2048, &tm_kp, bar(&bars.k_full[sk]), 0, 0, g,
+          tc::tma_load_4d_if(leader, dst + pp * 2048, tm_pool, bar(&full[st]), 0, 0, g,
                              __shfl_sync(0xffffffffu, ids, (j & 7) * kPages + pp));
+        if ((j & 7) == 4) {
+          ids_next = checked(ids_next, (j >> 3) + 1);
+          sc_next = scale_of(ids_next);
+        }
+        if (!isv && (j & 7) == 0) {
+          // The scales of these eight blocks. What their places held, thirty-two to twenty-five
+          // blocks ago, has been read: the stage just filled was released by QK of eight blocks ago,
+          // which its slot issued after PV of twelve blocks ago at the latest, so after that block's
+          // softmax; the stage filled before it by QK of nine, after the softmax of thirteen.
+          const float vs = page_scale(sc.y);
+          *reinterpret_cast<float4*>(smem + kOffScale + ((j % kScales) * kPages + lane) * 16) =
+              make_float4(page_scale(sc.x), log2f(vs), 1.f / vs, 0.f);
+          warp_arrive(bar(&bars.sc_full[(j >> 3) & 1]));
+        }
       } else {
 #pragma unroll
         for (int h = 0; h < 2; ++h)  // two 64-column halves
-          tc::tma_load_3d_if(leader, kdst + h * kTreeSlab, &tm_kt, bar(&bars.k_full[sk]), h * 64, g,
+          tc::tma_load_3d_if(leader, dst + h * kTreeSlab, tm_tree, bar(&full[st]), h * 64, g,
                              base + (sp.tb_lo + j - np) * kTreeKeys);
       }
-      k_done = j + 1;
-      if (j >= kStC && !wait_all(bar(&bars.c_empty[sc_]), ((j / kStC) & 1) ^ 1, abort)) break;
-      tc::expect_tx_if(leader, bar(&bars.c_full[sc_]), bytes);
-      if (j < np) {
-#pragma unroll
-        for (int pp = 0; pp < kPages; ++pp)
-          tc::tma_load_4d_if(leader, cdst + pp * 2048, &tm_vp, bar(&bars.c_full[sc_]), 0, 0, g,
-                             __shfl_sync(0xffffffffu, ids, (j & 7) * kPages + pp));
-      } else {
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          tc::tma_load_3d_if(leader, cdst + h * kTreeSlab, &tm_vt, bar(&bars.c_full[sc_]), h * 64, g,
-                             base + (sp.tb_lo + j - np) * kTreeKeys);
-      }
-      c_done = j + 1;
-      if (j < np && (j & 7) == 4) {
-        ids_next = checked(ids_next, (j >> 3) + 1);
-        sc_next = scale_of(ids_next);
-      }
+      done = j + 1;
     }
-    if (c_done < nb && lane == 0) {  // given up: leave no copy in flight
+    if (done < nb && lane == 0) {  // given up: leave no copy in flight
       report(p.status, SPEC_ERR_TIMEOUT);
       int zero = 0;
-      for (int j = max(0, k_done - kStK); j < k_done; ++j)
-        tc::mbar_wait(bar(&bars.k_full[j % kStK]), (j / kStK) & 1, &zero, kWaitLimit);
-      for (int j = max(0, c_done - kStC); j < c_done; ++j)
-        tc::mbar_wait(bar(&bars.c_full[j % kStC]), (j / kStC) & 1, &zero, kWaitLimit);
+      for (int j = max(0, done - kSt); j < done; ++j)
+        tc::mbar_wait(bar(&full[j % kSt]), (j / kSt) & 1, &zero, kWaitLimit);
     }
     __syncwarp();
   } else if (warp == 1 || warp == kMma1) {
-    // ------------------------------------------------------------------ MMA issuers, one a tile
-    const int t = warp == 1 ? 0 : 1;
-    if (t < ntiles && elect_one()) {
+    // ------------------------------------------------------------------ MMA issuers, one a slot
+    const int t = warp == 1 ? 0 : 1, j0 = ntiles == 2 ? 0 : t;
+    if (j0 < nb && elect_one()) {
       const uint32_t ts = tmem + 256 * t, to = ts + 128;
-      const uint32_t qb = sb + kOffQ + t * 2 * kSlab;
-      auto qk = [&](int j) {
+      const uint32_t q8 = sb + kOffQ + (ntiles == 2 ? t : 0) * 2 * kSlab, q16 = sb + kOffQ + (ntiles == 2 ? t : 1) * 2 * kSlab;
+      bool codes = false, rows = false;  // q has been waited for
+      auto qk = [&](int j, int n) {
         const int sk = j % kStK;
-        if (j == 0 && np > 0) ok = wait_one(bar(&bars.q8[t]), 0, abort);
-        if (j == np) ok = ok && wait_one(bar(&bars.q16[t]), 0, abort);
+        if (j < np && !codes) ok = codes = wait_one(bar(&bars.q8[ntiles == 2 ? t : 0]), 0, abort);
+        if (j >= np && !rows) ok = rows = wait_one(bar(&bars.q16[ntiles == 2 ? t : 1]), 0, abort);
         ok = ok && wait_one(bar(&bars.k_full[sk]), (j / kStK) & 1, abort);
         if (!ok) return;
         tc::fence_after_sync();
-        const uint32_t kb = sb + kOffK + sk * kSlab, d = ts + 64 * (j & 1);
-        const uint64_t qd = tc::sdesc_sw128(qb, 16, 1024), kd = tc::sdesc_sw128(kb, 16, 1024);
+        const uint32_t d = ts + 64 * (n & 1);
+        const uint64_t kd = tc::sdesc_sw128(sb + kOffK + sk * kStage, 16, 1024);
         if (j < np) {
+          const uint64_t qd = tc::sdesc_sw128(q8, 16, 1024);
 #pragma unroll
           for (int k = 0; k < 8; ++k)  // hi, then lo
             tc::mma_f8(d, qd + (((k >> 2) * kSlab + (k & 3) * 32) >> 4), kd + (((k & 3) * 32) >> 4), kIdQK, k > 0);
         } else {
+          const uint64_t qd = tc::sdesc_sw128(q16, 16, 1024);
 #pragma unroll 1
           for (int k = 0; k < 8; ++k)
             tc::mma_bf16(d, qd + (((k >> 2) * kSlab + (k & 3) * 32) >> 4),
                          kd + (((k >> 2) * kTreeSlab + (k & 3) * 32) >> 4), kIdTreeQK, k > 0);
         }
-        tc::mma_commit(bar(&bars.s_full[t][j & 1]));
+        tc::mma_commit(bar(&bars.s_full[t][n & 1]));
         tc::mma_commit(bar(&bars.k_empty[sk]));
       };
-      qk(0);
+      qk(j0, 0);
 #pragma unroll 1
-      for (int j = 0; ok && j < nb; ++j) {
-        if (j + 1 < nb) qk(j + 1);  // S of the next block while the softmax works on this one
+      for (int j = j0, n = 0; ok && j < nb; j += step, ++n) {
+        if (j + step < nb) qk(j + step, n + 1);  // S of the next block while the softmax works on this one
         const int sv = j % kStV;
         ok = ok && wait_one(bar(&bars.v_full[sv]), (j / kStV) & 1, abort) &&
-             wait_one(bar(&bars.p_full[t][j & 1]), (j >> 1) & 1, abort);
+             wait_one(bar(&bars.p_full[t][n & 1]), (n >> 1) & 1, abort);
         if (!ok) break;
         tc::fence_after_sync();
         // P stands where its S stood; the QK that next overwrites it follows this PV in order
         const uint64_t vd = tc::sdesc_sw128(sb + kOffV + sv * kSlab, kVSlab, 1024);
-        const uint32_t tp = ts + 64 * (j & 1);
+        const uint32_t tp = ts + 64 * (n & 1);
         if (j < np) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) tc::mma_bf16_ts(to, tp + 8 * k, vd + ((k * 2048) >> 4), kIdPV, j > 0 || k > 0);
+          for (int k = 0; k < 4; ++k) tc::mma_bf16_ts(to, tp + 8 * k, vd + ((k * 2048) >> 4), kIdPV, n > 0 || k > 0);
         } else {
 #pragma unroll 1
-          for (int k = 0; k < 8; ++k)  // P's two bf16 terms, four steps of 16 nodes each
-            tc::mma_bf16_ts(to, tp + 8 * k, vd + (((k & 3) * 2048) >> 4), kIdTreePV, j > 0 || k > 0);
+          for (int k = 0; k < 4; ++k)  // P's two bf16 terms, two steps of 16 nodes each
+            tc::mma_bf16_ts(to, tp + 8 * k, vd + (((k & 1) * 2048) >> 4), kIdTreePV, n > 0 || k > 0);
         }
-        tc::mma_commit(bar(&bars.pv_done[t][j & 1]));
+        tc::mma_commit(bar(&bars.pv_done[t][n & 1]));
         tc::mma_commit(bar(&bars.v_empty[sv]));
       }
       if (!ok) report(p.status, SPEC_ERR_TIMEOUT);
@@ -486,15 +494,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = wait_all(bar(&bars.c_full[sc_]), (j / kStC) & 1, abort);
       if (j >= kStV) ok = ok && wait_all(bar(&bars.v_empty[sv]), ((j / kStV) & 1) ^ 1, abort);
       if (!ok) break;
-      uint8_t* src = smem + kOffC + sc_ * kSlab;
+      uint8_t* src = smem + kOffC + sc_ * kStage;
       uint8_t* dst = smem + kOffV + sv * kSlab;
       if (j >= np) {
         // bf16 rows as they are, but for rows past the tree and elements that are not finite
         // (a weight of 0 times either would reach rows whose mask leaves the node out)
         const int tb = sp.tb_lo + j - np, nvalid = N - tb * kTreeKeys;
 #pragma unroll 1
-        for (int it = 0; it < 8; ++it) {
-          const int id = it * 128 + ct, half = id >> 9, off = id & 511, r = off >> 3;
+        for (int it = 0; it < 4; ++it) {
+          const int id = it * 128 + ct, half = id >> 8, off = id & 255, r = off >> 3;
           const uint4 w = *reinterpret_cast<const uint4*>(src + half * kTreeSlab + off * 16);
           uint32_t u[4] = {w.x, w.y, w.z, w.w};
           bool bad = false;
@@ -510,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               bad = true;
             }
           }
-          if (bad) atomicOr(reinterpret_cast<unsigned long long*>(&bars.bad[tb]), 1ull << r);
+          if (bad) atomicOr(reinterpret_cast<unsigned long long*>(&bars.bad[tb >> 1]), 1ull << (r + 32 * (tb & 1)));
           *reinterpret_cast<uint4*>(dst + half * kVSlab + off * 16) = make_uint4(u[0], u[1], u[2], u[3]);
         }
       } else {
@@ -543,16 +551,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       warp_arrive(bar(&bars.c_empty[sc_]));
     }
     if (!ok && lane == 0) report(p.status, SPEC_ERR_TIMEOUT);
-  } else if (tile < ntiles) {
+  } else {
     // ------------------------------------------------------------------ softmax
-    const uint32_t ts = tmem + 256 * tile + ((uint32_t)((warp & 3) * 32) << 16), to = ts + 128;
+    const uint32_t quarter = (uint32_t)((warp & 3) * 32) << 16, ts = tmem + 256 * slot + quarter, to = ts + 128;
     const bool live = __any_sync(0xffffffffu, valid);  // a warp without rows only keeps step
     const float scale_log2 = p.scale_log2;
     const uint4* qrow = reinterpret_cast<const uint4*>(p.q + orow * kD);
-    uint8_t* qs = smem + kOffQ + tile * 2 * kSlab;
+    float2* join = reinterpret_cast<float2*>(smem + kOffJoin);
     float m = -INFINITY, l = 0.f;  // running maximum and sum
     // M follows the row's maximum, and O is rescaled where it moves
-    auto raise = [&](int j, float mx) {
+    auto raise = [&](int n, float mx) {
       const bool moves = mx > -INFINITY && (m == -INFINITY || mx > m + kGrow);
       if (__any_sync(0xffffffffu, moves)) {
         float alpha = 1.f;
@@ -561,8 +569,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           m = mx;
           l *= alpha;
         }
-        if (j > 0) {  // O is complete up to the block before
-          ok = wait_all(bar(&bars.pv_done[tile][(j - 1) & 1]), ((j - 1) >> 1) & 1, abort) && ok;
+        if (n > 0) {  // O is complete up to the block before
+          ok = wait_all(bar(&bars.pv_done[slot][(n - 1) & 1]), ((n - 1) >> 1) & 1, abort) && ok;
           tc::fence_after_sync();
 #pragma unroll 1
           for (int ch = 0; ch < kD / 16; ++ch) {
@@ -577,7 +585,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       return m == -INFINITY ? 0.f : kShift - m;
     };
-    // the tree's q: its rows as they are, where the codes stood
+    // the tree's q: its rows as they are; of two tiles, where the codes stood
     auto store_q16 = [&]() {
 #pragma unroll 1
       for (int k = 0; k < 16; k += 4) {
@@ -585,32 +593,38 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] = valid ? ld(qrow + k + e) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) *reinterpret_cast<uint4*>(qs + (k >> 3) * kSlab + swz(row, (k + e) & 7)) = v[e];
+        for (int e = 0; e < 4; ++e) *reinterpret_cast<uint4*>(smem + kOffQ + (2 * slot + (k >> 3)) * kSlab + swz(row, (k + e) & 7)) = v[e];
       }
       tc::fence_proxy_async_smem();
-      warp_arrive(bar(&bars.q16[tile]));
+      warp_arrive(bar(&bars.q16[slot]));
     };
     float rowf = scale_log2;
-    if (np > 0) {
-      rowf *= split_row(qrow, valid, qs, row);
+    if (np > 0 && (ntiles == 2 || slot == 0)) {
+      const float qf = split_row(qrow, valid, smem + kOffQ + tile * 2 * kSlab, row);
+      if (ntiles == 1) join[row].x = qf;
+      rowf *= qf;
       tc::fence_proxy_async_smem();
-      warp_arrive(bar(&bars.q8[tile]));
-    } else {
-      store_q16();
+      warp_arrive(bar(&bars.q8[slot]));
     }
-    int left = min(P, sp.pg_hi * 16) - sp.pg_lo * 16;  // prefix keys from this block's first on
+    if (nb > np && (ntiles == 2 ? np == 0 : slot == 1)) store_q16();
+    if (np > 0 && ntiles == 1 && slot == 1) {  // the same row's factor, from the other slot
+      ok = wait_all(bar(&bars.q8[0]), 0, abort);
+      rowf *= join[row].x;
+    }
+    int j = ntiles == 2 ? 0 : slot, n = 0;
+    int left = min(P, sp.pg_hi * 16) - (sp.pg_lo + j * kPages) * 16;  // prefix keys from this block's first on
 #pragma unroll 1
-    for (int j = 0; ok && j < np; ++j, left -= kKeys) {
-      if ((j & 7) == 0) ok = wait_all(bar(&bars.sc_full[(j >> 3) & 1]), (j >> 4) & 1, abort);
-      const float4* scale = reinterpret_cast<const float4*>(smem + kOffScale) + (j & 15) * kPages;
+    for (; ok && j < np; j += step, ++n, left -= step * kKeys) {
+      if ((j & 7) < step) ok = wait_all(bar(&bars.sc_full[(j >> 3) & 1]), (j >> 4) & 1, abort);
+      const float4* scale = reinterpret_cast<const float4*>(smem + kOffScale) + (j % kScales) * kPages;
       float4 f[kPages];
 #pragma unroll
       for (int pp = 0; pp < kPages; ++pp) f[pp] = scale[pp];
-      ok = ok && wait_all(bar(&bars.s_full[tile][j & 1]), (j >> 1) & 1, abort);
+      ok = ok && wait_all(bar(&bars.s_full[slot][n & 1]), (n >> 1) & 1, abort);
       if (!ok) break;
       tc::fence_after_sync();
-      if (j == np - 1 && nb > np) store_q16();  // (every QK over the codes is complete)
-      const uint32_t tj = ts + 64 * (j & 1);
+      if (j == np - 1 && nb > np && ntiles == 2) store_q16();  // (every QK over the codes is complete)
+      const uint32_t tj = ts + 64 * (n & 1);
       if (live) {
         if (left < kKeys) {  // the last block's keys past the prefix
 #pragma unroll 1
@@ -631,7 +645,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           f[pp].x = factor(rowf, f[pp].x);
           mx = fmaxf(mx, fmaf(fmaxf(x, v[15]), f[pp].x, f[pp].y));
         }
-        const float off = raise(j, mx);
+        const float off = raise(n, mx);
         uint32_t pk[kKeys / 2];
 #pragma unroll
         for (int pp = 0; pp < kPages; ++pp) {
@@ -657,35 +671,34 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::tmem_wait_st();
       }
       tc::fence_before_sync();
-      if (ok) warp_arrive(bar(&bars.p_full[tile][j & 1]));
+      if (ok) warp_arrive(bar(&bars.p_full[slot][n & 1]));
     }
-    if (ok && nb > np) {
+    if (ok && j < nb) {
       pdl_wait();  // the mask may come from the kernel before
-      const uint64_t* mrow = p.mask + (size_t)(base + node) * p.mask_words + sp.tb_lo;
-      uint64_t bits = valid ? __ldcg(mrow) : 0ull;
+      const uint32_t* mrow = reinterpret_cast<const uint32_t*>(p.mask + (size_t)(base + node) * p.mask_words) + sp.tb_lo;
+      uint32_t bits = valid ? __ldcg(mrow + j - np) : 0u;
 #pragma unroll 1
-      for (int j = np; ok && j < nb; ++j) {  // P as two bf16 terms
-        ok = wait_all(bar(&bars.s_full[tile][j & 1]), (j >> 1) & 1, abort);
+      for (; ok && j < nb; j += step, ++n) {  // P as two bf16 terms
+        ok = wait_all(bar(&bars.s_full[slot][n & 1]), (n >> 1) & 1, abort);
         if (!ok) break;
         tc::fence_after_sync();
-        const uint32_t tj = ts + 64 * (j & 1);
+        const uint32_t tj = ts + 64 * (n & 1);
         if (live) {
-          const uint64_t see = bits;
-          if (valid && j + 1 < nb) bits = __ldcg(mrow + j + 1 - np);
+          const uint32_t see = bits;
+          if (valid && j + step < nb) bits = __ldcg(mrow + j + step - np);
           float s[kTreeKeys];
           tc::tmem_ld32(tj, s);
-          tc::tmem_ld32(tj + 32, s + 32);
           tc::tmem_wait_ld();
           float mx = -INFINITY;
 #pragma unroll
           for (int c = 0; c < kTreeKeys; ++c) {
-            s[c] = ((see >> c) & 1ull) ? s[c] * scale_log2 : -INFINITY;
+            s[c] = ((see >> c) & 1u) ? s[c] * scale_log2 : -INFINITY;
             mx = fmaxf(mx, s[c]);
           }
-          const float off = raise(j, mx);
+          const float off = raise(n, mx);
           float sum0 = 0.f, sum1 = 0.f;
 #pragma unroll
-          for (int h = 0; h < 4; ++h) {
+          for (int h = 0; h < 2; ++h) {
             uint32_t hi[8], lo[8];
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
@@ -696,54 +709,76 @@ __global__ void __launch_bounds__(kThreads, 1)
               lo[c] = pack_bf16x2(a - __uint_as_float(hi[c] << 16), d - __uint_as_float(hi[c] & 0xFFFF0000u));
             }
             tc::tmem_st8_u(tj + 8 * h, hi);
-            tc::tmem_st8_u(tj + 32 + 8 * h, lo);
+            tc::tmem_st8_u(tj + 16 + 8 * h, lo);
           }
           l += sum0 + sum1;
           tc::tmem_wait_st();
         }
         tc::fence_before_sync();
-        if (ok) warp_arrive(bar(&bars.p_full[tile][j & 1]));
+        if (ok) warp_arrive(bar(&bars.p_full[slot][n & 1]));
       }
     }
-    ok = ok && wait_all(bar(&bars.pv_done[tile][(nb - 1) & 1]), ((nb - 1) >> 1) & 1, abort);
+    if (n > 0) ok = ok && wait_all(bar(&bars.pv_done[slot][(n - 1) & 1]), ((n - 1) >> 1) & 1, abort);
     if (!ok && lane == 0) report(p.status, SPEC_ERR_TIMEOUT);
-    tc::fence_after_sync();
 
     // -------------------------------------------------------------------- epilogue
+    // Of one tile, the slots' sums are joined: both hold the same rows, and each thread takes 64
+    // columns of its row, from both O's; of two, a thread has its row's 128 columns.
+    float2 other = make_float2(-INFINITY, 0.f);
+    if (ntiles == 1) {
+      tc::fence_before_sync();
+      soft_sync();  // (the factors have been read)
+      join[slot * kRows + row] = make_float2(m, l);
+      soft_sync();
+      other = join[(slot ^ 1) * kRows + row];
+    }
+    tc::fence_after_sync();
     pdl_wait();  // nothing is written before the kernel before has finished
     if (live) {
-      float inv = l == 0.f ? 0.f : 1.f / l;
+      const float top = fmaxf(m, other.x);
+      const float w0 = m == -INFINITY ? 0.f : ex2_approx(m - top), w1 = other.x == -INFINITY ? 0.f : ex2_approx(other.x - top);
+      const float sum = l * w0 + other.y * w1;
+      float inv = sum == 0.f ? 0.f : 1.f / sum;
       // a tree node that this row sees holds an infinity or NaN in V
-      for (int i = 0; i < nb - np; ++i) {
-        const uint64_t bad = bars.bad[sp.tb_lo + i];
-        if (bad != 0 && valid && (__ldcg(p.mask + (size_t)(base + node) * p.mask_words + sp.tb_lo + i) & bad) != 0)
+#pragma unroll 1
+      for (int i = sp.tb_lo >> 1; 2 * i < sp.tb_lo + nb - np; ++i) {
+        const uint64_t bad = bars.bad[i];
+        if (bad != 0 && valid && (__ldcg(p.mask + (size_t)(base + node) * p.mask_words + i) & bad) != 0)
           inv = __int_as_float(0x7FC00000);
       }
-      if (!ok) inv = 0.f;
+      if (!ok || *abort) inv = 0.f;
+      const float i0 = inv * w0, i1 = inv * w1;
+      const bool mine = n > 0, theirs = ntiles == 1 && nb > (slot ^ 1);  // an O that was written
+      const uint32_t to2 = tmem + 256 * (slot ^ 1) + 128 + quarter;
       float4* po = p.part_o + ((size_t)group * p.splits + split) * (kRows * kD / 4) + row;
+      const int c0 = ntiles == 2 ? 0 : 4 * slot, c1 = ntiles == 2 ? 8 : c0 + 4;
 #pragma unroll 1
-      for (int ch = 0; ch < 4; ++ch) {
-        float x[32];
+      for (int ch = c0; ch < c1; ++ch) {
+        float x[16], y[16];
         __syncwarp();
-        tc::tmem_ld32(to + 32 * ch, x);
+        tc::tmem_ld16(to + 16 * ch, x);
+        if (theirs) tc::tmem_ld16(to2 + 16 * ch, y);
         tc::tmem_wait_ld();
         if (!valid) continue;
 #pragma unroll
-        for (int k = 0; k < 32; ++k) x[k] *= inv;
+        for (int k = 0; k < 16; ++k) {
+          x[k] = mine ? x[k] * i0 : 0.f;
+          if (theirs) x[k] += y[k] * i1;
+        }
         if (p.splits == 1) {
-          uint4* dst = reinterpret_cast<uint4*>(p.out + orow * kD + 32 * ch);
+          uint4* dst = reinterpret_cast<uint4*>(p.out + orow * kD + 16 * ch);
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
+          for (int k = 0; k < 2; ++k)
             dst[k] = make_uint4(pack_bf16x2(x[8 * k], x[8 * k + 1]), pack_bf16x2(x[8 * k + 2], x[8 * k + 3]),
                                 pack_bf16x2(x[8 * k + 4], x[8 * k + 5]), pack_bf16x2(x[8 * k + 6], x[8 * k + 7]));
         } else {
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            po[(ch * 8 + k) * kRows] = make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+          for (int k = 0; k < 4; ++k)
+            po[(ch * 4 + k) * kRows] = make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
         }
       }
-      if (valid) {
-        const float lse2 = l == 0.f ? -INFINITY : m + log2f(l) - kShift;
+      if (valid && (ntiles == 2 || slot == 0)) {
+        const float lse2 = sum == 0.f ? -INFINITY : top + log2f(sum) - kShift;
         if (p.splits > 1) p.part_lse[((size_t)group * p.splits + split) * kRows + row] = lse2;
         else if (p.lse != nullptr) p.lse[orow] = lse2 * kLn2;
       }
@@ -817,13 +852,22 @@ __global__ void __launch_bounds__(kMergeThreads) attn_kv8p_merge_kernel(const Me
 
 static int tiles_of(int max_nodes, int npt) { return ceil_div(max_nodes, npt); }
 
+// Row tiles that a CTA has: two where the sequence has them (they share K, V and V's conversion),
+// unless one a CTA is what it takes to put a CTA on every SM without cutting the keys into more
+// splits, each of which writes its partial result.
+static int tiles_per_cta(int batch, int max_nodes, int hq, int hkv) {
+  const int tiles = tiles_of(max_nodes, kRows / (hq / hkv));
+  return tiles > 1 && (long)batch * hkv * ceil_div(tiles, 2) >= sm_count() ? 2 : 1;
+}
+
 // Key splits per work item (sequence, KV head, two row tiles), from the sizes alone; one
 // CTA fits on an SM. Fewer items than SMs: the splits that cover the SMs. Otherwise the count
 // in 1..8 whose waves cost least (a CTA's fixed cost counted as six blocks), if that is at
 // least 8% below the unsplit cost (the merge kernel is not in the model).
 static int splits_of(int batch, int max_nodes, int hq, int hkv, int max_prefix) {
   const int npt = kRows / (hq / hkv);
-  const long items = (long)batch * hkv * ceil_div(tiles_of(max_nodes, npt), 2), sms = sm_count();
+  const long items = (long)batch * hkv * ceil_div(tiles_of(max_nodes, npt), tiles_per_cta(batch, max_nodes, hq, hkv));
+  const long sms = sm_count();
   const int blocks = ceil_div(max_prefix, kKeys) + ceil_div(max_nodes, kTreeKeys);
   long s = 1;
   if (items > 0 && items < sms) {
@@ -911,6 +955,7 @@ int launch_attn_kv8p(const void* q, const uint8_t* k_pool, const uint8_t* v_pool
   prm.npt = kRows / G;
   prm.splits = splits_of(batch, max_nodes, hq, hkv, max_prefix);
   prm.mtiles = tiles_of(max_nodes, prm.npt);
+  prm.per_cta = tiles_per_cta(batch, max_nodes, hq, hkv);
   prm.scale_log2 = sm_scale * kLog2e;
   prm.out = static_cast<__nv_bfloat16*>(out);
   prm.lse = lse;
@@ -924,7 +969,7 @@ int launch_attn_kv8p(const void* q, const uint8_t* k_pool, const uint8_t* v_pool
   prm.batch = batch;
   // (past eight waves the last one is a small share of the grid)
   prm.lpt = prm.splits == 1 && batch > 1 && batch <= kLptMax && tiles <= 16L * sm_count() ? 1 : 0;
-  const dim3 grid(prm.splits, ceil_div(prm.mtiles, 2), batch * hkv);
+  const dim3 grid(prm.splits, ceil_div(prm.mtiles, prm.per_cta), batch * hkv);
   if (launch_pdl(attn_kv8p_kernel, grid, dim3(kThreads), kSmem, stream, tm_kp, tm_vp, tm_kt, tm_vt, prm) != cudaSuccess)
     return SPEC_ERR_CUDA;
   if (prm.splits > 1) {
