@@ -492,7 +492,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int j = 0; j < nb; ++j) {
       const int sc_ = j % kStC, sv = j % kStV;
       ok = wait_all(bar(&bars.c_full[sc_]), (j / kStC) & 1, abort);
-      if (j >= kStV) ok = ok && wait_all(bar(&bars.v_empty[sv]), ((j / kStV) & 1) ^ 1, abort);
       if (!ok) break;
       uint8_t* src = smem + kOffC + sc_ * kStage;
       uint8_t* dst = smem + kOffV + sv * kSlab;
@@ -500,6 +499,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // bf16 rows as they are, but for rows past the tree and elements that are not finite
         // (a weight of 0 times either would reach rows whose mask leaves the node out)
         const int tb = sp.tb_lo + j - np, nvalid = N - tb * kTreeKeys;
+        if (j >= kStV) ok = wait_all(bar(&bars.v_empty[sv]), ((j / kStV) & 1) ^ 1, abort);
+        if (!ok) break;
 #pragma unroll 1
         for (int it = 0; it < 4; ++it) {
           const int id = it * 128 + ct, half = id >> 8, off = id & 255, r = off >> 3;
@@ -533,6 +534,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint4 w[4];
 #pragma unroll
         for (int it = 0; it < 4; ++it) w[it] = *reinterpret_cast<const uint4*>(src + src0 + it * 2048);
+        if (j >= kStV) ok = wait_all(bar(&bars.v_empty[sv]), ((j / kStV) & 1) ^ 1, abort);
+        if (!ok) break;
 #pragma unroll
         for (int it = 0; it < 4; ++it) {
           const uint32_t u[4] = {w[it].x, w[it].y, w[it].z, w[it].w};
