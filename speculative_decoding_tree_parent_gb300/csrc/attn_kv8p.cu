@@ -20,19 +20,28 @@
 // x log2 e + log2 vs (P stays below 2^15, and full precision reaches 2^25 below the largest);
 // the row sum adds P_j / vs_j per page.
 //
-// A CTA = (key split, row tile, sequence x KV head). A row tile is 128 rows: 128 / G nodes
-// (rounded down) of G heads each. K/V come in blocks: first the split's tree blocks (64 nodes,
-// bf16), then its prefix blocks (128 keys, 8 pages, TMA page by page). Two groups of four softmax
-// warps (one row per thread) take the blocks in turn, each with its own O; the sums are joined at
-// the end. One S and one P serve both: a group has S in registers soon after it is complete, so QK
-// of the next block runs, for the other group, under this one's exponentials, and P is written
-// only when it is all there, then read by PV at once. The time a block takes is thus about half of
-// what one group needs for it, and every barrier is passed once for 128 keys.
-// q's codes stand in TMEM (64 columns), the A operand of QK: read from shared memory for every
-// product they took as much of that memory's bandwidth as K did.
-// Warps (512 threads): 0 and 3 TMA producers (K, V), 1 and 2 MMA issuers (QK; PV), 4-7 and
-// 8-11 softmax, 12-15 V's converters. Every wait is bounded.
+// A CTA = (key split, one or two row tiles, sequence x KV head). A row tile is 128 rows: 128 / G
+// nodes (rounded down) of G heads each. K/V come in blocks: the split's prefix blocks (64 keys, 4
+// pages, TMA page by page), then its tree blocks (32 nodes, bf16). Two slots, each with its own MMA
+// issuer, four softmax warps (one row per thread) and TMEM (S of its even and of its odd blocks, P
+// over the S it comes from, O): of two tiles a slot has one, and K, V and V's conversion serve both;
+// of one tile the slots take the blocks in turn and their sums are joined at the end. QK of a slot's
+// next block runs under the softmax of this one.
+// q's codes (hi and lo) stand in shared memory, later its bf16 rows for the tree.
+// Warps (512 threads, 128 registers): 0 and 15 TMA producers (K, V's codes), 1 and 10 MMA issuers,
+// 2-5 and 6-9 softmax, 11-14 V's converters. Every wait is bounded.
 // Splits write O / l in fp32 and the log2-sum-exp, joined by a second kernel.
+//
+// Bound (one GB300): not HBM and not the tensor cores but the blocks' chain (QK, softmax, PV, each
+// handed on through a barrier) and the issue of its instructions; a block of 64 keys takes about
+// 1200 cycles for one tile and for two. 128 sequences of one token over 543,000 keys (1.1 GB): 293 us,
+// 3.8 TB/s; 32 trees of 64 nodes over 512 .. 8192 keys: 164 us, 0.91 of 1.93 PFLOP/s; 8 x 128 nodes
+// over 32768 keys: 984 us, 1.0 PFLOP/s.
+// What was measured beside it: one tile a CTA with its softmax split over all eight warps, 128-key
+// blocks and q in TMEM, 293 -> 300, 164 -> 246, 984 -> 1010 us; two tiles in 128-key blocks with one
+// S each, 330, 199, 1260; one producer for K and V 404, 161, 973 (one tile's blocks wait for its
+// copies); unrolled loops of 128 keys run at the rate their code is fetched (a fifth slower); MMAs
+// issued by a whole warp under a predicate instead of one thread 293, 175, 1048.
 #include "attn_common.cuh"
 #include "tc_host.cuh"
 #include "tc_math.cuh"
