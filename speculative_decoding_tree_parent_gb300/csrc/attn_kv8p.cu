@@ -64,7 +64,8 @@ constexpr uint32_t kSlab = 128 * 128;        // 16 KB: half a tile of q, a stage
 constexpr uint32_t kStage = kKeys * 128;      // 8 KB: a stage of K or of V's codes
 constexpr uint32_t kVSlab = kKeys * 128;     // half a stage of V: 64 rows of 64 elements
 constexpr uint32_t kTreeSlab = kTreeKeys * 128;
-constexpr uint32_t kOffQ = 0;                // two tiles: hi and lo codes, then the tree's bf16 rows; or one: codes, rows
+// q: of two tiles the hi and lo codes, then the tree's bf16 rows; of one codes and rows
+constexpr uint32_t kOffQ = 0;
 constexpr uint32_t kOffK = kOffQ + 4 * kSlab;
 constexpr uint32_t kOffC = kOffK + kStK * kStage;
 constexpr uint32_t kOffV = kOffC + kStC * kStage;
@@ -211,7 +212,9 @@ __device__ __forceinline__ float split_row(const uint4* src, bool valid, uint8_t
 #pragma unroll
   for (int k = 0; k < 16; ++k) {
     const uint4 v = valid ? ld(src + k) : make_uint4(0, 0, 0, 0);
-    m = __vmaxu2(__vmaxu2(m, v.x & 0x7FFF7FFFu), __vmaxu2(v.y & 0x7FFF7FFFu, __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
+    const uint32_t a = __vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu);
+    const uint32_t b = __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu);
+    m = __vmaxu2(m, __vmaxu2(a, b));
   }
   const uint32_t top = max(m & 0xFFFFu, m >> 16);
   const int e = max((int)(top >> 7), 1);       // exponent field of the largest element
@@ -434,7 +437,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int t = warp == 1 ? 0 : 1, j0 = ntiles == 2 ? 0 : t;
     if (j0 < nb && elect_one()) {
       const uint32_t ts = tmem + 256 * t, to = ts + 128;
-      const uint32_t q8 = sb + kOffQ + (ntiles == 2 ? t : 0) * 2 * kSlab, q16 = sb + kOffQ + (ntiles == 2 ? t : 1) * 2 * kSlab;
+      const uint32_t q8 = sb + kOffQ + (ntiles == 2 ? t : 0) * 2 * kSlab;
+      const uint32_t q16 = sb + kOffQ + (ntiles == 2 ? t : 1) * 2 * kSlab;
       bool codes = false, rows = false;  // q has been waited for
       auto qk = [&](int j, int n) {
         const int sk = j % kStK;
@@ -495,7 +499,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int ct = threadIdx.x - (kMma1 + 1) * 32;
     const int r0 = (ct & 7) | ((ct >> 6) << 3), cc = (ct >> 3) & 7;
     const uint32_t src0 = swz(r0, cc);
-    const uint32_t dst0 = (cc >> 2) * kVSlab + swz(r0, (cc & 3) * 2), dst1 = (cc >> 2) * kVSlab + swz(r0, (cc & 3) * 2 + 1);
+    const uint32_t dst0 = (cc >> 2) * kVSlab + swz(r0, (cc & 3) * 2);
+    const uint32_t dst1 = (cc >> 2) * kVSlab + swz(r0, (cc & 3) * 2 + 1);
     const int tail = min(P, sp.pg_hi * 16) - (sp.pg_lo + (np - 1) * kPages) * 16;  // rows of the last prefix block
 #pragma unroll 1
     for (int j = 0; j < nb; ++j) {
@@ -605,7 +610,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] = valid ? ld(qrow + k + e) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) *reinterpret_cast<uint4*>(smem + kOffQ + (2 * slot + (k >> 3)) * kSlab + swz(row, (k + e) & 7)) = v[e];
+        for (int e = 0; e < 4; ++e)
+          *reinterpret_cast<uint4*>(smem + kOffQ + (2 * slot + (k >> 3)) * kSlab + swz(row, (k + e) & 7)) = v[e];
       }
       tc::fence_proxy_async_smem();
       warp_arrive(bar(&bars.q16[slot]));
@@ -687,7 +693,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (ok && j < nb) {
       pdl_wait();  // the mask may come from the kernel before
-      const uint32_t* mrow = reinterpret_cast<const uint32_t*>(p.mask + (size_t)(base + node) * p.mask_words) + sp.tb_lo;
+      const uint32_t* mrow =
+          reinterpret_cast<const uint32_t*>(p.mask + (size_t)(base + node) * p.mask_words) + sp.tb_lo;
       uint32_t bits = valid ? __ldcg(mrow + j - np) : 0u;
 #pragma unroll 1
       for (; ok && j < nb; j += step, ++n) {  // P as two bf16 terms
@@ -748,7 +755,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     pdl_wait();  // nothing is written before the kernel before has finished
     if (live) {
       const float top = fmaxf(m, other.x);
-      const float w0 = m == -INFINITY ? 0.f : ex2_approx(m - top), w1 = other.x == -INFINITY ? 0.f : ex2_approx(other.x - top);
+      const float w0 = m == -INFINITY ? 0.f : ex2_approx(m - top);
+      const float w1 = other.x == -INFINITY ? 0.f : ex2_approx(other.x - top);
       const float sum = l * w0 + other.y * w1;
       float inv = sum == 0.f ? 0.f : 1.f / sum;
       // a tree node that this row sees holds an infinity or NaN in V

@@ -210,7 +210,8 @@ __global__ void __launch_bounds__(kPageThreads) page_table_kernel(const PageArgs
   }
   if (p.slot_map != nullptr) {
     const int last = min(p.total_nodes, ld(p.qo + p.batch));  // rows behind the last sequence stay as they are
-    for (int t0 = first * kPageTok; t0 < last; t0 += step * kPageTok) {
+    for (long at0 = (long)first * kPageTok; at0 < last; at0 += (long)step * kPageTok) {
+      const int t0 = (int)at0;
       long long slots[kPageTok];
       int b = page_seq_of(p.qo, p.batch, t0);
       int lo = ld(p.qo + b), hi = ld(p.qo + b + 1);
@@ -221,7 +222,7 @@ __global__ void __launch_bounds__(kPageThreads) page_table_kernel(const PageArgs
       for (int k = 0; k < kPageTok; ++k) {
         const int t = t0 + k;
         slots[k] = -1;
-        if (t >= last) continue;
+        if (at0 + k >= last) continue;
         while (t >= hi && b + 1 < p.batch) {  // the next sequence that has nodes
           ++b;
           lo = hi;
@@ -243,14 +244,14 @@ __global__ void __launch_bounds__(kPageThreads) page_table_kernel(const PageArgs
         }
         if (page >= 0) slots[k] = (long long)page * p.page_size + (at - lp * (unsigned)p.page_size);
       }
-      if (t0 + kPageTok <= last && (reinterpret_cast<uintptr_t>(p.slot_map) & 15) == 0) {
+      if (at0 + kPageTok <= last && (reinterpret_cast<uintptr_t>(p.slot_map) & 15) == 0) {
         longlong2* dst = reinterpret_cast<longlong2*>(p.slot_map + t0);
 #pragma unroll
         for (int k = 0; k < kPageTok / 2; ++k) dst[k] = make_longlong2(slots[2 * k], slots[2 * k + 1]);
       } else {
 #pragma unroll
         for (int k = 0; k < kPageTok; ++k)
-          if (t0 + k < last) p.slot_map[t0 + k] = slots[k];
+          if (at0 + k < last) p.slot_map[at0 + k] = slots[k];
       }
     }
   }
@@ -280,7 +281,8 @@ int launch_page_table(const int32_t* seq_len, const int32_t* qo, const int32_t* 
   const int ctas = ceil_div(slots > batch ? slots : batch, kPageThreads);
   if (launch_pdl(page_table_kernel, dim3(ctas < 608 ? ctas : 608), dim3(kPageThreads), 0, stream, p) != cudaSuccess)
     return SPEC_ERR_CUDA;
-  if (ctas > 1 && launch_pdl(page_count_kernel, dim3(1), dim3(kPageThreads), 0, stream, p) != cudaSuccess) return SPEC_ERR_CUDA;
+  if (ctas > 1 && launch_pdl(page_count_kernel, dim3(1), dim3(kPageThreads), 0, stream, p) != cudaSuccess)
+    return SPEC_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
 

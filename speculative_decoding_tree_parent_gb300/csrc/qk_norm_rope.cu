@@ -170,7 +170,8 @@ __global__ void __launch_bounds__(kRopeMaxWarps * 32, 2) qk_norm_rope_kernel(con
   };
   // four cosines and sines for the chunk at `at`
   auto load_turns = [](const float* tab, int rot, int at, Eight& c, Eight& s, int to) {
-    const float4 x = *reinterpret_cast<const float4*>(tab + at / 2), y = *reinterpret_cast<const float4*>(tab + (rot + at) / 2);
+    const float4 x = *reinterpret_cast<const float4*>(tab + at / 2);
+    const float4 y = *reinterpret_cast<const float4*>(tab + (rot + at) / 2);
     c.x[to] = x.x, c.x[to + 1] = x.y, c.x[to + 2] = x.z, c.x[to + 3] = x.w;
     s.x[to] = y.x, s.x[to + 1] = y.y, s.x[to + 2] = y.z, s.x[to + 3] = y.w;
   };
@@ -237,8 +238,9 @@ __global__ void __launch_bounds__(kRopeMaxWarps * 32, 2) qk_norm_rope_kernel(con
         const Eight u = widen(wa), v = widen(wb);
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {
-          const float2 y = fmul2(fmul2(make_float2(a.x[i], a.x[i + 1]), make_float2(r, r)), make_float2(u.x[i], u.x[i + 1]));
-          const float2 z = fmul2(fmul2(make_float2(b.x[i], b.x[i + 1]), make_float2(r, r)), make_float2(v.x[i], v.x[i + 1]));
+          const float2 r2 = make_float2(r, r);
+          const float2 y = fmul2(fmul2(make_float2(a.x[i], a.x[i + 1]), r2), make_float2(u.x[i], u.x[i + 1]));
+          const float2 z = fmul2(fmul2(make_float2(b.x[i], b.x[i + 1]), r2), make_float2(v.x[i], v.x[i + 1]));
           a.x[i] = y.x, a.x[i + 1] = y.y, b.x[i] = z.x, b.x[i + 1] = z.y;
         }
       }
