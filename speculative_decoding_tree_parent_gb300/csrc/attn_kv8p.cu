@@ -32,16 +32,16 @@
 // 2-5 and 6-9 softmax, 11-14 V's converters. Every wait is bounded.
 // Splits write O / l in fp32 and the log2-sum-exp, joined by a second kernel.
 //
-// Bound (one GB300): not HBM and not the tensor cores but the blocks' chain (QK, softmax, PV, each
-// handed on through a barrier) and the issue of its instructions; a block of 64 keys takes about
-// 1200 cycles for one tile and for two. 128 sequences of one token over 543,000 keys (1.1 GB): 293 us,
-// 3.8 TB/s; 32 trees of 64 nodes over 512 .. 8192 keys: 164 us, 0.91 of 1.93 PFLOP/s; 8 x 128 nodes
-// over 32768 keys: 984 us, 1.0 PFLOP/s.
-// What was measured beside it: one tile a CTA with its softmax split over all eight warps, 128-key
-// blocks and q in TMEM, 293 -> 300, 164 -> 246, 984 -> 1010 us; two tiles in 128-key blocks with one
-// S each, 330, 199, 1260; one producer for K and V 404, 161, 973 (one tile's blocks wait for its
-// copies); unrolled loops of 128 keys run at the rate their code is fetched (a fifth slower); MMAs
-// issued by a whole warp under a predicate instead of one thread 293, 175, 1048.
+// Bound (one GB300): not HBM and not the tensor cores but a slot's chain (S, softmax, P, each handed
+// on through a barrier) and the issue of its instructions: about 2300 cycles for a block of 64 keys,
+// of which the softmax takes the most; two slots go at a time. 128 sequences of one token over
+// 543,000 keys (1.1 GB): 274 us, 4.1 TB/s; 32 trees of 64 nodes over 512 .. 8192 keys: 156 us,
+// 0.96 of 1.93 PFLOP/s; 8 x 128 nodes over 32768 keys: 923 us, 1.06 PFLOP/s.
+// What was measured beside it (when it took 293, 164 and 984 us): one tile a CTA, its blocks of 128
+// keys handed to the slots in turn, q in TMEM 300, 246, 1010; two tiles in 128-key blocks with one S
+// each 330, 199, 1260; one producer for K and V 404, 161, 973 (one tile's blocks wait for its copies);
+// MMAs issued by a whole warp under a predicate instead of one thread 293, 175, 1048. Loops unrolled
+// over 128 keys ran at the rate at which their code is fetched, a fifth slower.
 #include "attn_common.cuh"
 #include "tc_host.cuh"
 #include "tc_math.cuh"
@@ -163,25 +163,31 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 
 // The whole warp waits for a phase, bounded: the hardware holds a try for microseconds before it
 // says no, so kTries of them are a second or so. (One lane waiting, with its answer shuffled to the
-// others, cost about 1000 cycles a wait to bring the warp back together.)
+// others, cost about 1000 cycles a wait to bring the warp back together. The first try stands by
+// itself and the others out of line: a loop around it cost a tenth of the kernel's time.)
 constexpr int kTries = 1 << 18;
+__device__ __noinline__ bool wait_more(uint32_t bar, uint32_t parity, volatile int* abort) {
+#pragma unroll 1
+  for (int i = 0; i < kTries && *abort == 0; ++i) {
+    const bool ok = tc::mbar_try_wait(bar, parity);
+    if (__all_sync(0xffffffffu, ok)) return true;
+  }
+  *abort = 1;
+  return false;
+}
 __device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, volatile int* abort) {
-  bool ok;
-  int i = 0;
-  do ok = tc::mbar_try_wait(bar, parity);
-  while (!ok && ++i < kTries && *abort == 0);
-  if (!ok) *abort = 1;
-  return __all_sync(0xffffffffu, ok);
+  const bool ok = tc::mbar_try_wait(bar, parity);
+  return __builtin_expect(__all_sync(0xffffffffu, ok), 1) || wait_more(bar, parity, abort);
 }
 
-// The same for one thread.
+// The same for one thread. (Here the further tries in line are the faster form.)
 __device__ __forceinline__ bool wait_one(uint32_t bar, uint32_t parity, volatile int* abort) {
-  bool ok;
-  int i = 0;
-  do ok = tc::mbar_try_wait(bar, parity);
-  while (!ok && ++i < kTries && *abort == 0);
-  if (!ok) *abort = 1;
-  return ok;
+  if (tc::mbar_try_wait(bar, parity)) return true;
+#pragma unroll 1
+  for (int i = 0; i < kTries && *abort == 0; ++i)
+    if (tc::mbar_try_wait(bar, parity)) return true;
+  *abort = 1;
+  return false;
 }
 
 // One lane of a converged warp.
