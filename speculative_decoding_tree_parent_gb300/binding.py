@@ -107,9 +107,16 @@ def _ptr(t) -> int | None:
     return t.data_ptr()
 
 
+# the current stream's handle without a Stream object around it (2.5 us of a call), where torch has it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> int | None:
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
+    return torch.cuda.current_stream().cuda_stream
 
 
 def _check(st: int, what: str) -> int:
@@ -418,9 +425,10 @@ def _rows(t, what):
     if not t.is_cuda:
         raise ValueError("device tensor expected")
     T, h, d = t.shape
-    if (d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d):
+    rows, heads, one = t.stride()
+    if (d > 1 and one != 1) or (h > 1 and heads != d):
         raise ValueError(f"{what}: contiguous heads expected")
-    return t.data_ptr(), t.stride(0) if T > 1 else h * d
+    return t.data_ptr(), rows if T > 1 else h * d
 
 
 def spec_qk_norm_rope(q, k, v, cos_sin, prefix_len, qo_indptr, q_out, k_out, v_out, depth=None, q_weight=None,
