@@ -880,7 +880,9 @@ static int tiles_of(int max_nodes, int npt) { return ceil_div(max_nodes, npt); }
 
 // Row tiles that a CTA has: two where the sequence has them (they share K, V and V's conversion),
 // unless one a CTA is what it takes to put a CTA on every SM without cutting the keys into more
-// splits, each of which writes its partial result.
+// splits, each of which writes its partial result. (One tree of 64 nodes over 4096 keys, 16 tiles:
+// 24 us with one a CTA and 9 splits, 31 with two and 19 or 10. 32 of them, 512 tiles: 243 and 156 us;
+// 8 x 128 nodes over 32768 keys, 512 tiles: 976 and 923.)
 static int tiles_per_cta(int batch, int max_nodes, int hq, int hkv) {
   const int tiles = tiles_of(max_nodes, kRows / (hq / hkv));
   return tiles > 1 && (long)batch * hkv * ceil_div(tiles, 2) >= sm_count() ? 2 : 1;
