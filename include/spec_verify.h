@@ -578,7 +578,8 @@ int spec_tree_verify_attn_kv8p(const void* q, const uint8_t* k_pool, const uint8
  *
  *   kv_scale    float [num_pages][hkv][2] (in/out)
  *   The other arguments, the checks and the device errors are those of spec_kv_commit with
- *   dtype = SPEC_BF16. d a multiple of 16 and page_size * d <= 8192, else
+ *   dtype = SPEC_BF16 (a path may have any length; a sequence whose node range does not lie
+ *   in [0, total_nodes) is SPEC_ERR_INDEX). d a multiple of 16 and page_size * d <= 8192, else
  *   SPEC_ERR_UNSUPPORTED.
  */
 int spec_kv_commit_kv8p(const void* k_tree, const void* v_tree, const int32_t* path, int path_cap,

@@ -45,8 +45,8 @@ bool commit_kv8p_shape(int page_size, int d);
 int launch_kv_commit_kv8p(const void* k_tree, const void* v_tree, const int32_t* path, int path_cap,
                           const int32_t* accept_len, const int32_t* qo, const int32_t* page_table, int max_pages,
                           int num_pages, int page_size, const int32_t* prefix_len, int32_t* seq_len_out,
-                          uint8_t* k_pool, uint8_t* v_pool, float* kv_scale, int batch, int hkv, int d,
-                          int32_t* status, cudaStream_t stream);
+                          uint8_t* k_pool, uint8_t* v_pool, float* kv_scale, int batch, int total_nodes, int hkv,
+                          int d, int32_t* status, cudaStream_t stream);
 int launch_qk_norm_rope(int dtype, const void* q_in, long q_stride, const void* k_in, long k_stride, const void* v_in,
                         long v_stride, const void* q_weight, const void* k_weight, float eps, const float* cos_sin,
                         int max_pos, int rot, bool interleaved, const int32_t* prefix_len, const int32_t* depth,
@@ -498,8 +498,8 @@ int spec_kv_commit_kv8p(const void* k_tree, const void* v_tree, const int32_t* p
   if (!commit_kv8p_shape(page_size, d) || !grid_fits(hkv)) return SPEC_ERR_UNSUPPORTED;
   if (!kv_scale) return SPEC_ERR_ARG;
   return launch_kv_commit_kv8p(k_tree, v_tree, path, path_cap, accept_len, qo_indptr, page_table, max_pages,
-                               num_pages, page_size, prefix_len, seq_len_out, k_pool, v_pool, kv_scale, batch, hkv, d,
-                               dev_status, static_cast<cudaStream_t>(stream));
+                               num_pages, page_size, prefix_len, seq_len_out, k_pool, v_pool, kv_scale, batch,
+                               total_nodes, hkv, d, dev_status, static_cast<cudaStream_t>(stream));
 }
 
 int spec_qk_norm_rope(int dtype, const void* q_in, long long q_stride, const void* k_in, long long k_stride,

@@ -32,7 +32,7 @@ struct CommitP8Args {
   int32_t* seq_len_out;
   uint8_t* pool[2];   // K, V codes [num_pages][hkv][page_size][d]
   float* kv_scale;    // [num_pages][hkv][2]
-  int hkv, d;
+  int batch, total, hkv, d;  // total: tree rows
   int32_t* status;
 };
 
@@ -91,7 +91,8 @@ __device__ __forceinline__ float scale_for(uint32_t bits) {
 // kPer: 16-element pieces of a page and head that a thread holds
 template <int kPer>
 __global__ void __launch_bounds__(2 * kQcHalf) kv_commit_kv8p_kernel(const CommitP8Args p) {
-  const int b = blockIdx.x;
+  // (batch and pages share the grid's x extent: y would end at 65535 pages)
+  const int b = blockIdx.x % (unsigned)p.batch, nth = blockIdx.x / (unsigned)p.batch;
   const int half = threadIdx.x / kQcHalf, tid = threadIdx.x % kQcHalf;  // 0: K, 1: V
   __shared__ uint32_t s_top[2][2][kQcHalf / 32];  // [head of a pair][half][warp]
   pdl_wait();
@@ -100,13 +101,13 @@ __global__ void __launch_bounds__(2 * kQcHalf) kv_commit_kv8p_kernel(const Commi
   const int ps = p.page_size;
   const int32_t* path = p.path + (size_t)b * p.path_cap;
   const int32_t* table = p.page_table + (size_t)b * p.max_pages;
-  const bool lead = blockIdx.y == 0 && blockIdx.z == 0;
-  if (L < 0 || L >= p.path_cap || L >= n || P < 0 || P > 0x7FFFFFFF - p.path_cap) {
+  const bool lead = nth == 0 && blockIdx.y == 0;
+  if (L < 0 || L >= p.path_cap || L >= n || base < 0 || n > p.total - base || P < 0 || P > 0x7FFFFFFF - p.path_cap) {
     if (lead && threadIdx.x == 0) report(p.status, SPEC_ERR_INDEX);
     return;
   }
-  const int lp = P / ps + (int)blockIdx.y;
-  if ((long long)lp * ps > (long long)P + L) return;  // the path ends before this page
+  if ((long)(P / ps + (long)nth) * ps > (long)P + L) return;  // the path ends before this page
+  const int lp = P / ps + nth;
   // the page's rows [r0, r1) take the path's nodes from r0 - shift on; rows below r0 are older
   const int shift = P - lp * ps;  // > 0 on the first page where it starts inside
   const int r0 = max(shift, 0), r1 = min(ps, shift + L + 1);
@@ -134,7 +135,7 @@ __global__ void __launch_bounds__(2 * kQcHalf) kv_commit_kv8p_kernel(const Commi
   };
   // the first head's rows are on their way while the sequence is checked
   uint4 x[kPer][2];
-  load(blockIdx.z, x);
+  load(blockIdx.y, x);
   int bad = 0;
   for (int i = threadIdx.x; i <= L; i += 2 * kQcHalf) {
     const int node = ld(path + i);
@@ -151,7 +152,7 @@ __global__ void __launch_bounds__(2 * kQcHalf) kv_commit_kv8p_kernel(const Commi
   if (__syncthreads_or(bad)) return;
   const size_t page = (size_t)ld(table + lp);
   int turn = 0;
-  for (int g = blockIdx.z; g < p.hkv; g += gridDim.z, turn ^= 1) {
+  for (int g = blockIdx.y; g < p.hkv; g += gridDim.y, turn ^= 1) {
     const size_t unit = page * p.hkv + g;
     float* sp = p.kv_scale + unit * 2 + half;
     const float old = r0 > 0 ? *sp : 0.f;  // (read by every thread before the barrier, written after it)
@@ -162,7 +163,7 @@ __global__ void __launch_bounds__(2 * kQcHalf) kv_commit_kv8p_kernel(const Commi
     if ((tid & 31) == 0) s_top[turn][half][tid >> 5] = top;
     // the next head's rows, while this one's are joined, turned into codes and stored
     uint4 y[kPer][2];
-    if (g + gridDim.z < p.hkv) load(g + gridDim.z, y);
+    if (g + gridDim.y < p.hkv) load(g + gridDim.y, y);
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < kQcHalf / 32; ++w) top = max(top, s_top[turn][half][w]);
@@ -212,20 +213,21 @@ bool commit_kv8p_shape(int page_size, int d) {
 int launch_kv_commit_kv8p(const void* k_tree, const void* v_tree, const int32_t* path, int path_cap,
                           const int32_t* accept_len, const int32_t* qo, const int32_t* page_table, int max_pages,
                           int num_pages, int page_size, const int32_t* prefix_len, int32_t* seq_len_out,
-                          uint8_t* k_pool, uint8_t* v_pool, float* kv_scale, int batch, int hkv, int d,
-                          int32_t* status, cudaStream_t stream) {
+                          uint8_t* k_pool, uint8_t* v_pool, float* kv_scale, int batch, int total_nodes, int hkv,
+                          int d, int32_t* status, cudaStream_t stream) {
   const CommitP8Args p{{static_cast<const __nv_bfloat16*>(k_tree), static_cast<const __nv_bfloat16*>(v_tree)},
                        path, path_cap, accept_len, qo, page_table, max_pages, num_pages, page_size, prefix_len,
-                       seq_len_out, {k_pool, v_pool}, kv_scale, hkv, d, status};
-  // most pages a path of path_cap nodes touches; a tree holds at most kMaxTreeNodes nodes
-  const int most = path_cap < kMaxTreeNodes ? path_cap : kMaxTreeNodes;
+                       seq_len_out, {k_pool, v_pool}, kv_scale, batch, total_nodes, hkv, d, status};
+  // most rows a path has (its nodes are the sequence's rows), and most pages that they touch
+  const long most = path_cap < total_nodes ? path_cap : total_nodes > 1 ? total_nodes : 1;
+  const long pages = (most + page_size - 2) / page_size + 1;
+  if (batch * pages > 0x7FFFFFFFL) return SPEC_ERR_UNSUPPORTED;
   // a CTA per head while they stand on the GPU at once (its longest chain is then the shortest),
   // else as many heads a CTA as make it so: the checks and the chain before the rows are then made
   // once for several heads, and a head's rows are loaded under the one before it (32 sequences of
   // about 500 rows, 8 heads: a CTA per head 39 us; at most 8, 16, 32 CTAs an SM: 26.8, 24.8, 28.8)
-  const int pages = ceil_div(most - 1, page_size) + 1;
-  const long share = 16L * sm_count() / ((long)batch * pages);
-  const dim3 grid(batch, pages, (unsigned)(share < 1 ? 1 : share < hkv ? share : hkv)), block(2 * kQcHalf);
+  const long share = 16L * sm_count() / (batch * pages);
+  const dim3 grid((unsigned)(batch * pages), (unsigned)(share < 1 ? 1 : share < hkv ? share : hkv)), block(2 * kQcHalf);
   const int per = ceil_div(page_size * (d / 16), kQcHalf);
   const cudaError_t e = per <= 1   ? launch_pdl(kv_commit_kv8p_kernel<1>, grid, block, 0, stream, p)
                         : per <= 2 ? launch_pdl(kv_commit_kv8p_kernel<2>, grid, block, 0, stream, p)
