@@ -95,7 +95,7 @@ struct Params {
   int max_len;  // longest prefix that the row of pages and the caller's bound allow
   const int32_t* prefix_len;
   const uint64_t* mask;
-  int mask_words;
+  int mask_words, max_nodes;
   const int32_t* qo;
   int hq, hkv, G, npt;  // npt: nodes of a row tile
   int splits, mtiles, batch, lpt;
@@ -306,7 +306,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // (warp: uniform)
   const int node0 = p.per_cta * blockIdx.y * p.npt;
   if (node0 >= N) return;
-  if (N > p.mask_words * 64 || P < 0 || P > p.max_len) {
+  // (the grid and the workspace hold max_nodes nodes a sequence, not the mask row's multiple of 64)
+  if (N > p.max_nodes || P < 0 || P > p.max_len) {
     if (threadIdx.x == 0 && split == 0) {
       pdl_wait();
       report(p.status, SPEC_ERR_CAPACITY);
@@ -826,7 +827,7 @@ struct MergeParams {
   const float* part_lse;
   const int32_t* qo;
   const int32_t* prefix_len;
-  int max_len, mask_words;
+  int max_len, max_nodes;
   int splits, mtiles, hkv, hq, G, npt;
   long tiles;
   __nv_bfloat16* out;
@@ -846,7 +847,7 @@ __global__ void __launch_bounds__(kMergeThreads) attn_kv8p_merge_kernel(const Me
   if (r >= p.npt * p.G) return;
   pdl_wait();  // the attention grid has finished: its partials are visible
   const int base = ld(p.qo + b), N = ld(p.qo + b + 1) - base, P = ld(p.prefix_len + b);
-  if (node >= N || N > p.mask_words * 64 || P < 0 || P > p.max_len) return;  // as the attention
+  if (node >= N || N > p.max_nodes || P < 0 || P > p.max_len) return;  // as the attention
   const float* ls = p.part_lse + (size_t)tile * p.splits * kRows + r;
   const float4* po = p.part_o + (size_t)tile * p.splits * (kRows * kD / 4) + c * kRows + r;
   float lv[MAXS];
@@ -976,6 +977,7 @@ int launch_attn_kv8p(const void* q, const uint8_t* k_pool, const uint8_t* v_pool
   prm.prefix_len = prefix_len;
   prm.mask = mask;
   prm.mask_words = (max_nodes + 63) >> 6;
+  prm.max_nodes = max_nodes;
   prm.qo = qo;
   prm.hq = hq;
   prm.hkv = hkv;
@@ -1001,7 +1003,7 @@ int launch_attn_kv8p(const void* q, const uint8_t* k_pool, const uint8_t* v_pool
   if (launch_pdl(attn_kv8p_kernel, grid, dim3(kThreads), kSmem, stream, tm_kp, tm_vp, tm_kt, tm_vt, prm) != cudaSuccess)
     return SPEC_ERR_CUDA;
   if (prm.splits > 1) {
-    MergeParams mp{prm.part_o, prm.part_lse, qo, prefix_len, prm.max_len, prm.mask_words, prm.splits, prm.mtiles, hkv,
+    MergeParams mp{prm.part_o, prm.part_lse, qo, prefix_len, prm.max_len, max_nodes, prm.splits, prm.mtiles, hkv,
                    hq, G, prm.npt, tiles, prm.out, lse};
     const long threads = tiles * 32 * kRows;
     const dim3 mg((unsigned)((threads + kMergeThreads - 1) / kMergeThreads)), mb(kMergeThreads);
