@@ -220,7 +220,8 @@ int spec_build_tree_mask(const int32_t* parent, const int32_t* qo_indptr, int ba
  *   ws         workspace of spec_workspace_size(SPEC_OP_ATTN, ...) bytes (key-split
  *              partial results; any contents).
  *   Device errors: SPEC_ERR_PAGE (page id outside [0, num_pages): the page is read
- *   as zeros), SPEC_ERR_TIMEOUT.
+ *   as zeros), SPEC_ERR_CAPACITY (a tree that passes what a launch for max_nodes holds),
+ *   SPEC_ERR_TIMEOUT.
  */
 int spec_tree_verify_attn(int dtype, const void* q, const void* k_pool, const void* v_pool,
                           int num_pages, int page_size, const int32_t* page_table, int max_pages,

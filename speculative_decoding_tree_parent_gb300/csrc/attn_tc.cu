@@ -252,7 +252,8 @@ __global__ void __launch_bounds__(TcCfg<kFp8, kPar>::kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // the two exits below are taken by every split CTA of a tile alike (they depend on b, g, pair)
   if (node0 >= N) return;  // this pair of M-tiles is past the sequence's tree
-  if (N > p.mask_words * 64 || P < 0 || P > p.max_pages * 16) {
+  // (a tree has to fit its mask rows, and the row tiles that the grid and the workspace hold)
+  if (N > p.mask_words * 64 || N > p.mtiles * npt || P < 0 || P > p.max_pages * 16) {
     if (threadIdx.x == 0 && split == 0) {
       pdl_wait();  // (the status word is written in stream order)
       report(p.status, SPEC_ERR_CAPACITY);
@@ -783,7 +784,8 @@ __global__ void __launch_bounds__(kMergeThreads) attn_tc_merge_kernel(const TcMe
   const int G = p.G;
   const int node_l = tt * (kTcRows / G) + r / G;
   const int base = __ldg(p.qo + b);  // qo is an input: safe to read before the wait
-  if (node_l >= __ldg(p.qo + b + 1) - base) return;
+  const int N = __ldg(p.qo + b + 1) - base;
+  if (node_l >= N || N > p.mtiles * (kTcRows / G)) return;  // (a tree past the row tiles was refused)
   pdl_wait();  // the attention grid has finished: its partials are visible
   // every load (split statistics and partial rows) is issued before any is used: one
   // round trip to L2
