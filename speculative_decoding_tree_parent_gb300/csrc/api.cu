@@ -76,6 +76,11 @@ static bool attn_wants_tc(int dtype, int d) { return dtype == SPEC_BF16 && d == 
 // Grids put (sequence, KV head) pairs, or sequences, on a launch's y or z dimension.
 static bool grid_fits(long n) { return n <= kMaxGridYZ; }
 
+// Heads and batch that the attention over page scales serves (a row tile holds a group's rows).
+static bool attn_kv8p_shape(long batch, int hq, int hkv, int d) {
+  return d == 128 && hq / hkv <= 128 && grid_fits(batch * hkv);
+}
+
 static std::atomic<int> g_early_reads{0};
 bool early_reads() { return g_early_reads.load(std::memory_order_relaxed) != 0; }
 
@@ -113,8 +118,8 @@ size_t spec_workspace_size(int op, int batch, int total_nodes, int max_nodes, in
       if (hq <= 0 || hkv <= 0 || hq % hkv || d <= 0 || max_nodes <= 0 || max_prefix < 0) return 0;
       return attn_ws_bytes(batch, total_nodes, max_nodes, hq, hkv, d, max_prefix);
     case SPEC_OP_ATTN_KV8P:
-      if (hq <= 0 || hkv <= 0 || hq % hkv || d != 128 || max_nodes <= 0 || max_nodes > kMaxNodes || max_prefix < 0)
-        return 0;
+      if (hq <= 0 || hkv <= 0 || hq % hkv || max_nodes <= 0 || max_nodes > kMaxNodes || max_prefix < 0) return 0;
+      if (!attn_kv8p_shape(batch, hq, hkv, d)) return 0;
       return attn_kv8p_ws_bytes(batch, max_nodes, hq, hkv, max_prefix);
     case SPEC_OP_ACCEPT:
       if (vocab <= 0) return 0;
@@ -467,8 +472,7 @@ int spec_tree_verify_attn_kv8p(const void* q, const uint8_t* k_pool, const uint8
       num_pages < 0 || max_pages < 0)
     return SPEC_ERR_ARG;
   if (hq <= 0 || hkv <= 0 || hq % hkv != 0) return SPEC_ERR_ARG;
-  if (d != 128 || page_size != 16 || hq / hkv > 128) return SPEC_ERR_UNSUPPORTED;
-  if (!grid_fits((long)batch * hkv)) return SPEC_ERR_UNSUPPORTED;
+  if (page_size != 16 || !attn_kv8p_shape(batch, hq, hkv, d)) return SPEC_ERR_UNSUPPORTED;
   if (batch == 0 || total_nodes == 0) return SPEC_OK;
   if (!q || !k_tree || !v_tree || !mask || !qo_indptr || !prefix_len || !out) return SPEC_ERR_ARG;
   if (max_prefix > 0 && (!k_pool || !v_pool || !kv_scale || !page_table || max_pages <= 0 || num_pages <= 0))
