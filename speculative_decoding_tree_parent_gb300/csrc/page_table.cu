@@ -19,6 +19,7 @@
 // which starts after the first has ended.
 // Bound: latency for a step; the 8-byte slots' stores for a batch of prompts.
 #include "common.cuh"
+#include "page_stack.cuh"
 
 namespace specv {
 
@@ -190,8 +191,8 @@ __global__ void __launch_bounds__(kPageThreads) page_table_kernel(const PageArgs
   const int n0 = ld(p.n_free);
   page_plan(p, s, blockIdx.x == 0);
   const int asked = s.grow[p.batch - 1], back = s.back[p.batch - 1];
-  const int n1 = n0 + back;
-  const bool sane = n0 >= 0 && n1 <= p.num_pages;  // else the stack is not what it should be: nothing moves
+  const bool sane = page_stack_holds(n0, back, p.num_pages);  // else the stack is not what it should be: nothing moves
+  const int n1 = sane ? n0 + back : 0;
   if (blockIdx.x == 0 && threadIdx.x == 0) {
     if (!sane) report(p.status, SPEC_ERR_CAPACITY);
     else if (asked > n1) report(p.status, SPEC_ERR_CAPACITY);
@@ -266,9 +267,8 @@ __global__ void __launch_bounds__(kPageThreads) page_count_kernel(const PageArgs
   pdl_wait();  // the kernel before has read the counters that this one may overwrite
   const int n0 = ld(p.n_free);
   page_plan(p, s, false);
-  const int n1 = n0 + s.back[p.batch - 1];
-  const bool sane = n0 >= 0 && n1 <= p.num_pages;
-  page_count(p, s, n0, sane, sane ? page_grants(s, p.batch, n1) : 0);
+  const bool sane = page_stack_holds(n0, s.back[p.batch - 1], p.num_pages);
+  page_count(p, s, n0, sane, sane ? page_grants(s, p.batch, n0 + s.back[p.batch - 1]) : 0);
 }
 
 int launch_page_table(const int32_t* seq_len, const int32_t* qo, const int32_t* held, int32_t* page_table,
