@@ -186,7 +186,9 @@ __device__ __forceinline__ void page_count(const PageArgs& p, const PagePlan& s,
 
 __global__ void __launch_bounds__(kPageThreads) page_table_kernel(const PageArgs p) {
   __shared__ PagePlan s;
-  pdl_trigger();
+  // Signals early to its own second kernel alone (which waits, and does not signal): the table is
+  // an input that a later kernel may read before its wait, where the caller lets it.
+  if (gridDim.x > 1) pdl_trigger();
   pdl_wait();
   const int n0 = ld(p.n_free);
   page_plan(p, s, blockIdx.x == 0);

@@ -1,0 +1,67 @@
+"""Rules of the kernels launched with programmatic stream serialization, read from the sources (no GPU
+is used). Such a kernel may start while the one before it runs, so
+
+- only the kernels that the header names may signal early: a later kernel may read the pool, the page
+  tables and the tree's inputs before its wait where the caller allows it, and whatever writes those
+  must have ended by then."""
+
+import os
+import re
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+CSRC = os.path.join(ROOT, "speculative_decoding_tree_parent_gb300", "csrc")
+
+
+def source(name):
+    with open(os.path.join(CSRC, name)) as fh:
+        return re.sub(r"//[^\n]*", "", fh.read())
+
+
+def kernels():
+    """{kernel name: (parameter list, body)} of every __global__ function."""
+    out = {}
+    for f in sorted(os.listdir(CSRC)):
+        if not f.endswith(".cu"):
+            continue
+        src = source(f)
+        for m in re.finditer(r"__global__\s+void\b", src):
+            at = src.index("{", m.end())
+            head = src[m.end():at]
+            name = re.findall(r"(\w+)\s*\(", re.sub(r"__\w+__\s*\([^()]*(\([^()]*\))?[^()]*\)", "", head))[0]
+            depth, i = 1, at + 1
+            while depth:
+                depth += {"{": 1, "}": -1}.get(src[i], 0)
+                i += 1
+            out[name] = (head, src[at:i])
+    return out
+
+
+KERNELS = kernels()
+
+
+def test_the_sources_are_understood():
+    assert {"attn_tc_kernel", "attn_tc_merge_kernel", "attn_kv8p_kernel", "kv_commit_kernel", "kv_commit_kv8p_kernel",
+            "page_table_kernel", "page_count_kernel", "qk_norm_rope_kernel", "accept_greedy_kernel",
+            "accept_greedy_lazy_kernel", "accept_walk_kernel", "tree_mask_kernel"} <= set(KERNELS)
+
+
+# who signals early, and the condition it does so under (None: always)
+EARLY = {"tree_mask_kernel": None, "attn_tc_kernel": None, "attn_tc_merge_kernel": None, "attn_kv8p_kernel": None,
+         "attn_kv8p_merge_kernel": None, "accept_greedy_kernel": "ca.k_tree == nullptr",
+         "page_table_kernel": "gridDim.x > 1"}
+
+
+def test_who_signals_early():
+    for name, (_, body) in KERNELS.items():
+        calls = re.findall(r"(if \([^;{}]*\)\s*)?\bpdl_trigger\(\);", body)
+        if name not in EARLY:
+            assert not calls, name
+        else:
+            cond = EARLY[name]
+            assert len(calls) == 1, name
+            assert calls[0].strip() == ("" if cond is None else f"if ({cond})"), (name, calls)
+    # the page table's second kernel waits before it does anything, and ends the early start there
+    body = KERNELS["page_count_kernel"][1]
+    assert body.index("pdl_wait()") < body.index("ld(")
