@@ -13,7 +13,7 @@ int launch_kv_commit(int elem_bytes, const void* k_tree, const void* v_tree, con
                      const int32_t* accept_len, const int32_t* qo, const int32_t* page_table, int max_pages,
                      int num_pages, int page_size, const int32_t* prefix_len, int32_t* seq_len_out, void* k_pool,
                      void* v_pool, int batch, int hkv, int d, int32_t* status, cudaStream_t stream, TokenInsert ins,
-                     const float* kv_scale);
+                     const float* kv_scale, bool behind_accept);
 int launch_accept(int mode, const int32_t* parent, const int32_t* tokens, const float* tl, const float* dl,
                   const float* uniforms, float temperature, int vocab, const int32_t* qo, int batch,
                   int total_nodes, int path_cap, int32_t* accept_len, int32_t* path, int32_t* out_tokens,
@@ -383,7 +383,8 @@ int spec_kv_commit(int dtype, const void* k_tree, const void* v_tree, const int3
   const int elem = dtype == SPEC_F32 ? 4 : 2;
   return launch_kv_commit(elem, k_tree, v_tree, path, path_cap, accept_len, qo_indptr, page_table, max_pages,
                           num_pages, page_size, prefix_len, seq_len_out, k_pool, v_pool, batch, hkv, d, dev_status,
-                          static_cast<cudaStream_t>(stream), TokenInsert{nullptr, nullptr, 0}, nullptr);
+                          static_cast<cudaStream_t>(stream), TokenInsert{nullptr, nullptr, 0}, nullptr,
+                          false);
 }
 
 int spec_tree_verify_attn_kv8(const void* q, const uint8_t* k_pool, const uint8_t* v_pool, const float* kv_scale,
@@ -458,7 +459,8 @@ int spec_kv_commit_kv8(const void* k_tree, const void* v_tree, const float* kv_s
   if (!kv_scale) return SPEC_ERR_ARG;
   return launch_kv_commit(2, k_tree, v_tree, path, path_cap, accept_len, qo_indptr, page_table, max_pages, num_pages,
                           page_size, prefix_len, seq_len_out, k_pool, v_pool, batch, hkv, d, dev_status,
-                          static_cast<cudaStream_t>(stream), TokenInsert{nullptr, nullptr, 0}, kv_scale);
+                          static_cast<cudaStream_t>(stream), TokenInsert{nullptr, nullptr, 0}, kv_scale,
+                          false);
 }
 
 

@@ -305,7 +305,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int base = ld(p.qo + b), N = ld(p.qo + b + 1) - base, P = ld(p.prefix_len + b);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // (warp: uniform)
   const int node0 = p.per_cta * blockIdx.y * p.npt;
-  if (node0 >= N) return;
+  if (node0 >= N) {
+    if ((blockIdx.x | blockIdx.y | blockIdx.z) == 0) pdl_wait();  // (the grid must not end before its predecessor)
+    return;
+  }
   // (the grid and the workspace hold max_nodes nodes a sequence, not the mask row's multiple of 64)
   if (N > p.max_nodes || P < 0 || P > p.max_len) {
     if (threadIdx.x == 0 && split == 0) {

@@ -251,7 +251,10 @@ __global__ void __launch_bounds__(TcCfg<kFp8, kPar>::kThreads, 1)
   const int ntiles = has1 ? 2 : 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // the two exits below are taken by every split CTA of a tile alike (they depend on b, g, pair)
-  if (node0 >= N) return;  // this pair of M-tiles is past the sequence's tree
+  if (node0 >= N) {  // this pair of M-tiles is past the sequence's tree
+    if ((split | pair | bg) == 0) pdl_wait();  // (the grid must not end before its predecessor)
+    return;
+  }
   // (a tree has to fit its mask rows, and the row tiles that the grid and the workspace hold)
   if (N > p.mask_words * 64 || N > p.mtiles * npt || P < 0 || P > p.max_pages * 16) {
     if (threadIdx.x == 0 && split == 0) {
@@ -760,7 +763,7 @@ struct TcMergeParams {
   const uint4* part_o;
   const float* part_lse;
   const int32_t* qo;
-  int splits, mtiles, hkv, hq, G;
+  int splits, mtiles, hkv, hq, G, early_reads;
   long groups;
   __nv_bfloat16* out;
   float* lse;
@@ -783,10 +786,14 @@ __global__ void __launch_bounds__(kMergeThreads) attn_tc_merge_kernel(const TcMe
   const int b = bg / p.hkv, g = bg - (bg / p.hkv) * p.hkv;
   const int G = p.G;
   const int node_l = tt * (kTcRows / G) + r / G;
-  const int base = __ldg(p.qo + b);  // qo is an input: safe to read before the wait
+  // the attention grid has finished: its partials are visible. (It signals before its own wait, so
+  // qo_indptr is read ahead only where the caller lets the attention do so.)
+  if (!p.early_reads) pdl_wait();
+  const int base = __ldg(p.qo + b);
   const int N = __ldg(p.qo + b + 1) - base;
+  if (idx == 0) pdl_wait();  // (whatever the sizes: the grid must not end before the attention)
   if (node_l >= N || N > p.mtiles * (kTcRows / G)) return;  // (a tree past the row tiles was refused)
-  pdl_wait();  // the attention grid has finished: its partials are visible
+  pdl_wait();
   // every load (split statistics and partial rows) is issued before any is used: one
   // round trip to L2
   const int S = p.splits;  // <= MAXS
@@ -1021,6 +1028,7 @@ int launch_attn_tc(const void* q, const void* k_pool, const void* v_pool, int nu
     mp.hkv = hkv;
     mp.hq = hq;
     mp.G = G;
+    mp.early_reads = prm.early_reads;
     mp.groups = groups;
     mp.out = prm.out;
     mp.lse = lse;

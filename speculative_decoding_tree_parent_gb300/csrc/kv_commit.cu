@@ -41,17 +41,21 @@ __global__ void __launch_bounds__(256) kv_commit_kernel(
     const int32_t* __restrict__ qo, const int32_t* __restrict__ page_table, int max_pages,
     int num_pages, int page_size, const int32_t* __restrict__ prefix_len,
     int32_t* __restrict__ seq_len_out, uint8_t* __restrict__ k_pool, uint8_t* __restrict__ v_pool,
-    int hkv, int row_bytes, int32_t* status, const TokenInsert ins, const float* __restrict__ kv_scale) {
+    int hkv, int row_bytes, int32_t* status, const TokenInsert ins, const float* __restrict__ kv_scale,
+    bool behind_accept) {
   const int b = blockIdx.x;
   __shared__ int s_ok;
   __shared__ int s_L;
-  // Everything the acceptance kernel does not write is read (or pulled into L2) before
-  // waiting for it: the sequence's bounds, its page-table entries past the prefix and
-  // its tree K/V rows (a few KB), so only accept_len / path remain on the critical path.
+  // Launched right behind the acceptance (spec_accept_commit), whose every CTA waited for the
+  // kernels before it: what the acceptance does not write is read (or pulled into L2) before
+  // waiting for it -- the sequence's bounds, its page-table entries past the prefix and its tree
+  // K/V rows (a few KB) -- so only accept_len / path remain on the critical path. As a call of its
+  // own the commit does not know what ran before it: it waits first.
+  if (!behind_accept) pdl_wait();
   const int base = __ldg(qo + b);
   const int n = __ldg(qo + b + 1) - base;
   const int P = __ldg(prefix_len + b);
-  {
+  if (behind_accept) {
     const int span = n < path_cap ? n : path_cap;
     const int lp0 = P / page_size, lp1 = (P + span - 1) / page_size;
     for (int lp = lp0 + (int)threadIdx.x; lp <= lp1 && lp < max_pages; lp += blockDim.x)
@@ -141,7 +145,7 @@ int launch_kv_commit(int elem_bytes, const void* k_tree, const void* v_tree, con
                      const int32_t* page_table, int max_pages, int num_pages, int page_size,
                      const int32_t* prefix_len, int32_t* seq_len_out, void* k_pool, void* v_pool,
                      int batch, int hkv, int d, int32_t* status, cudaStream_t stream, TokenInsert ins,
-                     const float* kv_scale) {
+                     const float* kv_scale, bool behind_accept) {
   // the pool's row: d codes for an FP8 cache (bf16 tree rows), else d elements
   const int row_bytes = kv_scale != nullptr ? d : d * elem_bytes;
   const uint8_t* kt = static_cast<const uint8_t*>(k_tree);
@@ -152,15 +156,15 @@ int launch_kv_commit(int elem_bytes, const void* k_tree, const void* v_tree, con
       kv_scale != nullptr
           ? launch_pdl(kv_commit_kernel<true>, dim3(batch), dim3(256), 0, stream, kt, vt, path, path_cap, accept_len,
                        qo, page_table, max_pages, num_pages, page_size, prefix_len, seq_len_out, kp, vp, hkv,
-                       row_bytes, status, ins, kv_scale)
+                       row_bytes, status, ins, kv_scale, behind_accept)
           : launch_pdl(kv_commit_kernel<false>, dim3(batch), dim3(256), 0, stream, kt, vt, path, path_cap,
                        accept_len, qo, page_table, max_pages, num_pages, page_size, prefix_len, seq_len_out, kp, vp,
-                       hkv, row_bytes, status, ins, kv_scale);
+                       hkv, row_bytes, status, ins, kv_scale, behind_accept);
   if (e != cudaSuccess) return SPEC_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
 
-// a cache of the tree's own element type (plain copy)
+// right behind the acceptance, a cache of the tree's own element type (plain copy)
 int launch_kv_commit(int elem_bytes, const void* k_tree, const void* v_tree, const int32_t* path,
                      int path_cap, const int32_t* accept_len, const int32_t* qo,
                      const int32_t* page_table, int max_pages, int num_pages, int page_size,
@@ -168,7 +172,7 @@ int launch_kv_commit(int elem_bytes, const void* k_tree, const void* v_tree, con
                      int batch, int hkv, int d, int32_t* status, cudaStream_t stream, TokenInsert ins) {
   return launch_kv_commit(elem_bytes, k_tree, v_tree, path, path_cap, accept_len, qo, page_table, max_pages,
                           num_pages, page_size, prefix_len, seq_len_out, k_pool, v_pool, batch, hkv, d, status,
-                          stream, ins, nullptr);
+                          stream, ins, nullptr, true);
 }
 
 }  // namespace specv

@@ -65,3 +65,41 @@ def test_who_signals_early():
     # the page table's second kernel waits before it does anything, and ends the early start there
     body = KERNELS["page_count_kernel"][1]
     assert body.index("pdl_wait()") < body.index("ld(")
+
+
+# launched in plain stream order (<<< >>>): they start when every kernel before them has ended
+PLAIN = {"tree_mask_kernel", "attn_simt_kernel", "attn_combine_kernel"}
+# the conditions under which a kernel may put its first wait off: the caller's early reads, and the
+# commit that the acceptance launches behind itself
+DEFERRED = {"if (!p.early)", "if (!p.early_reads)", "if (!early)", "if (!behind_accept)"}
+LOAD = re.compile(r"\b(?:__ld\w+|ld)\(|prefetch\.global")
+
+
+def waiting():
+    return sorted(n for n in KERNELS if n not in PLAIN)
+
+
+def test_kernels_in_plain_stream_order():
+    for name in PLAIN:
+        assert "pdl_wait" not in KERNELS[name][1]
+        for f in os.listdir(CSRC):
+            assert not re.search(r"launch_pdl\(\s*" + name, source(f)) if f.endswith(".cu") else True
+
+
+@pytest.mark.parametrize("name", waiting())
+def test_nothing_is_read_before_the_wait(name):
+    body = KERNELS[name][1]
+    at = body.find("pdl_wait();")
+    assert at >= 0, "never waits"
+    first = LOAD.search(body)
+    assert first is None or at < first.start()
+    cond = re.search(r"(if \([^;{}]*\))\s*$", body[:at])
+    assert cond is None or cond.group(1) in DEFERRED
+
+
+@pytest.mark.parametrize("name", ["attn_tc_kernel", "attn_kv8p_kernel", "attn_tc_merge_kernel"])
+def test_a_grid_without_rows_still_waits(name):
+    """With early reads every CTA of a batch of empty trees leaves at its sizes: the first one has to
+    wait all the same, or the grid ends before its predecessor, and the next kernel's wait with it."""
+    body = KERNELS[name][1]
+    assert re.search(r"if \((\([^;{}]*\) == 0|idx == 0)\) pdl_wait\(\);", body)

@@ -59,3 +59,16 @@ def test_a_tree_past_max_nodes_leaves_its_sequence(max_nodes, size, hq, hkv, bat
     got = np.stack([d.out[t, h].double().cpu().numpy() for t, h in picks])
     gl = np.array([float(d.lse[t, h]) for t, h in picks])
     assert (np.abs(got - ref) <= tol(ref, A)).all() and np.abs(gl - lse).max() <= LSE_TOL
+
+
+@pytest.mark.parametrize("early", [False, True])
+@pytest.mark.parametrize("longest", [64, 2048])
+def test_a_batch_of_empty_trees(longest, early):
+    """Rows behind the last sequence only: left as they were, and the calls behind it run as ever."""
+    c = S.case([longest, 5], [0, 0], 16, 4, seed=3, pad_rows=6)
+    d = S.device(c)
+    with B.early_reads(early):
+        for _ in range(3):
+            call(d, 4, 4, longest)
+    assert int(d.status.item()) == 0
+    assert (d.out == 7).all() and (d.lse == 7).all()
