@@ -252,7 +252,7 @@ __device__ void commit_sequence(const CommitArgs& ca, int b, int base, int n, in
                                 int P_pre = -1) {
   const int rank = kCta ? (int)threadIdx.x : (int)(threadIdx.x & 31);
   const int size = kCta ? (int)blockDim.x : 32;
-  const int P = P_pre >= 0 ? P_pre : __ldg(ca.prefix_len + b);
+  const int P = P_pre >= 0 ? P_pre : ld(ca.prefix_len + b);
   const int32_t* prow_pt = ca.page_table + (size_t)b * ca.max_pages;
   auto node_at = [&](int i) { return spath != nullptr ? spath[i] : gpath[i]; };
   int code = 0;
@@ -264,7 +264,7 @@ __device__ void commit_sequence(const CommitArgs& ca, int b, int base, int n, in
     for (int i = first + rank; i <= L; i += size) {
       const int node = node_at(i);
       const int lp = (P + i) / ca.page_size;
-      const int page = lp < ca.max_pages ? __ldg(prow_pt + lp) : -1;
+      const int page = lp < ca.max_pages ? ld(prow_pt + lp) : -1;
       int c = 0;
       if (node < 0 || node >= n || (i == 0 && node != 0)) c = SPEC_ERR_INDEX;
       else if (lp >= ca.max_pages) c = SPEC_ERR_CAPACITY;
@@ -285,7 +285,7 @@ __device__ void commit_sequence(const CommitArgs& ca, int b, int base, int n, in
     const int slot = P + i;
     const int node = node_at(i);
     const int lp = slot / ca.page_size;
-    const int page = lp < ca.max_pages ? __ldg(prow_pt + lp) : -1;  // another slot's check may have failed
+    const int page = lp < ca.max_pages ? ld(prow_pt + lp) : -1;  // another slot's check may have failed
     src = ((size_t)(base + node) * ca.hkv + g) * row_bytes + ((size_t)vi << 4);
     dst = (((size_t)page * ca.hkv + g) * ca.page_size + (slot % ca.page_size)) * row_bytes + ((size_t)vi << 4);
     return node >= 0 && node < n && page >= 0 && page < ca.num_pages;
@@ -296,8 +296,8 @@ __device__ void commit_sequence(const CommitArgs& ca, int b, int base, int n, in
     size_t src = 0;
     dsts[u] = 0;
     if (e < total && locate(e, src, dsts[u])) {
-      kb[u] = __ldg(reinterpret_cast<const uint4*>(ca.k_tree + src));
-      vb[u] = __ldg(reinterpret_cast<const uint4*>(ca.v_tree + src));
+      kb[u] = ld(reinterpret_cast<const uint4*>(ca.k_tree + src));
+      vb[u] = ld(reinterpret_cast<const uint4*>(ca.v_tree + src));
     }
   }
   const bool bad = kCta ? __syncthreads_or(code != 0) : __any_sync(0xffffffffu, code != 0);
@@ -315,8 +315,8 @@ __device__ void commit_sequence(const CommitArgs& ca, int b, int base, int n, in
   for (int e = rank + kPer * size; e < total; e += size) {
     size_t src, dst;
     locate(e, src, dst);
-    const uint4 kv = __ldg(reinterpret_cast<const uint4*>(ca.k_tree + src));
-    const uint4 vv = __ldg(reinterpret_cast<const uint4*>(ca.v_tree + src));
+    const uint4 kv = ld(reinterpret_cast<const uint4*>(ca.k_tree + src));
+    const uint4 vv = ld(reinterpret_cast<const uint4*>(ca.v_tree + src));
     *reinterpret_cast<uint4*>(ca.k_pool + dst) = kv;
     *reinterpret_cast<uint4*>(ca.v_pool + dst) = vv;
   }
@@ -357,14 +357,14 @@ __device__ __forceinline__ void walk_commit_load(const CommitArgs& ca, int b, in
       const int node = spath[i];
       if (node >= 0 && node < n) {
         const size_t src = ((size_t)(base + node) * ca.hkv + g) * row_bytes + ((size_t)vi << 4);
-        c.kb[u] = __ldg(reinterpret_cast<const uint4*>(ca.k_tree + src));
-        c.vb[u] = __ldg(reinterpret_cast<const uint4*>(ca.v_tree + src));
+        c.kb[u] = ld(reinterpret_cast<const uint4*>(ca.k_tree + src));
+        c.vb[u] = ld(reinterpret_cast<const uint4*>(ca.v_tree + src));
         slot_i[u] = i;
         c.dst[u] = (size_t)g * ca.page_size * row_bytes + ((size_t)vi << 4);  // + the page and slot below
       }
     }
   }
-  const int P = __ldg(ca.prefix_len + b);
+  const int P = ld(ca.prefix_len + b);
   const int32_t* prow_pt = ca.page_table + (size_t)b * ca.max_pages;
   int code = 0;
   if (!shape_ok || P < 0) {
@@ -375,7 +375,7 @@ __device__ __forceinline__ void walk_commit_load(const CommitArgs& ca, int b, in
     for (int i = rank; i <= L; i += size) {
       const int node = spath[i];
       const int lp = (P + i) / ca.page_size;
-      const int page = lp < ca.max_pages ? __ldg(prow_pt + lp) : -1;
+      const int page = lp < ca.max_pages ? ld(prow_pt + lp) : -1;
       int cc = 0;
       if (node < 0 || node >= n || (i == 0 && node != 0)) cc = SPEC_ERR_INDEX;
       else if (lp >= ca.max_pages) cc = SPEC_ERR_CAPACITY;
@@ -388,7 +388,7 @@ __device__ __forceinline__ void walk_commit_load(const CommitArgs& ca, int b, in
     if (slot_i[u] >= 0 && code == 0) {
       const int slot = P + slot_i[u];
       const int lp = slot / ca.page_size;
-      const int page = lp < ca.max_pages ? __ldg(prow_pt + lp) : 0;
+      const int page = lp < ca.max_pages ? ld(prow_pt + lp) : 0;
       c.dst[u] += (((size_t)page * ca.hkv) * ca.page_size + (slot % ca.page_size)) * row_bytes;
     }
   }
@@ -421,12 +421,12 @@ __device__ __forceinline__ void walk_commit_store(const CommitArgs& ca, int b, i
     const int r = e / vecs, vi = e - (e / vecs) * vecs;
     const int i = r / ca.hkv, g = r - (r / ca.hkv) * ca.hkv;
     const int slot = P + i;
-    const int page = __ldg(prow_pt + slot / ca.page_size);
+    const int page = ld(prow_pt + slot / ca.page_size);
     const size_t src = ((size_t)(base + spath[i]) * ca.hkv + g) * row_bytes + ((size_t)vi << 4);
     const size_t dst =
         (((size_t)page * ca.hkv + g) * ca.page_size + (slot % ca.page_size)) * row_bytes + ((size_t)vi << 4);
-    const uint4 kv = __ldg(reinterpret_cast<const uint4*>(ca.k_tree + src));
-    const uint4 vv = __ldg(reinterpret_cast<const uint4*>(ca.v_tree + src));
+    const uint4 kv = ld(reinterpret_cast<const uint4*>(ca.k_tree + src));
+    const uint4 vv = ld(reinterpret_cast<const uint4*>(ca.v_tree + src));
     *reinterpret_cast<uint4*>(ca.k_pool + dst) = kv;
     *reinterpret_cast<uint4*>(ca.v_pool + dst) = vv;
   }
@@ -477,7 +477,7 @@ __device__ int root_write(const CommitArgs& ca, int b, int P, int n, int path_ca
   bool ok = true;
   if (lp0 + lane <= lp1) {
     const int lp = lp0 + lane;
-    page = lp < ca.max_pages ? __ldg(ca.page_table + (size_t)b * ca.max_pages + lp) : -1;
+    page = lp < ca.max_pages ? ld(ca.page_table + (size_t)b * ca.max_pages + lp) : -1;
     ok = page >= 0 && page < ca.num_pages;
   }
   if (!__all_sync(0xffffffffu, ok)) return -1;
@@ -496,8 +496,8 @@ __device__ int root_write(const CommitArgs& ca, int b, int P, int n, int path_ca
 // (five CTAs per SM: the streaming loop needs the occupancy, the final CTA's epilogue may spill)
 template <bool kVec, bool kIns>
 __global__ void __launch_bounds__(kAcceptThreads, 5) accept_greedy_kernel(
-    const float* __restrict__ logits, int vocab, int gchunks, int tasks, const int32_t* __restrict__ qo,
-    int batch, int total_nodes, const int32_t* __restrict__ parent, const int32_t* __restrict__ tokens,
+    const float* logits, int vocab, int gchunks, int tasks, const int32_t* qo,
+    int batch, int total_nodes, const int32_t* parent, const int32_t* tokens,
     int path_cap, int32_t* accept_len, int32_t* path, int32_t* out_tokens, uint8_t* flags, unsigned* done,
     unsigned long long* slots, ArgPartial* partials, int* argmax, int32_t* status, const CommitArgs ca) {
   __shared__ float sv[2][kAcceptThreads / 32];
@@ -512,7 +512,7 @@ __global__ void __launch_bounds__(kAcceptThreads, 5) accept_greedy_kernel(
     }
     if (ca.k_tree != nullptr) {  // each sequence's page-table entries from its prefix end on
       for (int bb = threadIdx.x; bb < batch; bb += kAcceptThreads) {
-        const int P = __ldg(ca.prefix_len + bb);
+        const int P = ld(ca.prefix_len + bb);
         const int lp = P >= 0 ? P / ca.page_size : 0;
         if (lp < ca.max_pages)
           asm volatile("prefetch.global.L2 [%0];" ::"l"(ca.page_table + (size_t)bb * ca.max_pages + lp));
@@ -615,16 +615,16 @@ __global__ void __launch_bounds__(kAcceptThreads, 5) accept_greedy_kernel(
   if (early && warp == kRootWarp) {
     int base = 0;
     if (lane < batch) {
-      base = __ldg(qo + lane);
-      root_n = __ldg(qo + lane + 1) - base;
-      root_P = __ldg(ca.prefix_len + lane);  // not waited for before the walk
+      base = ld(qo + lane);
+      root_n = ld(qo + lane + 1) - base;
+      root_P = ld(ca.prefix_len + lane);  // not waited for before the walk
     }
     for (int b = 0; b < batch; ++b) root_stage(ca, __shfl_sync(0xffffffffu, base, b), root_buf(b));
   }
   if (staged) {
     for (int i = threadIdx.x; i < total_nodes; i += kAcceptThreads) {
-      s_par[i] = __ldg(parent + i);
-      s_tok[i] = __ldg(tokens + i);
+      s_par[i] = ld(parent + i);
+      s_tok[i] = ld(tokens + i);
     }
   }
   if (slots != nullptr) {  // each row's argmax is already folded into its slot
@@ -673,8 +673,8 @@ __global__ void __launch_bounds__(kAcceptThreads, 5) accept_greedy_kernel(
   }
   __syncthreads();
   for (int b = warp; b < batch; b += kAcceptThreads / 32) {
-    const int base = __ldg(qo + b);
-    const int n = min(__ldg(qo + b + 1) - base, kMaxTreeNodes);
+    const int base = ld(qo + b);
+    const int n = min(ld(qo + b + 1) - base, kMaxTreeNodes);
     if (staged) {
       int* sp = (ca.k_tree != nullptr && b < kCommitCta && path_cap <= kCommitPathStage) ? s_cpath[b] : nullptr;
       const int L = greedy_walk_warp_staged(b, n, s_par + base, s_tok + base, s_am + base, s_child + base, path_cap,
@@ -699,17 +699,17 @@ __global__ void __launch_bounds__(kAcceptThreads, 5) accept_greedy_kernel(
   if (batch <= kCommitCta) {  // few sequences: the whole CTA on each in turn
     const bool in_smem = staged && path_cap <= kCommitPathStage;
     for (int b = 0; b < batch; ++b) {
-      const int base = __ldg(qo + b);
+      const int base = ld(qo + b);
       const int rootP = early ? s_root_P[b] : -1;
-      commit_sequence<true, kIns>(ca, b, base, __ldg(qo + b + 1) - base, staged ? s_len[b] : accept_len[b],
+      commit_sequence<true, kIns>(ca, b, base, ld(qo + b + 1) - base, staged ? s_len[b] : accept_len[b],
                             in_smem ? s_cpath[b] : nullptr, path + (size_t)b * path_cap, path_cap, status,
                             rootP >= 0 ? 1 : 0, rootP);
       __syncthreads();
     }
   } else {
     for (int b = warp; b < batch; b += kAcceptThreads / 32) {
-      const int base = __ldg(qo + b);
-      commit_sequence<false, kIns>(ca, b, base, __ldg(qo + b + 1) - base, accept_len[b], nullptr,
+      const int base = ld(qo + b);
+      commit_sequence<false, kIns>(ca, b, base, ld(qo + b + 1) - base, accept_len[b], nullptr,
                              path + (size_t)b * path_cap, path_cap, status);
     }
   }
@@ -742,8 +742,8 @@ bool greedy_walks(int batch, int total_nodes, int vocab, int path_cap, int sms) 
 }
 
 __global__ void __cluster_dims__(kLazyCluster, 1, 1) __launch_bounds__(kLazyThreads, 2)
-    accept_greedy_lazy_kernel(const float* __restrict__ logits, int vocab, const int32_t* __restrict__ qo,
-                              const int32_t* __restrict__ parent, const int32_t* __restrict__ tokens, int path_cap,
+    accept_greedy_lazy_kernel(const float* logits, int vocab, const int32_t* qo,
+                              const int32_t* parent, const int32_t* tokens, int path_cap,
                               int32_t* accept_len, int32_t* path, int32_t* out_tokens, uint8_t* flags,
                               int32_t* status, bool vec, bool early, const CommitArgs ca) {
   cg::cluster_group cl = cg::this_cluster();
@@ -760,8 +760,8 @@ __global__ void __cluster_dims__(kLazyCluster, 1, 1) __launch_bounds__(kLazyThre
   const int b = blockIdx.y;
   const int rank = (int)cl.block_rank();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int base = __ldg(qo + b);
-  const int n = min(__ldg(qo + b + 1) - base, kMaxTreeNodes);
+  const int base = ld(qo + b);
+  const int n = min(ld(qo + b + 1) - base, kMaxTreeNodes);
   int32_t* prow = path + (size_t)b * path_cap;
   int32_t* trow = out_tokens + (size_t)b * path_cap;
   const bool writer = rank == 0 && threadIdx.x == 0;
@@ -771,8 +771,8 @@ __global__ void __cluster_dims__(kLazyCluster, 1, 1) __launch_bounds__(kLazyThre
     return;
   }
   for (int c = threadIdx.x; c < n; c += kLazyThreads) {
-    s_par[c] = __ldg(parent + base + c);
-    s_tok[c] = __ldg(tokens + base + c);
+    s_par[c] = ld(parent + base + c);
+    s_tok[c] = ld(tokens + base + c);
   }
   if (threadIdx.x == 0) s_path[0] = 0;  // the root
   const int per = ((vocab + kLazyCluster - 1) / kLazyCluster + 3) & ~3;
@@ -939,8 +939,8 @@ struct RowEval {
   float m_p, m_q, invT, inv_zp, inv_zq;
   __device__ __forceinline__ float pv(float x) const { return expf((x - m_p) * invT) * inv_zp; }
   __device__ __forceinline__ float qv(float x) const { return expf((x - m_q) * invT) * inv_zq; }
-  __device__ __forceinline__ float p(int t) const { return pv(__ldg(tl + t)); }
-  __device__ __forceinline__ float q(int t) const { return qv(__ldg(dl + t)); }
+  __device__ __forceinline__ float p(int t) const { return pv(ld(tl + t)); }
+  __device__ __forceinline__ float q(int t) const { return qv(ld(dl + t)); }
 };
 
 struct WalkSlice {
@@ -1005,8 +1005,8 @@ __device__ NodeStats walk_row_stats(cg::cluster_group& cl, WalkShared& sh, const
         for (int u = 0; u < 8; ++u) {  // every load issued (clamped into the slice), then used
           const int i = i0 + u * kWalkThreads;
           const int ic = i < n4 ? i : n4 - 1;
-          a[u] = __ldg(t4 + ic);
-          d[u] = __ldg(d4 + ic);
+          a[u] = ld(t4 + ic);
+          d[u] = ld(d4 + ic);
         }
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
@@ -1022,8 +1022,8 @@ __device__ NodeStats walk_row_stats(cg::cluster_group& cl, WalkShared& sh, const
       }
     } else {
       for (int i = threadIdx.x; i < pad; i += kWalkThreads) {
-        const float x = i < sl.n ? __ldg(trow + sl.c_lo + i) : -INFINITY;
-        const float y = i < sl.n ? __ldg(drow + sl.c_lo + i) : -INFINITY;
+        const float x = i < sl.n ? ld(trow + sl.c_lo + i) : -INFINITY;
+        const float y = i < sl.n ? ld(drow + sl.c_lo + i) : -INFINITY;
         sl.sp[i] = x;
         sl.sq[i] = y;
         mp = fmaxf(mp, x);
@@ -1032,8 +1032,8 @@ __device__ NodeStats walk_row_stats(cg::cluster_group& cl, WalkShared& sh, const
     }
   } else {
     for (int i = threadIdx.x; i < sl.n; i += kWalkThreads) {
-      mp = fmaxf(mp, __ldg(trow + sl.c_lo + i));
-      mq = fmaxf(mq, __ldg(drow + sl.c_lo + i));
+      mp = fmaxf(mp, ld(trow + sl.c_lo + i));
+      mq = fmaxf(mq, ld(drow + sl.c_lo + i));
     }
   }
 #pragma unroll
@@ -1095,8 +1095,8 @@ __device__ NodeStats walk_row_stats(cg::cluster_group& cl, WalkShared& sh, const
     }
   } else {
     for (int i = threadIdx.x; i < sl.n; i += kWalkThreads) {
-      if (okp) kahan(expf((__ldg(trow + sl.c_lo + i) - Mp) * invT), sp, cp);
-      if (okq) kahan(expf((__ldg(drow + sl.c_lo + i) - Mq) * invT), sq, cq);
+      if (okp) kahan(expf((ld(trow + sl.c_lo + i) - Mp) * invT), sp, cp);
+      if (okq) kahan(expf((ld(drow + sl.c_lo + i) - Mq) * invT), sq, cq);
     }
   }
   const F2 wp = f2_warp_sum(F2{sp, -cp}), wq = f2_warp_sum(F2{sq, -cq});
@@ -1207,10 +1207,10 @@ __device__ F2 walk_pass(cg::cluster_group& cl, WalkShared& sh, const WalkSlice& 
 }
 
 __global__ void __cluster_dims__(kWalkCluster, 1, 1) __launch_bounds__(kWalkThreads)
-    accept_walk_kernel(const int32_t* __restrict__ parent, const int32_t* __restrict__ tokens,
-                       const float* __restrict__ tl, const float* __restrict__ dl,
-                       const float* __restrict__ uniforms, float temperature, int vocab,
-                       const int32_t* __restrict__ qo, int path_cap, int32_t* accept_len, int32_t* path,
+    accept_walk_kernel(const int32_t* parent, const int32_t* tokens,
+                       const float* tl, const float* dl,
+                       const float* uniforms, float temperature, int vocab,
+                       const int32_t* qo, int path_cap, int32_t* accept_len, int32_t* path,
                        int32_t* out_tokens, uint8_t* flags,
                        int32_t* status, bool vec) {
   cg::cluster_group cl = cg::this_cluster();
@@ -1220,8 +1220,8 @@ __global__ void __cluster_dims__(kWalkCluster, 1, 1) __launch_bounds__(kWalkThre
   const int b = blockIdx.y;
   const int rank = (int)cl.block_rank();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int base = __ldg(qo + b);
-  const int n = __ldg(qo + b + 1) - base;
+  const int base = ld(qo + b);
+  const int n = ld(qo + b + 1) - base;
   const float invT = 1.0f / temperature;
   int32_t* prow = path + (size_t)b * path_cap;
   int32_t* trow = out_tokens + (size_t)b * path_cap;
@@ -1240,7 +1240,7 @@ __global__ void __cluster_dims__(kWalkCluster, 1, 1) __launch_bounds__(kWalkThre
     for (int w = threadIdx.x; w < kMaxTreeNodes / 32; w += blockDim.x) sh.kids[w] = 0u;
     __syncthreads();
     for (int c = v + 1 + threadIdx.x; c < n; c += blockDim.x)
-      if (__ldg(parent + base + c) == v) atomicOr(&sh.kids[c >> 5], 1u << (c & 31));
+      if (ld(parent + base + c) == v) atomicOr(&sh.kids[c >> 5], 1u << (c & 31));
     const float* trow_v = tl + (size_t)(base + v) * vocab;
     const float* drow_v = dl + (size_t)(base + v) * vocab;
     const NodeStats st = walk_row_stats(cl, sh, sl, trow_v, drow_v, invT, vec);  // (syncs the CTA)
@@ -1275,12 +1275,12 @@ __global__ void __cluster_dims__(kWalkCluster, 1, 1) __launch_bounds__(kWalkThre
       // their tokens, then p(x), q(x) (the fp32 values the passes use) and u: one round trip each
       for (int j = threadIdx.x; j < nk; j += blockDim.x) {
         const int c = sh.kid_c[j];
-        const int x = __ldg(tokens + base + c);
+        const int x = ld(tokens + base + c);
         sh.kid_x[j] = x;
         const bool okx = x >= 0 && x < vocab;
         sh.kid_p[j] = okx ? ev.p(x) : 0.f;
         sh.kid_q[j] = okx ? ev.q(x) : 0.f;
-        sh.kid_u[j] = __ldg(uniforms + 2 * (size_t)(base + c));
+        sh.kid_u[j] = ld(uniforms + 2 * (size_t)(base + c));
       }
       __syncthreads();
       for (int j = 0; j < nk; ++j) {
@@ -1331,7 +1331,7 @@ __global__ void __cluster_dims__(kWalkCluster, 1, 1) __launch_bounds__(kWalkThre
         ++L;
         if (writer) {
           prow[L] = accepted;
-          trow[L - 1] = __ldg(tokens + base + accepted);
+          trow[L - 1] = ld(tokens + base + accepted);
         }
         v = accepted;
         continue;
@@ -1351,7 +1351,7 @@ __global__ void __cluster_dims__(kWalkCluster, 1, 1) __launch_bounds__(kWalkThre
       }
       __syncthreads();
       // threshold and segment bounds in double-float: the segment intervals tile the line
-      const F2 thr = f2_mul_f(total2, __ldg(uniforms + 2 * (size_t)(base + v) + 1));
+      const F2 thr = f2_mul_f(total2, ld(uniforms + 2 * (size_t)(base + v) + 1));
       const int s_lo = warp * sl.seg, s_hi = min(sl.n, s_lo + sl.seg);
       const F2 seg_start = f2_add(cta_pre, F2{sh.pre_hi[warp], sh.pre_lo[warp]});
       const F2 seg_end = f2_add(seg_start, F2{sh.part_hi[warp], sh.part_lo[warp]});

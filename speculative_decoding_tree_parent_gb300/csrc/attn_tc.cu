@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(TcCfg<kFp8, kPar>::kThreads, 1)
     __shared__ int s_key[kLptMax];
     __shared__ int s_seq;
     for (int t = threadIdx.x; t < p.batch; t += blockDim.x)
-      s_key[t] = __ldg(p.prefix_len + t) + (__ldg(p.qo + t + 1) - __ldg(p.qo + t));
+      s_key[t] = ld(p.prefix_len + t) + (ld(p.qo + t + 1) - ld(p.qo + t));
     __syncthreads();
     for (int t = threadIdx.x; t < p.batch; t += blockDim.x) {
       const int k = s_key[t];
@@ -242,9 +242,9 @@ __global__ void __launch_bounds__(TcCfg<kFp8, kPar>::kThreads, 1)
     for (int i = (threadIdx.x & 31) * 32; i < p.max_pages; i += 32 * 32)
       asm volatile("prefetch.global.L2 [%0];" ::"l"(p.page_table + (size_t)b * p.max_pages + i));
   }
-  const int base = __ldg(p.qo + b);
-  const int N = __ldg(p.qo + b + 1) - base;
-  const int P = __ldg(p.prefix_len + b);
+  const int base = ld(p.qo + b);
+  const int N = ld(p.qo + b + 1) - base;
+  const int P = ld(p.prefix_len + b);
   const int npt = kTcRows / G;  // tree nodes per M-tile
   const int node0 = 2 * pair * npt;
   const bool has1 = node0 + npt < N;  // tile 1 holds rows of this sequence
@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(TcCfg<kFp8, kPar>::kThreads, 1)
       const int lp = sr.pg_lo + blk * 4 + (lane & 3);
       int page = p.num_pages;
       if (blk < npb && lp < sr.pg_hi) {
-        const int pg = __ldg(p.page_table + (size_t)b * p.max_pages + lp);
+        const int pg = ld(p.page_table + (size_t)b * p.max_pages + lp);
         if (pg >= 0 && pg < p.num_pages) page = pg;
         else report(p.status, SPEC_ERR_PAGE);
       }
@@ -554,7 +554,7 @@ __global__ void __launch_bounds__(TcCfg<kFp8, kPar>::kThreads, 1)
       // exponent and its row sum is divided by it
       float sl2_pre = sl2, lvs_pre = 0.f, ivs_pre = 1.f;
       if (kFp8) {
-        const float ks = __ldg(p.kv_scale + g), vs = __ldg(p.kv_scale + p.hkv + g);
+        const float ks = ld(p.kv_scale + g), vs = ld(p.kv_scale + p.hkv + g);
         sl2_pre = sl2 * ks;
         lvs_pre = log2f(vs);
         ivs_pre = 1.f / vs;
@@ -789,8 +789,8 @@ __global__ void __launch_bounds__(kMergeThreads) attn_tc_merge_kernel(const TcMe
   // the attention grid has finished: its partials are visible. (It signals before its own wait, so
   // qo_indptr is read ahead only where the caller lets the attention do so.)
   if (!p.early_reads) pdl_wait();
-  const int base = __ldg(p.qo + b);
-  const int N = __ldg(p.qo + b + 1) - base;
+  const int base = ld(p.qo + b);
+  const int N = ld(p.qo + b + 1) - base;
   if (idx == 0) pdl_wait();  // (whatever the sizes: the grid must not end before the attention)
   if (node_l >= N || N > p.mtiles * (kTcRows / G)) return;  // (a tree past the row tiles was refused)
   pdl_wait();

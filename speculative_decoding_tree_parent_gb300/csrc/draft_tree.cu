@@ -73,14 +73,14 @@ struct TreeLayout {
 
 size_t tree_state_bytes(int batch, int max_nodes) { return (size_t)batch * TreeLayout::make(max_nodes).per_seq; }
 
-__global__ void tree_init_kernel(const int32_t* __restrict__ root_tokens, int batch, TreeArgs a) {
+__global__ void tree_init_kernel(const int32_t* root_tokens, int batch, TreeArgs a) {
   const int b = blockIdx.x;
   const TreeLayout l = TreeLayout::make(a.max_nodes);
   uint8_t* st = a.state + (size_t)b * l.per_seq;
   pdl_wait();
   for (int i = threadIdx.x; i < a.max_nodes; i += blockDim.x) {
     a.parent_out[(size_t)b * a.max_nodes + i] = -1;
-    a.tokens_out[(size_t)b * a.max_nodes + i] = i == 0 ? __ldg(root_tokens + b) : -1;
+    a.tokens_out[(size_t)b * a.max_nodes + i] = i == 0 ? ld(root_tokens + b) : -1;
   }
   if (threadIdx.x == 0) {
     TreeHeader* h = reinterpret_cast<TreeHeader*>(st);
@@ -125,7 +125,7 @@ struct RowTopk {
 };
 
 template <int KMAX, bool kVec>
-__device__ __forceinline__ bool tree_row_topk(const float* __restrict__ row_base, int vocab, int k, RowTopk& out) {
+__device__ __forceinline__ bool tree_row_topk(const float* row_base, int vocab, int k, RowTopk& out) {
   namespace cg = cooperative_groups;
   cg::cluster_group cl = cg::this_cluster();
   const int rank = (int)cl.block_rank();
@@ -166,7 +166,7 @@ __device__ __forceinline__ bool tree_row_topk(const float* __restrict__ row_base
 #pragma unroll
         for (int q = 0; q < kU; ++q) {
           const int i4 = i0 + q * kTreeThreads;
-          xv[q] = i4 < n4 ? (stream ? __ldcs(r4 + i4) : __ldg(r4 + i4)) : make_float4(0.f, 0.f, 0.f, 0.f);
+          xv[q] = i4 < n4 ? (stream ? __ldcs(r4 + i4) : ld(r4 + i4)) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
 #pragma unroll
         for (int q = 0; q < kU; ++q) {
@@ -185,7 +185,7 @@ __device__ __forceinline__ bool tree_row_topk(const float* __restrict__ row_base
 #pragma unroll
         for (int q = 0; q < kU; ++q) {
           const int t = i0 + q * kTreeThreads;
-          xv[q] = t < n_sl ? (stream ? __ldcs(row + t) : __ldg(row + t)) : 0.f;
+          xv[q] = t < n_sl ? (stream ? __ldcs(row + t) : ld(row + t)) : 0.f;
         }
 #pragma unroll
         for (int q = 0; q < kU; ++q) {
@@ -489,7 +489,7 @@ __device__ __forceinline__ int pop_node(TreeHeader* h, double* score, int* depth
 
 template <int KMAX, bool kVec>
 __global__ void __cluster_dims__(kTreeCluster, 1, 1) __launch_bounds__(kTreeThreads, 1)
-    tree_expand_kernel(const float* __restrict__ logits, int vocab, long row_stride, long node_stride, TreeArgs a) {
+    tree_expand_kernel(const float* logits, int vocab, long row_stride, long node_stride, TreeArgs a) {
   const int b = blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const TreeLayout l = TreeLayout::make(a.max_nodes);
@@ -926,7 +926,7 @@ __device__ __noinline__ void tree_replay_fast(TreeHeader* h, double* score, int*
 // every CTA has read it, and nothing waits: the other clusters are done when they count in.
 template <int KMAX, bool kVec>
 __global__ void __cluster_dims__(kTreeCluster, 1, 1) __launch_bounds__(kTreeThreads, 1)
-    tree_expand_multi_kernel(const float* __restrict__ logits, int vocab, long row_stride, long req_stride,
+    tree_expand_multi_kernel(const float* logits, int vocab, long row_stride, long req_stride,
                              TreeArgs a, int fast_cap) {
   namespace cg = cooperative_groups;
   cg::cluster_group cl = cg::this_cluster();

@@ -36,12 +36,12 @@ __device__ __forceinline__ uint4 quant16(const uint4& u, const uint4& v, float s
 
 template <bool kQuant>
 __global__ void __launch_bounds__(256) kv_commit_kernel(
-    const uint8_t* __restrict__ k_tree, const uint8_t* __restrict__ v_tree,
-    const int32_t* __restrict__ path, int path_cap, const int32_t* __restrict__ accept_len,
-    const int32_t* __restrict__ qo, const int32_t* __restrict__ page_table, int max_pages,
-    int num_pages, int page_size, const int32_t* __restrict__ prefix_len,
-    int32_t* __restrict__ seq_len_out, uint8_t* __restrict__ k_pool, uint8_t* __restrict__ v_pool,
-    int hkv, int row_bytes, int32_t* status, const TokenInsert ins, const float* __restrict__ kv_scale,
+    const uint8_t* k_tree, const uint8_t* v_tree,
+    const int32_t* path, int path_cap, const int32_t* accept_len,
+    const int32_t* qo, const int32_t* page_table, int max_pages,
+    int num_pages, int page_size, const int32_t* prefix_len,
+    int32_t* seq_len_out, uint8_t* k_pool, uint8_t* v_pool,
+    int hkv, int row_bytes, int32_t* status, const TokenInsert ins, const float* kv_scale,
     bool behind_accept) {
   const int b = blockIdx.x;
   __shared__ int s_ok;
@@ -52,9 +52,9 @@ __global__ void __launch_bounds__(256) kv_commit_kernel(
   // K/V rows (a few KB) -- so only accept_len / path remain on the critical path. As a call of its
   // own the commit does not know what ran before it: it waits first.
   if (!behind_accept) pdl_wait();
-  const int base = __ldg(qo + b);
-  const int n = __ldg(qo + b + 1) - base;
-  const int P = __ldg(prefix_len + b);
+  const int base = ld(qo + b);
+  const int n = ld(qo + b + 1) - base;
+  const int P = ld(prefix_len + b);
   if (behind_accept) {
     const int span = n < path_cap ? n : path_cap;
     const int lp0 = P / page_size, lp1 = (P + span - 1) / page_size;
@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(256) kv_commit_kernel(
   }
   pdl_wait();  // accept_len / path come from the acceptance kernel just before
   if (threadIdx.x == 0) {
-    int L = __ldg(accept_len + b);
+    int L = ld(accept_len + b);
     int ok = 1;
     if (L < 0 || L >= path_cap || L >= n || P < 0) {
       report(status, SPEC_ERR_INDEX);
@@ -88,14 +88,14 @@ __global__ void __launch_bounds__(256) kv_commit_kernel(
   if (!s_ok) return;
   // validation of every slot (L + 1 <= path_cap entries, one thread each)
   for (int i = threadIdx.x; i <= L; i += blockDim.x) {
-    const int node = __ldg(path + (size_t)b * path_cap + i);
+    const int node = ld(path + (size_t)b * path_cap + i);
     const int slot = P + i;
     const int lp = slot / page_size;
     int code = 0;
     if (node < 0 || node >= n || (i == 0 && node != 0)) code = SPEC_ERR_INDEX;
     else if (lp >= max_pages) code = SPEC_ERR_CAPACITY;
     else {
-      const int page = __ldg(page_table + (size_t)b * max_pages + lp);
+      const int page = ld(page_table + (size_t)b * max_pages + lp);
       if (page < 0 || page >= num_pages) code = SPEC_ERR_PAGE;
     }
     if (code) {
@@ -114,29 +114,29 @@ __global__ void __launch_bounds__(256) kv_commit_kernel(
     const int vi = e - r * vecs_per_row;
     const int i = r / hkv;
     const int g = r - i * hkv;
-    const int node = __ldg(path + (size_t)b * path_cap + i);
+    const int node = ld(path + (size_t)b * path_cap + i);
     const int slot = P + i;
-    const int page = __ldg(page_table + (size_t)b * max_pages + slot / page_size);
+    const int page = ld(page_table + (size_t)b * max_pages + slot / page_size);
     const int prow = slot - (slot / page_size) * page_size;
     const size_t dst = (((size_t)page * hkv + g) * page_size + prow) * row_bytes + ((size_t)vi << 4);
     if (kQuant) {
       const size_t src = ((size_t)(base + node) * hkv + g) * (2 * row_bytes) + ((size_t)vi << 5);
       const uint4* ks = reinterpret_cast<const uint4*>(k_tree + src);
       const uint4* vs = reinterpret_cast<const uint4*>(v_tree + src);
-      const uint4 k0v = __ldg(ks), k1v = __ldg(ks + 1), v0v = __ldg(vs), v1v = __ldg(vs + 1);
-      *reinterpret_cast<uint4*>(k_pool + dst) = quant16(k0v, k1v, __ldg(kv_scale + g));
-      *reinterpret_cast<uint4*>(v_pool + dst) = quant16(v0v, v1v, __ldg(kv_scale + hkv + g));
+      const uint4 k0v = ld(ks), k1v = ld(ks + 1), v0v = ld(vs), v1v = ld(vs + 1);
+      *reinterpret_cast<uint4*>(k_pool + dst) = quant16(k0v, k1v, ld(kv_scale + g));
+      *reinterpret_cast<uint4*>(v_pool + dst) = quant16(v0v, v1v, ld(kv_scale + hkv + g));
     } else {
       const size_t src = ((size_t)(base + node) * hkv + g) * row_bytes + ((size_t)vi << 4);
-      const uint4 kv = __ldg(reinterpret_cast<const uint4*>(k_tree + src));
-      const uint4 vv = __ldg(reinterpret_cast<const uint4*>(v_tree + src));
+      const uint4 kv = ld(reinterpret_cast<const uint4*>(k_tree + src));
+      const uint4 vv = ld(reinterpret_cast<const uint4*>(v_tree + src));
       *reinterpret_cast<uint4*>(k_pool + dst) = kv;
       *reinterpret_cast<uint4*>(v_pool + dst) = vv;
     }
   }
   if (ins.token_buf != nullptr)  // the accepted tokens and the bonus after the root (room checked above)
     for (int i = threadIdx.x; i <= L; i += blockDim.x)
-      ins.token_buf[(size_t)b * ins.token_stride + P + 1 + i] = __ldg(ins.out_tokens + (size_t)b * path_cap + i);
+      ins.token_buf[(size_t)b * ins.token_stride + P + 1 + i] = ld(ins.out_tokens + (size_t)b * path_cap + i);
   if (threadIdx.x == 0 && seq_len_out != nullptr) seq_len_out[b] = P + L + 1;
 }
 

@@ -103,3 +103,22 @@ def test_a_grid_without_rows_still_waits(name):
     wait all the same, or the grid ends before its predecessor, and the next kernel's wait with it."""
     body = KERNELS[name][1]
     assert re.search(r"if \((\([^;{}]*\) == 0|idx == 0)\) pdl_wait\(\);", body)
+
+
+@pytest.mark.parametrize("name", waiting())
+def test_loads_are_plain(name):
+    """__ldg and const __restrict__ promise that a value does not change while the kernel runs, which
+    lets a load be moved ahead of the wait: not for what the kernel before may write."""
+    head, body = KERNELS[name]
+    assert "__ldg" not in body and "__restrict__" not in head
+
+
+def test_loads_in_the_functions_they_call_are_plain():
+    for f in os.listdir(CSRC):
+        src = source(f)
+        if "pdl_wait()" in src and f != "common.cuh":
+            assert "__ldg" not in src and "__restrict__" not in src, f
+    # (the one function of the shared header that uses it serves kernels in plain stream order)
+    users = [f for f in os.listdir(CSRC) if re.search(r"\bseq_of_row\(", source(f)) and f != "common.cuh"]
+    assert "__ldg" not in re.sub(r"int seq_of_row\(.*?\n}", "", source("common.cuh"), flags=re.S)
+    assert all("pdl_wait()" not in source(f) for f in users)
