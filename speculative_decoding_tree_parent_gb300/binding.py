@@ -109,13 +109,14 @@ def _ptr(t) -> int | None:
 
 # the current stream's handle without a Stream object around it (2.5 us of a call), where torch has it
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream(stream) -> int | None:
     if stream is not None:
         return stream.cuda_stream
     if _raw_stream is not None:
-        return _raw_stream(torch.cuda.current_device())
+        return _raw_stream(_device())
     return torch.cuda.current_stream().cuda_stream
 
 
@@ -377,58 +378,97 @@ def spec_tree_verify_attn_parents(q, k_pool, v_pool, page_table, prefix_len, max
     return _check(st, "spec_tree_verify_attn_parents")
 
 
+def _refuse(t, dtype, n, what):
+    if t.dtype is not dtype:
+        raise ValueError(f"{what}: {dtype} expected, got {t.dtype}")
+    if t.numel() < n:
+        raise ValueError(f"{what}: {n} elements expected, got {t.numel()}")
+    raise ValueError("device tensor expected" if not t.is_cuda else "contiguous tensor expected")
+
+
+def _ptrs(args):
+    """Pointers of contiguous device tensors (or None), each given with its type and the elements
+    that the call may touch. (One loop, each property asked once: a call's own time counts.)"""
+    out = []
+    for t, dtype, n, what in args:
+        if t is None:
+            out.append(None)
+            continue
+        if t.dtype is not dtype or (n and t.numel() < n) or not t.is_cuda or not t.is_contiguous():
+            _refuse(t, dtype, n, what)
+        out.append(t.data_ptr())
+    return out
+
+
+def _kv8p_pool(k_pool, v_pool, kv_scale, hkv, d):
+    """(num_pages, page_size) of pools and scales whose shapes are those of the rows."""
+    shape = k_pool.shape
+    pages, heads, ps, e = shape
+    if v_pool.shape != shape or kv_scale.shape != (pages, heads, 2):
+        raise ValueError("kv_scale: [num_pages][hkv][2], and pools of one shape, expected")
+    if heads != hkv or e != d:
+        raise ValueError(f"pools: {hkv} KV heads of {d} elements expected, got {heads} of {e}")
+    return pages, ps
+
+
+_BF, _F32, _I32, _I64, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.int64, torch.uint8
+
+
 def spec_tree_verify_attn_kv8p(q, k_pool, v_pool, kv_scale, page_table, prefix_len, max_prefix, k_tree, v_tree,
                                mask, qo_indptr, max_nodes, out, lse=None, ws=None, sm_scale=0.0, dev_status=None,
                                stream=None):
     """Tree-verify attention over an FP8 cache with page scales: k_pool/v_pool uint8 E4M3
     codes [pages,Hkv,16,128], kv_scale float32 [pages,Hkv,2] (K scale, V scale); q, k_tree,
     v_tree and out bf16. ws: spec_workspace_size(SPEC_OP_ATTN_KV8P, ...) bytes."""
-    for t, what in ((q, "q"), (k_tree, "k_tree"), (v_tree, "v_tree"), (out, "out")):
-        _need(t, torch.bfloat16, what)
-    _need_kv8p(k_pool, v_pool, kv_scale)
     T, hq, d = q.shape
-    num_pages, hkv, ps, _ = k_pool.shape
-    st = load().spec_tree_verify_attn_kv8p(
-        _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(kv_scale), num_pages, ps, _ptr(page_table), page_table.shape[1],
-        _ptr(prefix_len), int(max_prefix), _ptr(k_tree), _ptr(v_tree), _ptr(mask), _ptr(qo_indptr),
-        qo_indptr.numel() - 1, T, int(max_nodes), hq, hkv, d, float(sm_scale), _ptr(out), _ptr(lse),
-        _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), _ptr(dev_status), _stream(stream))
+    _, hkv, e = k_tree.shape
+    if e != d:
+        raise ValueError(f"k_tree: heads of {d} elements expected, got {e}")
+    pages, ps = _kv8p_pool(k_pool, v_pool, kv_scale, hkv, d)
+    most, B, n = page_table.shape[1], qo_indptr.numel() - 1, T * hkv * d
+    q, kp, vp, sc, pt, pl, kt, vt, mk, qo, out, lse, status = _ptrs((
+        (q, _BF, 0, "q"), (k_pool, _U8, 0, "k_pool (E4M3 codes)"), (v_pool, _U8, 0, "v_pool (E4M3 codes)"),
+        (kv_scale, _F32, 0, "kv_scale"), (page_table, _I32, B * most, "page_table"), (prefix_len, _I32, B, "prefix_len"),
+        (k_tree, _BF, n, "k_tree"), (v_tree, _BF, n, "v_tree"), (mask, _I64, T * ((int(max_nodes) + 63) // 64), "mask"),
+        (qo_indptr, _I32, 0, "qo_indptr"), (out, _BF, T * hq * d, "out"), (lse, _F32, T * hq, "lse"),
+        (dev_status, _I32, 1, "dev_status")))
+    st = (_lib or load()).spec_tree_verify_attn_kv8p(
+        q, kp, vp, sc, pages, ps, pt, most, pl, int(max_prefix), kt, vt, mk, qo, B, T, int(max_nodes), hq, hkv, d,
+        float(sm_scale), out, lse, _ptr(ws), 0 if ws is None else ws.nbytes, status, _stream(stream))
     return _check(st, "spec_tree_verify_attn_kv8p")
-
-
-def _need_kv8p(k_pool, v_pool, kv_scale):
-    _need(k_pool, torch.uint8, "k_pool (E4M3 codes)")
-    _need(v_pool, torch.uint8, "v_pool (E4M3 codes)")
-    _need(kv_scale, torch.float32, "kv_scale")
-    if v_pool.shape != k_pool.shape or tuple(kv_scale.shape) != (k_pool.shape[0], k_pool.shape[1], 2):
-        raise ValueError("kv_scale: [num_pages][hkv][2], and pools of one shape, expected")
 
 
 def spec_kv_commit_kv8p(k_tree, v_tree, path, accept_len, qo_indptr, page_table, prefix_len, k_pool, v_pool,
                         kv_scale, seq_len_out=None, dev_status=None, stream=None):
     """Commit of bf16 tree K/V rows into an FP8 cache with page scales (codes and scales
     are updated in place)."""
-    _need(k_tree, torch.bfloat16, "k_tree")
-    _need(v_tree, torch.bfloat16, "v_tree")
-    _need_kv8p(k_pool, v_pool, kv_scale)
     T, hkv, d = k_tree.shape
-    num_pages, _, ps, _ = k_pool.shape
-    st = load().spec_kv_commit_kv8p(
-        _ptr(k_tree), _ptr(v_tree), _ptr(path), path.shape[1], _ptr(accept_len), _ptr(qo_indptr), _ptr(page_table),
-        page_table.shape[1], num_pages, ps, _ptr(prefix_len), _ptr(seq_len_out), _ptr(k_pool), _ptr(v_pool),
-        _ptr(kv_scale), qo_indptr.numel() - 1, T, hkv, d, _ptr(dev_status), _stream(stream))
+    pages, ps = _kv8p_pool(k_pool, v_pool, kv_scale, hkv, d)
+    most, cap, B = page_table.shape[1], path.shape[1], qo_indptr.numel() - 1
+    kt, vt, path, acc, qo, pt, pl, seq, kp, vp, sc, status = _ptrs((
+        (k_tree, _BF, 0, "k_tree"), (v_tree, _BF, T * hkv * d, "v_tree"), (path, _I32, B * cap, "path"),
+        (accept_len, _I32, B, "accept_len"), (qo_indptr, _I32, 0, "qo_indptr"),
+        (page_table, _I32, B * most, "page_table"), (prefix_len, _I32, B, "prefix_len"),
+        (seq_len_out, _I32, B, "seq_len_out"), (k_pool, _U8, 0, "k_pool (E4M3 codes)"),
+        (v_pool, _U8, 0, "v_pool (E4M3 codes)"), (kv_scale, _F32, 0, "kv_scale"), (dev_status, _I32, 1, "dev_status")))
+    st = (_lib or load()).spec_kv_commit_kv8p(
+        kt, vt, path, cap, acc, qo, pt, most, pages, ps, pl, seq, kp, vp, sc, B, T, hkv, d, status, _stream(stream))
     return _check(st, "spec_kv_commit_kv8p")
 
 
-def _rows(t, what):
-    """(pointer, elements between rows) of [T][heads][d] rows whose heads are contiguous."""
+def _rows(t, dtype, T, d, what):
+    """(pointer, elements between rows, heads) of [T][heads][d] rows whose heads are contiguous."""
+    n, h, e = t.shape
+    if t.dtype is not dtype:
+        raise ValueError(f"{what}: {dtype} expected, got {t.dtype}")
+    if n < T or e != d:
+        raise ValueError(f"{what}: {T} rows of heads of {d} elements expected, got {tuple(t.shape)}")
     if not t.is_cuda:
         raise ValueError("device tensor expected")
-    T, h, d = t.shape
     rows, heads, one = t.stride()
     if (d > 1 and one != 1) or (h > 1 and heads != d):
         raise ValueError(f"{what}: contiguous heads expected")
-    return t.data_ptr(), rows if T > 1 else h * d
+    return t.data_ptr(), rows if T > 1 else h * d, h
 
 
 def spec_qk_norm_rope(q, k, v, cos_sin, prefix_len, qo_indptr, q_out, k_out, v_out, depth=None, q_weight=None,
@@ -436,23 +476,23 @@ def spec_qk_norm_rope(q, k, v, cos_sin, prefix_len, qo_indptr, q_out, k_out, v_o
     """Norm per head and rotation of projected rows: q [T,Hq,D], k and v [T,Hkv,D] (views of
     a fused projection: any row stride), cos_sin float32 [max_pos, rot_dim] or None (no
     rotation); q_out, k_out, v_out contiguous. v and v_out may both be None."""
-    dt = _dtype(q)
-    for t, what in ((k, "k"), (q_out, "q_out"), (k_out, "k_out"), (v, "v"), (v_out, "v_out"),
-                    (q_weight, "q_weight"), (k_weight, "k_weight")):
-        if t is not None:
-            _need(t, q.dtype, what)
+    dt, el, B = _dtype(q), q.dtype, qo_indptr.numel() - 1
     T, hq, d = q.shape
-    hkv = k.shape[1]
-    if cos_sin is not None:
-        _need(cos_sin, torch.float32, "cos_sin")
-    qp, qs = _rows(q, "q")
-    kp, ks = _rows(k, "k")
-    vp, vs = (None, 0) if v is None else _rows(v, "v")
+    qp, qs, _ = _rows(q, el, T, d, "q")
+    kp, ks, hkv = _rows(k, el, T, d, "k")
+    vp, vs, hv = (None, 0, hkv) if v is None else _rows(v, el, T, d, "v")
+    if hv != hkv:
+        raise ValueError(f"v: {hkv} heads expected, got {hv}")
     max_pos, rot = (0, 0) if cos_sin is None else cos_sin.shape
-    st = load().spec_qk_norm_rope(
-        dt, qp, qs, kp, ks, vp, vs, _ptr(q_weight), _ptr(k_weight), float(eps), _ptr(cos_sin), max_pos, rot,
-        1 if interleaved else 0, _ptr(prefix_len), _ptr(depth), _ptr(qo_indptr), qo_indptr.numel() - 1, T, hq, hkv, d,
-        _ptr(q_out), _ptr(k_out), _ptr(v_out), _ptr(dev_status), _stream(stream))
+    n = T * hkv * d
+    qw, kw, tab, pl, dep, qo, q_to, k_to, v_to, status = _ptrs((
+        (q_weight, el, d, "q_weight"), (k_weight, el, d, "k_weight"), (cos_sin, _F32, 0, "cos_sin"),
+        (prefix_len, _I32, B, "prefix_len"), (depth, _I32, T, "depth"), (qo_indptr, _I32, 0, "qo_indptr"),
+        (q_out, el, T * hq * d, "q_out"), (k_out, el, n, "k_out"), (v_out, el, n, "v_out"),
+        (dev_status, _I32, 1, "dev_status")))
+    st = (_lib or load()).spec_qk_norm_rope(
+        dt, qp, qs, kp, ks, vp, vs, qw, kw, float(eps), tab, max_pos, rot, 1 if interleaved else 0, pl, dep, qo, B, T, hq, hkv,
+        d, q_to, k_to, v_to, status, _stream(stream))
     return _check(st, "spec_qk_norm_rope")
 
 
@@ -461,15 +501,13 @@ def spec_page_table_resize(seq_len, qo_indptr, held, page_table, free_pages, n_f
     """Grow (with shrink also cut) the page-table rows to the lengths of a step, from a
     stack of free pages; slot_map int64 [total_nodes]. held_out / n_free_out may be held /
     n_free themselves."""
-    for t, what in ((seq_len, "seq_len"), (held, "held"), (page_table, "page_table"), (free_pages, "free_pages"),
-                    (n_free, "n_free"), (held_out, "held_out"), (n_free_out, "n_free_out"),
-                    (qo_indptr, "qo_indptr")):
-        _need(t, torch.int32, what)
-    if slot_map is not None:
-        _need(slot_map, torch.int64, "slot_map")
-    st = load().spec_page_table_resize(
-        _ptr(seq_len), _ptr(qo_indptr), _ptr(held), _ptr(page_table), page_table.shape[1], _ptr(free_pages),
-        free_pages.numel(), _ptr(n_free), int(page_size), 1 if shrink else 0, qo_indptr.numel() - 1,
-        0 if slot_map is None else slot_map.numel(), _ptr(held_out), _ptr(n_free_out), _ptr(slot_map),
-        _ptr(dev_status), _stream(stream))
+    B, most = qo_indptr.numel() - 1, page_table.shape[1]
+    seq, qo, h, pt, free, nf, ho, no, slots, status = _ptrs((
+        (seq_len, _I32, B, "seq_len"), (qo_indptr, _I32, 0, "qo_indptr"), (held, _I32, B, "held"),
+        (page_table, _I32, B * most, "page_table"), (free_pages, _I32, 0, "free_pages"), (n_free, _I32, 1, "n_free"),
+        (held_out, _I32, B, "held_out"), (n_free_out, _I32, 1, "n_free_out"), (slot_map, _I64, 0, "slot_map"),
+        (dev_status, _I32, 1, "dev_status")))
+    st = (_lib or load()).spec_page_table_resize(
+        seq, qo, h, pt, most, free, free_pages.numel(), nf, int(page_size), 1 if shrink else 0, B,
+        0 if slot_map is None else slot_map.numel(), ho, no, slots, status, _stream(stream))
     return _check(st, "spec_page_table_resize")
