@@ -549,6 +549,12 @@ int spec_kv_commit_kv8(const void* k_tree, const void* v_tree, const float* kv_s
  *   NaN or NaN codes. A row that does see a NaN or an infinity in k or v may be NaN in
  *   every element. A row that sees no key at all is 0 with lse = -infinity.
  *   Rows at or past qo_indptr[batch] are left as they were.
+ *   Arithmetic: scores, softmax statistics, sums and lse in fp32. Fewer bits: q enters the
+ *   prefix's scores as the sum of two E4M3 terms (exact for elements within 2^9 of their
+ *   row's largest, else off by at most 2^-17 of that); a weight meets V in fp16 (prefix:
+ *   2^-11 of it) or as two bf16 terms (tree: 2^-16), while the row sum adds it unrounded;
+ *   out is rounded to bf16 once. An output element is off by about 2^-11 sum p |v| and that
+ *   last rounding.
  *   ws          workspace of spec_workspace_size(SPEC_OP_ATTN_KV8P, ...) bytes (256-byte
  *               aligned; any contents).
  *   Device errors: SPEC_ERR_PAGE (the page is read as zeros), SPEC_ERR_CAPACITY (a tree
@@ -573,8 +579,11 @@ int spec_tree_verify_attn_kv8p(const void* q, const uint8_t* k_pool, const uint8
  *   s = s0, whatever it held; a page with older rows s = max(s0, its scale). Written rows
  *   become the E4M3 codes nearest to x / s (ties to the even code, beyond +-448, and
  *   infinities, saturated to +-448, NaN kept); where s has grown, the older rows' codes
- *   become those nearest to value * old scale / s. Rows past the written ones keep their
- *   codes (they hold nothing). So a scale never shrinks while its page holds a token.
+ *   become those nearest to value * old scale / s. (Products and quotients in fp32: exact
+ *   for the powers of two that this call writes; a scale that came with a page may be any
+ *   number, and then they are rounded to fp32 before the code is taken.) Rows past the
+ *   written ones keep their codes (they hold nothing). So a scale never shrinks while its
+ *   page holds a token.
  *   A page that receives rows must belong to one sequence of the call.
  *
  *   kv_scale    float [num_pages][hkv][2] (in/out)

@@ -9,8 +9,8 @@
 // K's codes go to the tensor cores as they are (kind::f8f6f4), so QK needs no widened copy of
 // K. Its other operand has to be E4M3 too: a row of q, scaled by a power of two to a largest
 // element in [2^7, 2^8), is the sum of two E4M3 values, hi = e4m3(q) and lo = e4m3(q - hi): a
-// bf16 has 8 significant bits, an E4M3 4, so the sum is exact for elements within 2^10 of the
-// row's largest (and off by at most 2^-18 of it below). Two products of twice bf16's rate cost
+// bf16 has 8 significant bits, an E4M3 4, so the sum is exact for elements within 2^9 of the
+// row's largest (and off by at most 2^-17 of it below). Two products of twice bf16's rate cost
 // what one bf16 product does.
 // P V runs in fp16: E4M3 is a subset of fp16, and P needs the range (a key that takes nearly
 // all of a row's weight leaves the others' weights 2^20 and more below it, where two E4M3
