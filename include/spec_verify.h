@@ -66,9 +66,13 @@
  *     serialization, so a call may begin while the kernel enqueued before it
  *     is still running. By default every kernel waits for that predecessor
  *     before it reads or writes anything (a predecessor's writes are visible
- *     only after that wait, whether or not it signals early). A caller whose
- *     preceding kernel writes none of the inputs listed below can let two
- *     kernels read them before the wait with spec_set_early_reads(1):
+ *     only after that wait, whether or not it signals early); the commit that
+ *     spec_accept_commit launches reads what its acceptance does not write
+ *     while that runs, as the acceptance has waited. A caller whose
+ *     preceding kernel writes none of the inputs listed below (nor, where that
+ *     is an attention, which signals before its own wait, the kernel before
+ *     it) can let two kernels read them before the wait with
+ *     spec_set_early_reads(1):
  *     spec_tree_verify_attn (and its _kv8, _kv8p and _parents forms) then reads q,
  *     k_pool, v_pool, k_tree, v_tree, page_table, prefix_len, qo_indptr and
  *     kv_scale (everything but the mask or parent array) before it waits, and
@@ -84,7 +88,8 @@
  *     depth (spec_build_tree_mask), out, lse and the workspace (the attention
  *     and its split merge) and the acceptance results (greedy spec_accept when
  *     it streams every row); the commit kernels and the acceptance walks,
- *     which may write the pool, never do.
+ *     which may write the pool, the page-table resize and the norm + rotation
+ *     never do (the resize signals to its own second kernel alone).
  */
 #ifndef SPEC_VERIFY_H
 #define SPEC_VERIFY_H

@@ -33,9 +33,9 @@
 // Splits write O / l in fp32 and the log2-sum-exp, joined by a second kernel.
 //
 // Bound (one GB300): not HBM and not the tensor cores but a slot's chain (S, softmax, P, each handed
-// on through a barrier) and the issue of its instructions: about 2300 cycles for a block of 64 keys,
-// of which the softmax takes the most; two slots go at a time. 128 sequences of one token over
-// 543,000 keys (1.1 GB): 274 us, 4.1 TB/s; 32 trees of 64 nodes over 512 .. 8192 keys: 156 us,
+// on through a barrier) and the issue of its instructions: about 1700 cycles for a block of 64 keys on
+// the long case below, of which the softmax takes the most; two slots go at a time. 128 sequences of one token over
+// 543,000 keys (1.1 GB): 275 us, 4.1 TB/s; 32 trees of 64 nodes over 512 .. 8192 keys: 156 us,
 // 0.96 of 1.93 PFLOP/s; 8 x 128 nodes over 32768 keys: 923 us, 1.06 PFLOP/s.
 // What was measured beside it (when it took 293, 164 and 984 us): one tile a CTA, its blocks of 128
 // keys handed to the slots in turn, q in TMEM 300, 246, 1010; two tiles in 128-key blocks with one S

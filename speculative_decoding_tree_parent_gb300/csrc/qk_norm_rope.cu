@@ -13,11 +13,10 @@
 // Layout: a thread holds two chunks of eight elements of a head, so chosen that a pair never
 // leaves its thread and neighbouring lanes touch neighbouring 16 bytes (halves of the head for
 // adjacent pairs, halves of the rotated part for split ones), and the norm needs log2(d / 16)
-// shuffles. A CTA has up to 10 warps' worth of heads and a run of nodes, as many CTAs as stand on
-// the GPU at once. The rows come through shared memory by asynchronous copies, 8 / sizeof(T) nodes
+// shuffles. A CTA has up to 10 warps' worth of heads and a run of nodes; the grid is 768 threads an SM. The rows come through shared memory by asynchronous copies, 8 / sizeof(T) nodes
 // ahead, each thread reading back what it copied: 40 KB in flight a CTA, which registers cannot
 // hold (one node a CTA, in registers: 118 us on 10,000 nodes of 64 + 16 heads of 128 in bf16; a
-// run of nodes, the next in registers: 99; so: 75, 5.5 TB/s read and written). A node's weights
+// run of nodes, the next in registers: 99; so: 76, 5.5 TB/s read and written). A node's weights
 // and its sequence stay with the thread from node to node.
 #include "common.cuh"
 #include "tc_host.cuh"
@@ -26,7 +25,10 @@
 namespace specv {
 
 constexpr int kRopeMaxWarps = 10;
-constexpr int kRopeThreads = 768;  // threads an SM holds at the registers that the kernel takes
+// Threads an SM that the grid is made for. (At the kernel's 96 registers an SM holds 640: two blocks of
+// 320 threads, as for 64 + 16 heads of 128, all stand at once; of smaller blocks the last ones wait for
+// a place, 32 + 16 heads of 128 in bf16: 72 us for 10,000 tokens, 1.9 times their bytes' time.)
+constexpr int kRopeThreads = 768;
 
 struct RopeArgs {
   const void* q_in;
@@ -286,7 +288,7 @@ static cudaError_t launch_rope(const RopeArgs& p, bool interleaved, int total_no
   const int warps = ceil_div(heads, 32 / LPH);
   const int y = ceil_div(warps, kRopeMaxWarps);
   const dim3 block(ceil_div(warps, y) * 32);
-  // as many CTAs as stand on the GPU at once, each with its share of the nodes
+  // kRopeThreads an SM, each CTA with its share of the nodes
   const int resident = ceil_div(sm_count() * (kRopeThreads / (int)block.x), y);
   const dim3 grid(total_nodes < resident ? total_nodes : resident, y);
   return interleaved ? launch_pdl(qk_norm_rope_kernel<T, LPH, true>, grid, block, 0, stream, p)
