@@ -9,10 +9,12 @@
 //
 // Bound: latency on an accepted path (sizes and path -> rows -> maximum -> stores), HBM on a
 // prompt chunk (bf16 rows read once, codes written once).
-// Layout: a CTA per (sequence, touched page, share of the KV heads), half its threads for K, half for V;
+// Layout: a CTA per (sequence, touched page or several, share of the KV heads), half its threads for K, half for V;
 // a thread keeps its 16-element pieces of the page in registers from the maximum to the
 // store. No two CTAs write the same page and head, so nothing is exchanged between them; each
 // makes the sequence's checks itself and comes to the same verdict.
+#include <algorithm>
+
 #include "common.cuh"
 #include "tc_host.cuh"
 
@@ -88,9 +90,11 @@ __device__ __forceinline__ float scale_for(uint32_t bits) {
   return exp2f((float)max(-kPageScaleExp, min(kPageScaleExp, e)));
 }
 
-// kPer: 16-element pieces of a page and head that a thread holds
-template <int kPer>
-__global__ void __launch_bounds__(2 * kQcHalf) kv_commit_kv8p_kernel(const CommitP8Args p) {
+// kPer: 16-element pieces of a page and head that a thread holds; kMany: the grid has fewer places
+// than the path may have pages. (32 chunks of about 500 rows: 23.7 us without the loop, 25.8 with it;
+// an accepted path takes as long either way.)
+template <int kPer, bool kMany>
+__global__ void __launch_bounds__(2 * kQcHalf, !kMany ? 0 : kPer == 1 ? 5 : kPer == 2 ? 3 : 2) kv_commit_kv8p_kernel(const CommitP8Args p) {
   // (batch and pages share the grid's x extent: y would end at 65535 pages)
   const int b = blockIdx.x % (unsigned)p.batch, nth = blockIdx.x / (unsigned)p.batch;
   const int half = threadIdx.x / kQcHalf, tid = threadIdx.x % kQcHalf;  // 0: K, 1: V
@@ -106,101 +110,107 @@ __global__ void __launch_bounds__(2 * kQcHalf) kv_commit_kv8p_kernel(const Commi
     if (lead && threadIdx.x == 0) report(p.status, SPEC_ERR_INDEX);
     return;
   }
-  if ((long)(P / ps + (long)nth) * ps > (long)P + L) return;  // the path ends before this page
-  const int lp = P / ps + nth;
-  // the page's rows [r0, r1) take the path's nodes from r0 - shift on; rows below r0 are older
-  const int shift = P - lp * ps;  // > 0 on the first page where it starts inside
-  const int r0 = max(shift, 0), r1 = min(ps, shift + L + 1);
   const int pieces = p.d >> 4;
-  // where this thread's new pieces come from (head 0), -1: an older row, none, or a bad node, which
-  // is not followed
-  long from[kPer];
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int e = tid + i * kQcHalf, r = e / pieces;
-    from[i] = -1;
-    if (r < r0 || r >= r1) continue;
-    const int node = ld(path + r - shift);
-    if (node >= 0 && node < n) from[i] = (long)(base + node) * p.hkv * p.d + 16 * (e - r * pieces);
-  }
-  auto load = [&](int g, uint4 (&x)[kPer][2]) {
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      x[i][0] = x[i][1] = make_uint4(0, 0, 0, 0);
-      if (from[i] < 0) continue;
-      const uint4* src = reinterpret_cast<const uint4*>(p.tree[half] + from[i] + (long)g * p.d);
-      x[i][0] = ld(src);
-      x[i][1] = ld(src + 1);
-    }
-  };
-  // the first head's rows are on their way while the sequence is checked
-  uint4 x[kPer][2];
-  load(blockIdx.y, x);
-  int bad = 0;
-  for (int i = threadIdx.x; i <= L; i += 2 * kQcHalf) {
-    const int node = ld(path + i);
-    const int q = (P + i) / ps;
-    if (node < 0 || node >= n || (i == 0 && node != 0)) bad = SPEC_ERR_INDEX;
-    else if (q >= p.max_pages) bad = SPEC_ERR_CAPACITY;
-    else {
-      const int page = ld(table + q);
-      if (page < 0 || page >= p.num_pages) bad = SPEC_ERR_PAGE;
-    }
-    if (bad) break;
-  }
-  if (bad && lead) report(p.status, bad);
-  if (__syncthreads_or(bad)) return;
-  const size_t page = (size_t)ld(table + lp);
+  bool checked = false;
   int turn = 0;
-  for (int g = blockIdx.y; g < p.hkv; g += gridDim.y, turn ^= 1) {
-    const size_t unit = page * p.hkv + g;
-    float* sp = p.kv_scale + unit * 2 + half;
-    const float old = r0 > 0 ? *sp : 0.f;  // (read by every thread before the barrier, written after it)
-    uint32_t top = 0;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) top = max(top, top16(x[i][0], x[i][1]));
-    top = __reduce_max_sync(0xffffffffu, top);
-    if ((tid & 31) == 0) s_top[turn][half][tid >> 5] = top;
-    // the next head's rows, while this one's are joined, turned into codes and stored
-    uint4 y[kPer][2];
-    if (g + gridDim.y < p.hkv) load(g + gridDim.y, y);
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kQcHalf / 32; ++w) top = max(top, s_top[turn][half][w]);
-    uint8_t* codes = p.pool[half] + unit * ps * p.d;
-    float now = scale_for(top);
-    float was = now;
-    if (r0 > 0) {
-      was = page_scale(old);
-      now = fmaxf(now, was);
-    }
-    const float inv = exact_inverse(now);
+  for (long at = P / ps + (long)nth; at * ps <= (long)P + L; at += gridDim.x / (unsigned)p.batch) {
+    const int lp = (int)at;
+    // the page's rows [r0, r1) take the path's nodes from r0 - shift on; rows below r0 are older
+    const int shift = P - lp * ps;  // > 0 on the first page where it starts inside
+    const int r0 = max(shift, 0), r1 = min(ps, shift + L + 1);
+    // where this thread's new pieces come from (head 0), -1: an older row, none, or a bad node, which
+    // is not followed
+    long from[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int e = tid + i * kQcHalf, r = e / pieces;
-      if (r >= r1) continue;
-      uint4* dst = reinterpret_cast<uint4*>(codes) + e;  // rows are contiguous: piece e of the page
-      if (r >= r0) {
-        *dst = inv != 0.f ? make_uint4(code4(x[i][0].x, x[i][0].y, inv), code4(x[i][0].z, x[i][0].w, inv),
-                                       code4(x[i][1].x, x[i][1].y, inv), code4(x[i][1].z, x[i][1].w, inv))
-                          : make_uint4(code4_div(x[i][0].x, x[i][0].y, now), code4_div(x[i][0].z, x[i][0].w, now),
-                                       code4_div(x[i][1].x, x[i][1].y, now), code4_div(x[i][1].z, x[i][1].w, now));
-      } else if (now != was) {
-        const uint4 c = *dst;
-        const uint32_t in[4] = {c.x, c.y, c.z, c.w};
-        uint32_t out[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float4 v = e4m3x4_to_f32(in[k]);
-          out[k] = inv != 0.f ? code4(v.x * was * inv, v.y * was * inv, v.z * was * inv, v.w * was * inv)
-                              : code4_div(v.x * was, v.y * was, v.z * was, v.w * was, now);
-        }
-        *dst = make_uint4(out[0], out[1], out[2], out[3]);
-      }
+      from[i] = -1;
+      if (r < r0 || r >= r1) continue;
+      const int node = ld(path + r - shift);
+      if (node >= 0 && node < n) from[i] = (long)(base + node) * p.hkv * p.d + 16 * (e - r * pieces);
     }
-    if (tid == 0) *sp = now;
+    auto load = [&](int g, uint4 (&x)[kPer][2]) {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) x[i][0] = y[i][0], x[i][1] = y[i][1];
+      for (int i = 0; i < kPer; ++i) {
+        x[i][0] = x[i][1] = make_uint4(0, 0, 0, 0);
+        if (from[i] < 0) continue;
+        const uint4* src = reinterpret_cast<const uint4*>(p.tree[half] + from[i] + (long)g * p.d);
+        x[i][0] = ld(src);
+        x[i][1] = ld(src + 1);
+      }
+    };
+    // the first head's rows are on their way while the sequence is checked
+    uint4 x[kPer][2];
+    load(blockIdx.y, x);
+    if (!checked) {
+      int bad = 0;
+      for (int i = threadIdx.x; i <= L; i += 2 * kQcHalf) {
+        const int node = ld(path + i);
+        const int q = (P + i) / ps;
+        if (node < 0 || node >= n || (i == 0 && node != 0)) bad = SPEC_ERR_INDEX;
+        else if (q >= p.max_pages) bad = SPEC_ERR_CAPACITY;
+        else {
+          const int page = ld(table + q);
+          if (page < 0 || page >= p.num_pages) bad = SPEC_ERR_PAGE;
+        }
+        if (bad) break;
+      }
+      if (bad && lead) report(p.status, bad);
+      if (__syncthreads_or(bad)) return;
+      checked = true;
+    }
+    const size_t page = (size_t)ld(table + lp);
+    for (int g = blockIdx.y; g < p.hkv; g += gridDim.y, turn ^= 1) {
+      const size_t unit = page * p.hkv + g;
+      float* sp = p.kv_scale + unit * 2 + half;
+      const float old = r0 > 0 ? *sp : 0.f;  // (read by every thread before the barrier, written after it)
+      uint32_t top = 0;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) top = max(top, top16(x[i][0], x[i][1]));
+      top = __reduce_max_sync(0xffffffffu, top);
+      if ((tid & 31) == 0) s_top[turn][half][tid >> 5] = top;
+      // the next head's rows, while this one's are joined, turned into codes and stored
+      uint4 y[kPer][2];
+      if (g + gridDim.y < p.hkv) load(g + gridDim.y, y);
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < kQcHalf / 32; ++w) top = max(top, s_top[turn][half][w]);
+      uint8_t* codes = p.pool[half] + unit * ps * p.d;
+      float now = scale_for(top);
+      float was = now;
+      if (r0 > 0) {
+        was = page_scale(old);
+        now = fmaxf(now, was);
+      }
+      const float inv = exact_inverse(now);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int e = tid + i * kQcHalf, r = e / pieces;
+        if (r >= r1) continue;
+        uint4* dst = reinterpret_cast<uint4*>(codes) + e;  // rows are contiguous: piece e of the page
+        if (r >= r0) {
+          *dst = inv != 0.f ? make_uint4(code4(x[i][0].x, x[i][0].y, inv), code4(x[i][0].z, x[i][0].w, inv),
+                                         code4(x[i][1].x, x[i][1].y, inv), code4(x[i][1].z, x[i][1].w, inv))
+                            : make_uint4(code4_div(x[i][0].x, x[i][0].y, now), code4_div(x[i][0].z, x[i][0].w, now),
+                                         code4_div(x[i][1].x, x[i][1].y, now), code4_div(x[i][1].z, x[i][1].w, now));
+        } else if (now != was) {
+          const uint4 c = *dst;
+          const uint32_t in[4] = {c.x, c.y, c.z, c.w};
+          uint32_t out[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float4 v = e4m3x4_to_f32(in[k]);
+            out[k] = inv != 0.f ? code4(v.x * was * inv, v.y * was * inv, v.z * was * inv, v.w * was * inv)
+                                : code4_div(v.x * was, v.y * was, v.z * was, v.w * was, now);
+          }
+          *dst = make_uint4(out[0], out[1], out[2], out[3]);
+        }
+      }
+      if (tid == 0) *sp = now;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) x[i][0] = y[i][0], x[i][1] = y[i][1];
+    }
+    if (!kMany) break;
   }
   if (lead && threadIdx.x == 0 && p.seq_len_out != nullptr) p.seq_len_out[b] = P + L + 1;
 }
@@ -220,18 +230,28 @@ int launch_kv_commit_kv8p(const void* k_tree, const void* v_tree, const int32_t*
                        seq_len_out, {k_pool, v_pool}, kv_scale, batch, total_nodes, hkv, d, status};
   // most rows a path has (its nodes are the sequence's rows), and most pages that they touch
   const long most = path_cap < total_nodes ? path_cap : total_nodes > 1 ? total_nodes : 1;
-  const long pages = (most + page_size - 2) / page_size + 1;
-  if (batch * pages > 0x7FFFFFFFL) return SPEC_ERR_UNSUPPORTED;
+  const long all = (most + page_size - 2) / page_size + 1;
   // a CTA per head while they stand on the GPU at once (its longest chain is then the shortest),
   // else as many heads a CTA as make it so: the checks and the chain before the rows are then made
   // once for several heads, and a head's rows are loaded under the one before it (32 sequences of
   // about 500 rows, 8 heads: a CTA per head 39 us; at most 8, 16, 32 CTAs an SM: 26.8, 24.8, 28.8)
+  // A path may be much shorter than path_cap allows, and a CTA without a page costs about a
+  // microsecond of its place: the grid holds the longest tree's pages, or as many as leave every head
+  // a CTA at 16 CTAs an SM, and a CTA takes further pages in turn (with room for 131,072 rows: 32
+  // chunks of 500 rows 36 us, 54 with a CTA for every page; 4 paths of 4 rows 9 and 15)
+  const long tree = (kMaxTreeNodes + page_size - 2) / page_size + 1, room = 16L * sm_count() / batch / hkv;
+  const long pages = std::min(all, std::max(tree, room));
+  if (batch * pages > 0x7FFFFFFFL) return SPEC_ERR_UNSUPPORTED;
   const long share = 16L * sm_count() / (batch * pages);
   const dim3 grid((unsigned)(batch * pages), (unsigned)(share < 1 ? 1 : share < hkv ? share : hkv)), block(2 * kQcHalf);
   const int per = ceil_div(page_size * (d / 16), kQcHalf);
-  const cudaError_t e = per <= 1   ? launch_pdl(kv_commit_kv8p_kernel<1>, grid, block, 0, stream, p)
-                        : per <= 2 ? launch_pdl(kv_commit_kv8p_kernel<2>, grid, block, 0, stream, p)
-                                   : launch_pdl(kv_commit_kv8p_kernel<4>, grid, block, 0, stream, p);
+  const auto kernel = pages < all ? (per <= 1   ? kv_commit_kv8p_kernel<1, true>
+                                     : per <= 2 ? kv_commit_kv8p_kernel<2, true>
+                                                : kv_commit_kv8p_kernel<4, true>)
+                                  : (per <= 1   ? kv_commit_kv8p_kernel<1, false>
+                                     : per <= 2 ? kv_commit_kv8p_kernel<2, false>
+                                                : kv_commit_kv8p_kernel<4, false>);
+  const cudaError_t e = launch_pdl(kernel, grid, block, 0, stream, p);
   if (e != cudaSuccess) return SPEC_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }

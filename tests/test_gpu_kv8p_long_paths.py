@@ -15,7 +15,7 @@ if not torch.cuda.is_available():
 
 @pytest.mark.parametrize("rows,prefix,cap,ps", [
     (1025, 0, 1025, 16), (1041, 0, 1043, 16), (1041, 7, 4096, 16), (2000, 16, 2048, 16), (2048, 5, 2048, 16),
-    (8192, 3, 8192, 16), (2048, 33, 2050, 1), (3000, 63, 3000, 64)])
+    (8192, 3, 8192, 16), (2048, 33, 2050, 1), (3000, 63, 3000, 64), (40, 9, 20000, 16)])
 def test_every_row_of_a_long_path(rows, prefix, cap, ps):
     c = setup([prefix, 40, prefix + 1], [rows - 1, 2, 17], 2, 64, ps, cap=cap, seed=rows)
     t = put(c)
