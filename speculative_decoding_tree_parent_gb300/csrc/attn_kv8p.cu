@@ -312,8 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // (the grid and the workspace hold max_nodes nodes a sequence, not the mask row's multiple of 64)
   if (N > p.max_nodes || P < 0 || P > p.max_len) {
     if (threadIdx.x == 0 && split == 0) {
-      pdl_wait();
-      report(p.status, SPEC_ERR_CAPACITY);
+      report_waited(p.status, SPEC_ERR_CAPACITY);
     }
     return;
   }
@@ -386,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     auto checked = [&](int page, int k) -> int {
       if (page >= 0 && page < p.num_pages) return page;
-      if (!isv && sp.pg_lo + 32 * k + lane < sp.pg_hi) report(p.status, SPEC_ERR_PAGE);
+      if (!isv && sp.pg_lo + 32 * k + lane < sp.pg_hi) report_waited(p.status, SPEC_ERR_PAGE);
       return p.num_pages;  // out of range: TMA reads zeros
     };
     auto scale_of = [&](int page) {
@@ -436,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       done = j + 1;
     }
     if (done < nb && lane == 0) {  // given up: leave no copy in flight
-      report(p.status, SPEC_ERR_TIMEOUT);
+      report_waited(p.status, SPEC_ERR_TIMEOUT);
       int zero = 0;
       for (int j = max(0, done - kSt); j < done; ++j)
         tc::mbar_wait(bar(&full[j % kSt]), (j / kSt) & 1, &zero, kWaitLimit);
@@ -497,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::mma_commit(bar(&bars.pv_done[t][n & 1]));
         tc::mma_commit(bar(&bars.v_empty[sv]));
       }
-      if (!ok) report(p.status, SPEC_ERR_TIMEOUT);
+      if (!ok) report_waited(p.status, SPEC_ERR_TIMEOUT);
       // every product issued has completed before TMEM is released
       tc::mma_commit(bar(&bars.fin[t]));
       int zero = 0;
@@ -577,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       warp_arrive(bar(&bars.v_full[sv]));
       warp_arrive(bar(&bars.c_empty[sc_]));
     }
-    if (!ok && lane == 0) report(p.status, SPEC_ERR_TIMEOUT);
+    if (!ok && lane == 0) report_waited(p.status, SPEC_ERR_TIMEOUT);
   } else {
     // ------------------------------------------------------------------ softmax
     const uint32_t quarter = (uint32_t)((warp & 3) * 32) << 16, ts = tmem + 256 * slot + quarter, to = ts + 128;
@@ -748,7 +747,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     if (n > 0) ok = ok && wait_all(bar(&bars.pv_done[slot][(n - 1) & 1]), ((n - 1) >> 1) & 1, abort);
-    if (!ok && lane == 0) report(p.status, SPEC_ERR_TIMEOUT);
+    if (!ok && lane == 0) report_waited(p.status, SPEC_ERR_TIMEOUT);
 
     // -------------------------------------------------------------------- epilogue
     // Of one tile, the slots' sums are joined: both hold the same rows, and each thread takes 64

@@ -258,8 +258,7 @@ __global__ void __launch_bounds__(TcCfg<kFp8, kPar>::kThreads, 1)
   // (a tree has to fit its mask rows, and the row tiles that the grid and the workspace hold)
   if (N > p.mask_words * 64 || N > p.mtiles * npt || P < 0 || P > p.max_pages * 16) {
     if (threadIdx.x == 0 && split == 0) {
-      pdl_wait();  // (the status word is written in stream order)
-      report(p.status, SPEC_ERR_CAPACITY);
+      report_waited(p.status, SPEC_ERR_CAPACITY);
     }
     return;
   }
@@ -298,7 +297,7 @@ __global__ void __launch_bounds__(TcCfg<kFp8, kPar>::kThreads, 1)
       if (blk < npb && lp < sr.pg_hi) {
         const int pg = ld(p.page_table + (size_t)b * p.max_pages + lp);
         if (pg >= 0 && pg < p.num_pages) page = pg;
-        else report(p.status, SPEC_ERR_PAGE);
+        else report_waited(p.status, SPEC_ERR_PAGE);
       }
       return page;
     };
@@ -397,7 +396,7 @@ __global__ void __launch_bounds__(TcCfg<kFp8, kPar>::kThreads, 1)
         const uint32_t bar_free = kFp8 ? bar_f8e(j % kF8Stages) : bar_kve(j % kStages);
         const int parity = kFp8 ? ((j / kF8Stages) & 1) ^ 1 : ((j / kStages) & 1) ^ 1;
         if (!warp_wait(bar_free, parity, abort)) {
-          if (lane == 0) report(p.status, SPEC_ERR_TIMEOUT);
+          if (lane == 0) report_waited(p.status, SPEC_ERR_TIMEOUT);
           break;
         }
         load_block(j);
@@ -465,7 +464,7 @@ __global__ void __launch_bounds__(TcCfg<kFp8, kPar>::kThreads, 1)
           tc::mma_commit(bar_pv(t));
           tc::mma_commit(bar_kve(j % kStages));
         }
-        if (!ok) report(p.status, SPEC_ERR_TIMEOUT);
+        if (!ok) report_waited(p.status, SPEC_ERR_TIMEOUT);
         // every MMA this thread issued has completed before TMEM is released
         const uint32_t bar_fin = tc::smem_u32(&bars.mma_fin[t]);
         tc::mma_commit(bar_fin);
@@ -489,7 +488,7 @@ __global__ void __launch_bounds__(TcCfg<kFp8, kPar>::kThreads, 1)
       for (int j = 0; j < nb; ++j) {
         const int st = j % kStages;
         if (j >= kStages && !warp_wait(bar_kve(st), ((j / kStages) & 1) ^ 1, abort)) {
-          if (lane == 0) report(p.status, SPEC_ERR_TIMEOUT);
+          if (lane == 0) report_waited(p.status, SPEC_ERR_TIMEOUT);
           break;
         }
         if (j >= npb) {
@@ -510,7 +509,7 @@ __global__ void __launch_bounds__(TcCfg<kFp8, kPar>::kThreads, 1)
         }
         const int s8 = j % kF8Stages;
         if (!warp_wait(bar_f8f(s8), (j / kF8Stages) & 1, abort)) {
-          if (lane == 0) report(p.status, SPEC_ERR_TIMEOUT);
+          if (lane == 0) report_waited(p.status, SPEC_ERR_TIMEOUT);
           break;
         }
         const uint8_t* src = smem + Cfg::kOffF8 + s8 * kF8Stage;
@@ -590,7 +589,7 @@ __global__ void __launch_bounds__(TcCfg<kFp8, kPar>::kThreads, 1)
           if (cur < lo + kTcKeys) bits |= 1ull << (cur - lo);
           const int pp = spar[cur];
           if (cur == 0 ? pp != -1 : (pp < 0 || pp >= cur)) {
-            report(p.status, SPEC_ERR_PARENT);
+            report_waited(p.status, SPEC_ERR_PARENT);
             return 0ull;
           }
           if (cur == 0) break;
@@ -694,7 +693,7 @@ __global__ void __launch_bounds__(TcCfg<kFp8, kPar>::kThreads, 1)
         tc::mbar_arrive(bar_pf(tile));
       }
       ok = ok && warp_wait(bar_pv(tile), (nb - 1) & 1, abort);
-      if (!ok && (threadIdx.x & 127) == 0) report(p.status, SPEC_ERR_TIMEOUT);
+      if (!ok && (threadIdx.x & 127) == 0) report_waited(p.status, SPEC_ERR_TIMEOUT);
       tc::fence_after_sync();
       // O row out of TMEM: final output when unsplit, else this split's partial (O / l in
       // bf16, 8 values per 16-byte chunk, chunk-major) and its log2-sum-exp m + log2(l)

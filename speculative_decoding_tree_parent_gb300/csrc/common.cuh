@@ -66,6 +66,11 @@ __device__ __forceinline__ float4 e4m3x4_to_f32(uint32_t w) {
 // pdl_wait(), whether or not it signals early.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+// report() for kernels that may run ahead of the wait: the status word is written in stream order.
+__device__ __forceinline__ void report_waited(int32_t* status, int code) {
+  pdl_wait();
+  report(status, code);
+}
 // A plain load, for what the kernel before may have written: __ldg promises the compiler that a
 // value never changes, and it may move such a load ahead of pdl_wait() (a captured step then
 // committed the path of the step before it).

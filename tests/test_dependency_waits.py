@@ -122,3 +122,11 @@ def test_loads_in_the_functions_they_call_are_plain():
     users = [f for f in os.listdir(CSRC) if re.search(r"\bseq_of_row\(", source(f)) and f != "common.cuh"]
     assert "__ldg" not in re.sub(r"int seq_of_row\(.*?\n}", "", source("common.cuh"), flags=re.S)
     assert all("pdl_wait()" not in source(f) for f in users)
+
+
+@pytest.mark.parametrize("name", ["attn_tc_kernel", "attn_kv8p_kernel"])
+def test_errors_are_reported_after_the_wait(name):
+    """With early reads the attention runs ahead of its wait, and the status word is something that
+    it writes."""
+    body = KERNELS[name][1]
+    assert not re.search(r"\breport\(", body) and "report_waited(p.status, SPEC_ERR_PAGE)" in body
