@@ -788,11 +788,18 @@ __global__ void __launch_bounds__(kMergeThreads) attn_tc_merge_kernel(const TcMe
   // the attention grid has finished: its partials are visible. (It signals before its own wait, so
   // qo_indptr is read ahead only where the caller lets the attention do so.)
   if (!p.early_reads) pdl_wait();
-  const int base = ld(p.qo + b);
-  const int N = ld(p.qo + b + 1) - base;
-  if (idx == 0) pdl_wait();  // (whatever the sizes: the grid must not end before the attention)
-  if (node_l >= N || N > p.mtiles * (kTcRows / G)) return;  // (a tree past the row tiles was refused)
-  pdl_wait();
+  int base = 0, N = 0;
+  auto past = [&]() {  // a row that the attention has not written
+    base = ld(p.qo + b);
+    N = ld(p.qo + b + 1) - base;
+    return node_l >= N || N > p.mtiles * (kTcRows / G);  // (a tree past the row tiles was refused)
+  };
+  if (p.early_reads) {
+    const bool skip = past();
+    if (idx == 0) pdl_wait();  // (whatever the sizes: the grid must not end before the attention)
+    if (skip) return;
+    pdl_wait();
+  }
   // every load (split statistics and partial rows) is issued before any is used: one
   // round trip to L2
   const int S = p.splits;  // <= MAXS
@@ -805,6 +812,7 @@ __global__ void __launch_bounds__(kMergeThreads) attn_tc_merge_kernel(const TcMe
     lv[s] = s < S ? __ldcg(ls + (size_t)s * kTcRows) : -INFINITY;
     q[s] = s < S ? __ldcg(po + (size_t)s * (kTcRows * kTcD / 8)) : make_uint4(0, 0, 0, 0);
   }
+  if (!p.early_reads && past()) return;  // (the sizes come with the partials: one round trip)
   float M = -INFINITY;
 #pragma unroll
   for (int s = 0; s < MAXS; ++s) M = fmaxf(M, lv[s]);
