@@ -522,6 +522,7 @@ __global__ void __launch_bounds__(Shape<kW, kDual>::kThreads, 1) attn_kv4_kernel
         const uint32_t pb = sb + S::kOffP + t * 2 * kPBuf;
         int i = 0;       // the CTA's block
         int n_qk = 0, n_pv = 0;  // the slot's blocks
+        int n_q = 0;             // its tiles: those of which it has a block
 #pragma unroll 1
         for (int s = 0; ok; ++s) {
           ok = wait_one(bar(bars.seg_full[s % kSegs]), (s / kSegs) & 1);
@@ -530,11 +531,14 @@ __global__ void __launch_bounds__(Shape<kW, kDual>::kThreads, 1) attn_kv4_kernel
           const int keys = bars.seg[s % kSegs].P - bars.seg[s % kSegs].j0 * kKeys;  // prefix keys from the first block on
           tc::mbar_arrive(bar(bars.seg_empty[s % kSegs]));
           if (nb == 0) break;
-          ok = wait_one(bar(bars.q_full[t]), s & 1);
-          if (!ok) break;
-          tc::fence_after_sync();
           constexpr int kStep = kDual ? 1 : 2;
           const int k0 = kDual ? 0 : (i ^ t) & 1;
+          if (k0 < nb) {
+            ok = wait_one(bar(bars.q_full[t]), n_q & 1);
+            if (!ok) break;
+            tc::fence_after_sync();
+            ++n_q;
+          }
           auto qk = [&](int k) {
             const int at = i + k, kb = at & 1;
             ok = ok && wait_one(bar(bars.kt_full[kb]), (at >> 1) & 1);
@@ -831,9 +835,11 @@ __global__ void __launch_bounds__(Shape<kW, kDual>::kThreads, 1) attn_kv4_kernel
         warp_arrive(bar(bars.q_full[slot]));
         named_sync(6 + slot, 128 * kG);
       } else {
+        // (only to a slot that has a block of the tile: an issuer without one waits for nothing else here, and a phase
+        // that it has not seen when the next is over would never be seen)
         __syncwarp();
-        tc::mbar_arrive_if(lane == 0, bar(bars.q_full[0]));
-        tc::mbar_arrive_if(lane == 0, bar(bars.q_full[1]));
+        tc::mbar_arrive_if(lane == 0 && nb > (i & 1), bar(bars.q_full[0]));
+        tc::mbar_arrive_if(lane == 0 && nb > ((i & 1) ^ 1), bar(bars.q_full[1]));
         named_sync(1, kSoft);
       }
       // ---- blocks
