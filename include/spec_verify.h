@@ -667,7 +667,8 @@ int spec_kv_commit_kv8p(const void* k_tree, const void* v_tree, const int32_t* p
  *   Rows at or past qo_indptr[batch] are left as they were. Device errors: SPEC_ERR_INDEX (a
  *   negative first or count, rows outside total_rows: that sequence's rows are left as they were),
  *   SPEC_ERR_CAPACITY (a slot past max_pages), SPEC_ERR_PAGE (a page id outside the pool): in both
- *   cases those rows are zeros.
+ *   cases those rows are zeros. Each sequence is judged by its own numbers, whether or not qo_indptr rises; of
+ *   rows that two ranges share it is not said whose they hold.
  */
 int spec_tree_verify_attn_kv4(const void* q, const uint8_t* kv_pool, const float* kv_scale, int num_pages,
                               int page_size, const int32_t* page_table, int max_pages,
