@@ -646,7 +646,8 @@ int spec_kv_commit_kv8p(const void* k_tree, const void* v_tree, const int32_t* p
  *   2^30 (row tiles of 16 to 128 rows, blocks of 128 keys or 32 nodes).
  *   Device errors: SPEC_ERR_PAGE (the page is read as zeros), SPEC_ERR_CAPACITY (a tree
  *   past max_nodes, a prefix past max_prefix: that sequence's rows are left as they were),
- *   SPEC_ERR_INDEX (a node range outside [0, total_nodes): likewise), SPEC_ERR_TIMEOUT.
+ *   SPEC_ERR_INDEX (a node range that falls or is not within [0, total_nodes]: likewise, whatever the
+ *   others' ranges), SPEC_ERR_TIMEOUT.
  *
  * spec_kv_commit_kv4 — spec_kv_commit from bf16 tree rows into a 4-bit pool.
  *   Every 16 elements x of a row: with a the largest finite |x| and f the head's kv_scale,

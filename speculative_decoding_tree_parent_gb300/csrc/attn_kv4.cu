@@ -329,10 +329,12 @@ __global__ void __launch_bounds__(Shape<kW, kDual>::kThreads, 1) attn_kv4_kernel
   // ---- the CTA's share of all blocks: sizes summed over the batch, then the sequence where the share starts
   auto units_of = [&](int b) -> int {
     if (b >= p.batch) return 0;
-    const int base = ld(p.qo + b), N = ld(p.qo + b + 1) - base, P = ld(p.prefix_len + b);
-    if (N <= 0) return 0;
-    if (N > p.max_nodes || P < 0 || P > p.max_len || base < 0 || N > p.total - base) {
-      if (blockIdx.x == 0) report(p.status, base < 0 || N > p.total - base ? SPEC_ERR_INDEX : SPEC_ERR_CAPACITY);
+    const int base = ld(p.qo + b), end = ld(p.qo + b + 1), P = ld(p.prefix_len + b);
+    const bool outside = base < 0 || end < base || end > p.total;
+    const int N = end - base;
+    if (!outside && N == 0) return 0;
+    if (outside || N > p.max_nodes || P < 0 || P > p.max_len) {
+      if (blockIdx.x == 0) report(p.status, outside ? SPEC_ERR_INDEX : SPEC_ERR_CAPACITY);
       return 0;
     }
     return (N + p.npt - 1) / p.npt * p.hkv * (blocks_of(P, N) + kTileCost);
