@@ -643,7 +643,7 @@ int spec_kv_commit_kv8p(const void* k_tree, const void* v_tree, const int32_t* p
  *   row's largest; weights of the prefix are rounded to fp16 beside a row's largest of 2^5 at least, those of the
  *   tree to two bf16 terms; scores, sums and outputs in fp32, the result rounded once to bf16.
  *   SPEC_ERR_UNSUPPORTED where batch * hkv * (row tiles of max_nodes) * (blocks of max_prefix and max_nodes) passes
- *   2^30 (row tiles of 16 to 128 rows, blocks of 128 keys or 32 nodes).
+ *   2^30 (row tiles of 16 to 128 rows, blocks of 128 keys or 32 nodes), or max_prefix 2^31 - 1025.
  *   Device errors: SPEC_ERR_PAGE (the page is read as zeros), SPEC_ERR_CAPACITY (a tree
  *   past max_nodes, a prefix past max_prefix: that sequence's rows are left as they were),
  *   SPEC_ERR_INDEX (a node range that falls or is not within [0, total_nodes]: likewise, whatever the

@@ -99,8 +99,12 @@ static bool attn_kv8p_shape(long batch, int hq, int hkv, int d) {
   return d == 128 && hq / hkv <= 128 && grid_fits(batch * hkv);
 }
 
-// The record of a 4-bit cache fixes page and head; a row tile holds a group's rows.
-static bool attn_kv4_shape(int hq, int hkv, int d) { return d == 128 && hq / hkv <= 128 && grid_fits(hkv); }
+// The record of a 4-bit cache fixes page and head; a row tile holds a group's rows; a prefix rounded up to whole blocks, and
+// the block after it, are counted in an int.
+constexpr int kMostPrefix4 = 0x7FFFFFFF - 1024;
+static bool attn_kv4_shape(int hq, int hkv, int d, int max_prefix) {
+  return d == 128 && hq / hkv <= 128 && grid_fits(hkv) && max_prefix <= kMostPrefix4;
+}
 
 static std::atomic<int> g_early_reads{0};
 bool early_reads() { return g_early_reads.load(std::memory_order_relaxed) != 0; }
@@ -144,7 +148,7 @@ size_t spec_workspace_size(int op, int batch, int total_nodes, int max_nodes, in
       return attn_kv8p_ws_bytes(batch, max_nodes, hq, hkv, max_prefix);
     case SPEC_OP_ATTN_KV4:
       if (hq <= 0 || hkv <= 0 || hq % hkv || max_nodes <= 0 || max_nodes > kMaxNodes || max_prefix < 0) return 0;
-      if (!attn_kv4_shape(hq, hkv, d)) return 0;
+      if (!attn_kv4_shape(hq, hkv, d, max_prefix)) return 0;
       return attn_kv4_ws_bytes(batch, max_nodes, hq, hkv, max_prefix);
     case SPEC_OP_ACCEPT:
       if (vocab <= 0) return 0;
@@ -543,7 +547,7 @@ int spec_tree_verify_attn_kv4(const void* q, const uint8_t* kv_pool, const float
       num_pages < 0 || max_pages < 0)
     return SPEC_ERR_ARG;
   if (hq <= 0 || hkv <= 0 || hq % hkv != 0) return SPEC_ERR_ARG;
-  if (page_size != 16 || !attn_kv4_shape(hq, hkv, d)) return SPEC_ERR_UNSUPPORTED;
+  if (page_size != 16 || !attn_kv4_shape(hq, hkv, d, max_prefix)) return SPEC_ERR_UNSUPPORTED;
   if (batch == 0 || total_nodes == 0) return SPEC_OK;
   if (!q || !k_tree || !v_tree || !mask || !qo_indptr || !prefix_len || !out) return SPEC_ERR_ARG;
   if (max_prefix > 0 && (!kv_pool || !page_table || max_pages <= 0 || num_pages <= 0)) return SPEC_ERR_ARG;
