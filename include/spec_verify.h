@@ -708,7 +708,8 @@ int spec_kv_read_kv4(const uint8_t* kv_pool, const float* kv_scale, int num_page
  *   tokens     int32 [batch][path_cap]; NULL where neither logprob nor rank is asked for.
  *   logprob, entropy  float [batch][path_cap];  rank  int32 [batch][path_cap];
  *   top_ids    int32 [batch][path_cap][topk];  top_logprobs  float likewise. Any may be NULL.
- *   topk       in [0, 32]; vocab <= 2^24; temperature positive (it and its inverse finite).
+ *   topk       in [0, 32]; vocab <= 2^24; temperature positive, at most 3e38, with a finite
+ *              log2(e) / temperature in fp32 (4.25e-39 and up), else SPEC_ERR_ARG.
  *   A token of probability 0 (logit -infinity) is no alternative: places that are left get id -1
  *   and -infinity. A row with a NaN or +infinity, or with nothing above -infinity, has NaN for
  *   logprob and entropy; its ids and rank mean nothing.

@@ -601,7 +601,8 @@ int spec_token_logprobs(int dtype, const void* logits, long long row_stride, int
   if (dtype != SPEC_F32 && dtype != SPEC_BF16) return SPEC_ERR_UNSUPPORTED;
   if (batch < 0 || total_rows < 0 || path_cap < 1 || vocab < 1 || row_stride < vocab || topk < 0) return SPEC_ERR_ARG;
   if (topk > 32 || vocab > (1 << 24) || row_stride > (1LL << 40)) return SPEC_ERR_UNSUPPORTED;
-  if (!(temperature > 0.f) || !(1.0f / temperature <= 3.0e38f) || !(temperature <= 3.0e38f)) return SPEC_ERR_ARG;
+  // (the exponentials' factor, log2(e) / temperature, is an fp32 number)
+  if (!(temperature > 0.f) || !(1.0f / temperature * 1.4426950408889634f <= 3.4028235e38f) || !(temperature <= 3.0e38f)) return SPEC_ERR_ARG;
   if (batch == 0) return SPEC_OK;
   if (!logits || (!path) != (!accept_len) || (path && !qo_indptr)) return SPEC_ERR_ARG;
   if (!tokens && (logprob || rank)) return SPEC_ERR_ARG;
