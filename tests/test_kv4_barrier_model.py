@@ -333,6 +333,7 @@ def test_protocol(rows, heavy):
     (16, dict(mistake="an idle slot's tiles count")), (64, dict(mistake="an idle slot's tiles count")),
     (64, dict(mistake="no wait before O is rescaled")), (128, dict(mistake="no wait before O is rescaled")),
     (16, dict(mistake="no wait for V")), (128, dict(mistake="no wait for V")),
+    (16, dict(mistake="V's wait alone")), (64, dict(mistake="V's wait alone")),     # (its phase before may not be over)
     (16, dict(stages=5))])      # an odd number of stages with two groups of converters: a stage belongs to neither
 def test_planted_mistakes_are_found(rows, kw):
     found = 0
