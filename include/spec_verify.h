@@ -641,7 +641,8 @@ int spec_kv_commit_kv8p(const void* k_tree, const void* v_tree, const int32_t* p
  *               aligned; any contents).
  *   Arithmetic: K and V are widened exactly; q, scaled per row, is exact in fp16 for elements within 2^31 of the
  *   row's largest; weights of the prefix are rounded to fp16 beside a row's largest of 2^5 at least, those of the
- *   tree to two bf16 terms; scores, sums and outputs in fp32, the result rounded once to bf16.
+ *   tree to two bf16 terms; scores, sums and outputs in fp32, the result rounded once to bf16. (Products are summed
+ *   before they are divided by the row sum: tree values up to 2^100 times the head's V scale stay in fp32's range.)
  *   SPEC_ERR_UNSUPPORTED where batch * hkv * (row tiles of max_nodes) * (blocks of max_prefix and max_nodes) passes
  *   2^30 (row tiles of 16 to 128 rows, blocks of 128 keys or 32 nodes), or max_prefix 2^31 - 1025.
  *   Device errors: SPEC_ERR_PAGE (the page is read as zeros), SPEC_ERR_CAPACITY (a tree
@@ -710,6 +711,8 @@ int spec_kv_read_kv4(const uint8_t* kv_pool, const float* kv_scale, int num_page
  *   top_ids    int32 [batch][path_cap][topk];  top_logprobs  float likewise. Any may be NULL.
  *   topk       in [0, 32]; vocab <= 2^24; temperature positive, at most 3e38, with a finite
  *              log2(e) / temperature in fp32 (4.25e-39 and up), else SPEC_ERR_ARG.
+ *   The difference of a logit and its row's largest is taken in fp32 before it is divided: past fp32's
+ *   largest number it counts as infinite, whatever the temperature.
  *   A token of probability 0 (logit -infinity) is no alternative: places that are left get id -1
  *   and -infinity. A row with a NaN or +infinity, or with nothing above -infinity, has NaN for
  *   logprob and entropy; its ids and rank mean nothing.

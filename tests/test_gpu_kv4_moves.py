@@ -193,3 +193,17 @@ def test_a_captured_call_over_a_pool_with_nan_behind_the_prefixes():
         full.prefix, full.qo, full.mask, full.sizes, full.pool = c.prefix, c.qo, mask, sizes, pool
         check(full, d)
         assert int(d.status.item()) == 0
+
+
+@pytest.mark.parametrize("nodes", [4, 20, 200])
+def test_large_values_in_the_tree(nodes):
+    """Values of 2^98 beside a head's V scale of 1, 2^90 beside one of 2^-4: products summed over 1024 nodes would stay finite."""
+    c = C.case([40, 0], [nodes, 3], 8, 2, seed=61)
+    c.kv_scale[1] = [1.0, 2.0 ** -4]
+    c.vt[:, 0] *= np.float32(2.0 ** 96)
+    c.vt[:, 1] *= np.float32(2.0 ** 90)
+    assert np.abs(c.vt[:, 0]).max() < 2.0 ** 99 and np.abs(c.vt[:, 1]).max() < 2.0 ** 95
+    d = C.device(c)
+    attend(c, d)
+    assert int(d.status.item()) == 0
+    check(c, d)
