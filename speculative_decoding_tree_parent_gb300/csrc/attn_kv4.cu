@@ -28,13 +28,16 @@
 // has two groups of four converter warps and a slot one of softmax warps (decode of 128 sequences 244 -> 212 us); of 64
 // rows a slot it is one and two (32 trees of 64 nodes 338 -> 321). Every wait is bounded.
 //
-// What bounds it: of 128 rows the softmax warps (a scheduler issues in 71% of its cycles, the tensor pipe is active in 37%;
-// without the conversions 11% less time, without the exponentials 4%, without all of the softmax 24%), of 16 rows the
-// conversions (24%) and the issue of the copies. Unrolling the conversions' loops cost more than it gave (their code
-// has to be fetched), a third issuer warp for O's products changed nothing. GB300: one token over 517, 32 query heads
-// over 8, 12.5 us; 64 nodes over 4096 27.5; 128 tokens over 256 to 8190, 64 heads over 8, 183 (3.4 TB/s of records; 197 with
-// one producer warp); 32 trees of 64 nodes over 512 to 8192, 32 heads over 8, 218; 8 of 101 to 128 nodes over 32768, 64
-// heads over 8, 1080 (0.91 PFLOP/s).
+// What bounds it: of 128 rows the issue of instructions (4 sequences of 128 nodes over 16384: a scheduler issues in 73% of its
+// cycles, the tensor pipe is active in 39%; about 8000 warp instructions a block, of which the softmax is 3100, the
+// conversions 1700, waits and loops the rest; without the conversions 11% less time, without the exponentials 4%, without all
+// of the softmax 24%), of 16 rows the conversions (24%) and the issue of the copies. Every shape spills a few registers (8 to 40
+// bytes of stack): of 128 and 64 rows 41 and 35 loads of a warp a block (0.5%) bring some back, of 32 rows 5, of 16 one; they
+// are stored a tile at a time. Unrolling the conversions' loops cost more than it gave (their code has to be fetched), a
+// third issuer warp for O's products changed nothing. GB300: one token over 517, 32 query heads
+// over 8, 12 us; 64 nodes over 4096 27; 128 tokens over 256 to 8190, 64 heads over 8, 182 (3.4 TB/s of records; 197 with
+// one producer warp); 32 trees of 64 nodes over 512 to 8192, 32 heads over 8, 217; 8 of 101 to 128 nodes over 32768, 64
+// heads over 8, 1075 (0.91 PFLOP/s).
 #include "attn_common.cuh"
 #include "kv4.cuh"
 #include "tc_host.cuh"
@@ -57,8 +60,10 @@ constexpr uint32_t kPBuf = kKeys * 128;                // P of a block: 128-byte
 constexpr uint32_t kColS = 0, kColO = 128, kColK = 256, kColV = 384;
 constexpr int kSegs = 4;
 // What a tile of R rows costs beside its blocks (q, the result, the pipeline's start, a tree block's more), in blocks: the
-// shares count it. 32 ragged trees of 64 nodes (128 rows) take 262 us with 4, 231 with 6, 218 with 8, 221 with 12; 128 ragged
-// sequences of one node (16 rows) 201 with 3, 197 with 4, 199 with 5, 205 with 8; between them 32 and 64 rows.
+// shares count it. Ragged batches, us of a call among others: 32 trees of 64 nodes (128 rows) 235 with 4, 212 with 6, 198 with 8,
+// 197 with 10, 200 with 12; 64 of 16 nodes (64 rows) 177, 163, 162, 164, 166; 64 of 8 nodes (32 rows) 121, 111, 107, 108,
+// 110; 128 of one node (16 rows) 202 with 3, 196 with 4, 187 with 6, 190 with 8, 193 with 10. (The costs of 16 and 32 rows were
+// the best with one producer warp; with two, 6 and 8 would be 5% and 3% better.)
 __host__ __device__ constexpr int tile_cost(int R) { return R == 16 ? 4 : R == 32 ? 6 : 8; }
 constexpr float kShift = 5.f;   // log2 of a row's largest P where off is set
 constexpr float kLimit = 15.f;  // log2 of the largest P

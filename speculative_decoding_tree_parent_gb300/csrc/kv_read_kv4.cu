@@ -2,7 +2,7 @@
 // The first product is exact in fp16; the second is rounded to fp32, then once to bf16.
 //
 // Bound: HBM, 512 bytes written for 144 read (a token of a head, K and V). GB300: 4 tokens 6.1 us, 32 sequences of 512
-// tokens, 8 heads, 25 us; of 8191 tokens 250 us (5.5 TB/s).
+// tokens, 8 heads, 23 us; of 8191 tokens 235 us (5.8 TB/s).
 // Layout: a CTA per (sequence, page, share of the KV heads). Half of its 256 threads take K, a group of
 // one token each, and store its 32 bytes as they come; half take V, one element of the
 // page's 16 tokens each, turned through shared memory into rows. Eight CTAs an SM (32 registers; what spills is the judges'): 32

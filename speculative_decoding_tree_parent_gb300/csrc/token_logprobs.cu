@@ -11,14 +11,16 @@
 // maxima is a bound that at least k elements reach; the few segments that reach it are read a second time (from
 // the L2), and the elements that do are sorted by counting.
 //
-// Bound: HBM for many rows (a row is read once), with the issue of instructions close behind it; latency for a few.
+// Bound: HBM for many rows (a row is read once; of bf16 neither is full: HBM at 68%, the issue of instructions at 66%);
+// latency for a few.
 // Layout: a cluster of 1 to 8 CTAs a row, so that a few rows still use many SMs; each writes its part into the first CTA's
 // shared memory. CTAs of 256 threads, four an SM for bf16 and five for fp32, so that one CTA's end (the alternatives)
 // runs beside the others' reading: 4093 bf16 rows of 128256 took 382 us at two CTAs of 512 threads, 220 at four
 // of 256 with the arithmetic in pairs, 235 at five (registers spill); 160 fp32 rows 39 us at four and 31 at five. A second
 // turn's loads ahead of the first's use changed nothing.
 // GB300: 5 rows of 128256 in fp32, 5 alternatives, 9.8 us; 160 rows, 20 alternatives, 30 us (2.8 TB/s); 4093 rows in bf16,
-// 1 alternative, 229 us (4.6 TB/s; 218 without Z's remainder), as many in fp32 with 5 alternatives 352 us (6.0 TB/s). What runs once a CTA is kept short:
+// 1 alternative, 229 us (4.6 TB/s; 218 without Z's remainder), as many in fp32 with 5 alternatives 338 to 356 us (6.2 to 5.9 TB/s,
+// as a call among others or alone), 160 bf16 rows along paths, 20 alternatives, 27. What runs once a CTA is kept short:
 // on few rows its code has to be fetched (a sort of the maxima within and across warps took 1 us more of 160 rows).
 #include <cooperative_groups.h>
 
